@@ -434,6 +434,150 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_c
                                        int max_blocks_per_seq, int num_blocks, int max_query_len,
                                        pkv_dtype dtype, int32_t* dev_err, pkv_stream_t stream);
 
+/* ----------------------------------------------------------------------
+ * Caches of a bounded size
+ *
+ * [VM] gives a sequence a block whenever it grows past its last one; nothing
+ * in the pages bounds a long sequence's cache. Two ways of holding it to a
+ * fixed size are served here; both are this library's choice:
+ *   by position  attention sees a sequence's first tokens ("sinks") and a
+ *                sliding window of its newest ones; blocks that lie wholly
+ *                outside both may be given back, and their block-table entries
+ *                are not read;
+ *   by use       every decode step adds each cached token's attention weight
+ *                to a score, and from time to time the cache is cut to a
+ *                budget: the first tokens, the newest ones and the highest-
+ *                scored of the rest stay, and the gaps are closed.
+ * ---------------------------------------------------------------------- */
+
+/* pkv_paged_attention_decode over the first tokens and a window ([VM], [ABS]):
+ * of sequence s with L = context_lens[s] tokens, its newest included, the query
+ * sees the tokens t < L with t < num_sinks or t >= L - window, that is
+ * min(L, num_sinks + window) of them (all when L is not larger):
+ *     out[s][h][:] = sum over the visible t of softmax(x)_t * v_t,
+ * x_t as in pkv_paged_attention_decode. L == 0 gives an all-zero row. K and V
+ * rows of tokens that are not visible are never read, nor are block-table
+ * entries of blocks without a visible token.
+ *
+ *   window     >= 1; num_sinks >= 0 (may sum to more than a context)
+ *   dtype      PKV_F32, PKV_F16 or PKV_BF16, of q, out and the caches
+ *   workspace  at least pkv_decode_window_workspace_bytes() bytes; its first
+ *              num_seqs * num_heads int32 must be zero before the first call and
+ *              every call leaves them zero. Two calls that share a workspace
+ *              must not overlap on the GPU.
+ * All other arguments, layouts and errors as in pkv_paged_attention_decode,
+ * but no wait can run out; PKV_ERR_INVALID_ARG for window < 1 or
+ * num_sinks < 0, PKV_ERR_UNSUPPORTED when max_blocks_per_seq * block_size
+ * exceeds 2^31 - 256. */
+pkv_status pkv_paged_attention_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                             int window, int num_sinks, int num_heads, int num_kv_heads,
+                                             int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
+                                             int num_blocks, int max_context_len, pkv_dtype dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream);
+
+/* Bytes of workspace pkv_paged_attention_decode_window needs. Pure host
+ * function; 0 for non-positive sizes or num_heads not a multiple of
+ * num_kv_heads. */
+size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim);
+
+/* pkv_paged_attention_prefill over the first tokens and a window ([WL], [VM]):
+ * the query at position P of its sequence sees the tokens t <= P with
+ * t < num_sinks or t > P - window, so the last query of a call sees what
+ * pkv_paged_attention_decode_window would show it. Arguments and errors as in
+ * pkv_paged_attention_prefill, plus PKV_ERR_INVALID_ARG for window < 1 or
+ * num_sinks < 0. Block-table entries of blocks that no query of the call sees
+ * need not be valid. V rows of tokens that some query of the call sees must
+ * be finite (an infinity or a NaN there may also reach queries that do not
+ * see the token); rows that no query sees may hold anything. */
+pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, const int32_t* context_lens,
+                                              const int32_t* query_start, float scale, int window, int num_sinks,
+                                              int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                              int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                              int max_query_len, pkv_dtype dtype, int32_t* dev_err,
+                                              pkv_stream_t stream);
+
+/* pkv_paged_attention_decode that also adds up the attention each cached token
+ * receives: besides out, for every sequence s, kv head g and token t < L,
+ *     scores_out[s][g][t] = old + sum over the query heads h of g of softmax(x_h)_t,
+ *     old = scores[s][g][t] for t < L - 1 when scores is not NULL, else 0
+ * (the newest token has no past: whatever its place held is replaced). The sum
+ * runs over the heads in order, in fp32; results do not depend on the work
+ * split. Entries at and behind L are neither read nor written, and a sequence
+ * with L == 0 (an idle row of a fixed batch) has none.
+ *
+ *   scores      float [num_seqs][num_kv_heads][score_stride], or NULL
+ *   scores_out  the same shape; the same address as scores (in place) or no
+ *               byte in common with it
+ *   score_stride  >= max_context_len
+ *   workspace   at least pkv_decode_scores_workspace_bytes() bytes; zeroing and
+ *               sharing as for pkv_paged_attention_decode_window
+ *   dtype       PKV_F32, PKV_F16 or PKV_BF16
+ * Two kernels. Other arguments and errors as in
+ * pkv_paged_attention_decode_window; PKV_ERR_INVALID_ARG also for a
+ * score_stride that is too small and for overlapping score arrays. */
+pkv_status pkv_paged_attention_decode_scores(void* out, float* scores_out, const float* scores, int64_t score_stride,
+                                             const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                             int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                             int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                             int max_context_len, pkv_dtype dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream);
+
+/* Bytes of workspace pkv_paged_attention_decode_scores needs (it holds the
+ * logits of num_seqs * num_heads rows of max_context_len, rounded up to 8).
+ * Pure host function; 0 as for pkv_decode_window_workspace_bytes. */
+size_t pkv_decode_scores_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                         int max_context_len);
+
+/* Cut every sequence's cache to at most `budget` tokens ([VM]). Sequence s of
+ * L = context_lens[s] tokens keeps, for each kv head by itself, all of them
+ * when L <= budget, and otherwise its first num_sinks, its last num_recent
+ * and, of the tokens between, the budget - num_sinks - num_recent with the
+ * largest scores (equal scores: the lower position; -0 equals +0; NaN counts
+ * below every number). With n = min(L, budget) and kept[s][g][0 .. n) the kept
+ * positions in ascending order, for i < n:
+ *     K and V row of position i, head g  = the row of position kept[s][g][i]
+ *     scores_out[s][g][i]                = scores[s][g][kept[s][g][i]]
+ * where rows are read through block_tables and written through
+ * dst_block_tables, and new_context_lens[s] = n. Bytes are moved as they are:
+ * bit-exact. Nothing at and behind position n is written.
+ *
+ *   scores        float [num_seqs][num_kv_heads][score_stride], score_stride >=
+ *                 max_context_len; read
+ *   scores_out    float [num_seqs][num_kv_heads][out_stride], out_stride >=
+ *                 min(budget, max_context_len); the same address and stride as
+ *                 scores (in place) or no byte in common with it
+ *   dst_block_tables  int32 [num_seqs][max_blocks_per_seq]: the blocks that hold
+ *                 the result (the first ceil(n / block_size) entries of a row).
+ *                 Each entry is the entry of block_tables at the same place, a
+ *                 block that this sequence alone uses, or a block that is in no
+ *                 row of block_tables (a fresh one; a block that other
+ *                 sequences hold must be replaced by one); a block is the
+ *                 destination of one entry only. The two tables may be the same
+ *                 array. pkv_bm_shrink_batch hands out such tables.
+ *   new_context_lens  int32 [num_seqs]; may be context_lens
+ *   kept          int32 [num_seqs][num_kv_heads][budget], written up to n
+ *   dtype         any pkv_dtype: the pools' element type
+ *
+ * Two kernels, no workspace. Errors: host - INVALID_ARG (NULL or misaligned
+ * pointers, budget < 1, num_sinks or num_recent < 0 or together more than
+ * budget, strides, overlapping score arrays, max_context_len >
+ * max_blocks_per_seq * block_size), UNSUPPORTED (head_dim, block_size, dtype,
+ * num_seqs or num_kv_heads > 65535, a table longer than 2^31 - 256 tokens).
+ * Device - a context length outside [0, max_context_len] is clamped and sets
+ * PKV_DEV_ERR_CONTEXT_LEN; a row whose source or destination block is outside
+ * [0, num_blocks) is not moved and sets PKV_DEV_ERR_BLOCK_ID. num_seqs == 0
+ * enqueues nothing. */
+pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores, int64_t score_stride,
+                            float* scores_out, int64_t out_stride, const int32_t* block_tables,
+                            const int32_t* dst_block_tables, const int32_t* context_lens,
+                            int32_t* new_context_lens, int32_t* kept, int budget, int num_sinks, int num_recent,
+                            int num_kv_heads, int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
+                            int num_blocks, int max_context_len, pkv_dtype dtype, int32_t* dev_err,
+                            pkv_stream_t stream);
+
 /* Bytes of workspace pkv_paged_attention_decode needs for these sizes: the
  * segment counters (num_seqs * num_heads int32) plus a fixed area for the
  * partial results of the split segments (independent of the context lengths;

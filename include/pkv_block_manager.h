@@ -160,6 +160,22 @@ pkv_status pkv_bm_beam_step_many(pkv_block_manager* bm, const int32_t* beams, co
                                  int32_t requests, int32_t width, int32_t n_new, int32_t* new_beams, int64_t* slots,
                                  int64_t* cow_pairs, int32_t* num_cow, int32_t* shared_blocks);
 
+/* Cut `n` distinct live sequences to their first new_lens[i] tokens' worth of
+ * table ([VM]; the host side of pkv_evict_tokens, which moves the kept rows
+ * there). A sequence whose length is new_lens[i] already is left as it is.
+ * Otherwise it holds ceil(new_lens[i] / block_size) blocks afterwards: entry j
+ * stays where no other live sequence holds that block at the time of the call,
+ * and is a fresh block where one does; blocks behind go back to the free
+ * stack. No fresh block is one that any sequence held before the call, so
+ * with the tables exported before and after it (pkv_bm_export) as block_tables
+ * and dst_block_tables the rows may move in any order across sequences. Blocks
+ * that came free may be handed out by the next call: enqueue the move first,
+ * or on the same stream as what will write them. All or nothing:
+ * PKV_ERR_OUT_OF_BLOCKS (nothing changed) when the free stack holds too few
+ * fresh blocks; PKV_ERR_INVALID_ARG when n < 0, an id repeats or is not live,
+ * or a new length is < 0 or longer than its sequence. n = 0 is a no-op. */
+pkv_status pkv_bm_shrink_batch(pkv_block_manager* bm, const int32_t* seqs, const int32_t* new_lens, int32_t n);
+
 /* Length (tokens) and table length (blocks) of live sequence `seq`. */
 pkv_status pkv_bm_seq_info(const pkv_block_manager* bm, int32_t seq, int64_t* length, int32_t* num_blocks);
 

@@ -43,6 +43,8 @@ lib.pkv_bm_beam_step.argtypes = [_P, _P, _P, _I32, _I32, _P, _P, _P, ctypes.POIN
 lib.pkv_bm_beam_step.restype = ctypes.c_int
 lib.pkv_bm_beam_step_many.argtypes = [_P, _P, _P, _I32, _I32, _I32, _P, _P, _P, ctypes.POINTER(_I32), _P]
 lib.pkv_bm_beam_step_many.restype = ctypes.c_int
+lib.pkv_bm_shrink_batch.argtypes = [_P, _P, _P, _I32]
+lib.pkv_bm_shrink_batch.restype = ctypes.c_int
 lib.pkv_bm_seq_info.argtypes = [_P, _I32, ctypes.POINTER(_I64), ctypes.POINTER(_I32)]
 lib.pkv_bm_seq_info.restype = ctypes.c_int
 lib.pkv_bm_export.argtypes = [_P, _P, _I32, _I32, _P, _P]
@@ -166,6 +168,18 @@ class BlockManager:
                                          slots.ctypes.data, pairs.ctypes.data, ctypes.byref(ncow),
                                          shared.ctypes.data), "pkv_bm_beam_step_many")
         return new, slots, pairs[:ncow.value].copy(), shared
+
+    def shrink_batch(self, seqs, new_lens, max_blocks: int) -> tuple[np.ndarray, np.ndarray, np.ndarray]:
+        """Cut each sequence seqs[i] to new_lens[i] tokens: blocks behind are
+        released, shared ones among the rest replaced by fresh ones. Returns
+        what evict_tokens takes: (block_tables before, block_tables after,
+        context_lens before), rows of max_blocks entries."""
+        s, m = _i32(seqs), _i32(new_lens)
+        if s.shape != m.shape:
+            raise ValueError("seqs and new_lens differ in length")
+        before, lens = self.export(s, max_blocks)
+        _check(lib.pkv_bm_shrink_batch(self._h, s.ctypes.data, m.ctypes.data, s.size), "pkv_bm_shrink_batch")
+        return before, self.export(s, max_blocks)[0], lens
 
     def seq_info(self, seq: int) -> tuple[int, int]:
         """(length in tokens, table length in blocks) of seq."""

@@ -390,6 +390,53 @@ pkv_status pkv_bm_beam_step(pkv_block_manager* bm, const int32_t* beams, const i
   return pkv_bm_beam_step_many(bm, beams, parents, 1, width, n_new, new_beams, slots, cow_pairs, num_cow, nullptr);
 }
 
+pkv_status pkv_bm_shrink_batch(pkv_block_manager* bm, const int32_t* seqs, const int32_t* new_lens, int32_t n) {
+  if (bm == nullptr || n < 0 || (n > 0 && (seqs == nullptr || new_lens == nullptr))) return PKV_ERR_INVALID_ARG;
+  if (n == 0) return PKV_OK;
+  const int64_t bs = bm->block_size;
+  std::vector<int32_t> dropped;  // blocks that lose a reference
+  pkv_status bad = PKV_OK;
+  try {  // every allocation of the call happens here, before anything changes
+    bm->ensure_scratch();
+    int64_t need = 0;
+    size_t drops = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      if (!bm->is_live(seqs[i]) || new_lens[i] < 0 || new_lens[i] > bm->seqs[(size_t)seqs[i]].len ||
+          !bm->mark(seqs[i])) {
+        bad = PKV_ERR_INVALID_ARG;
+        break;
+      }
+      const pkv_block_manager::Seq& q = bm->seqs[(size_t)seqs[i]];
+      if (new_lens[i] == q.len) continue;
+      const size_t keep = (size_t)((new_lens[i] + bs - 1) / bs);
+      for (size_t j = 0; j < keep; ++j) need += bm->ref[(size_t)q.table[j]] > 1;
+      drops += q.table.size();
+    }
+    if (bad == PKV_OK && need > (int64_t)bm->free_stack.size()) bad = PKV_ERR_OUT_OF_BLOCKS;
+    if (bad == PKV_OK) dropped.reserve(drops);
+  } catch (...) {
+    bad = PKV_ERR_OUT_OF_BLOCKS;
+  }
+  bm->reset_scratch();
+  if (bad != PKV_OK) return bad;
+  // references as they were on entry decide, so all are looked at before any is dropped
+  for (int32_t i = 0; i < n; ++i) {
+    pkv_block_manager::Seq& q = bm->seqs[(size_t)seqs[i]];
+    if (new_lens[i] == q.len) continue;
+    const size_t keep = (size_t)((new_lens[i] + bs - 1) / bs);
+    for (size_t j = 0; j < q.table.size(); ++j) {
+      const int32_t b = q.table[j];
+      if (j < keep && bm->ref[(size_t)b] == 1) continue;
+      dropped.push_back(b);
+      if (j < keep) q.table[j] = bm->take_block();
+    }
+    q.table.resize(keep);
+    q.len = new_lens[i];
+  }
+  for (int32_t b : dropped) bm->drop_ref(b);
+  return PKV_OK;
+}
+
 pkv_status pkv_bm_seq_info(const pkv_block_manager* bm, int32_t seq, int64_t* length, int32_t* num_blocks) {
   if (bm == nullptr || !bm->is_live(seq)) return PKV_ERR_INVALID_ARG;
   const pkv_block_manager::Seq& s = bm->seqs[(size_t)seq];
