@@ -468,7 +468,7 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_c
  * All other arguments, layouts and errors as in pkv_paged_attention_decode,
  * but no wait can run out; PKV_ERR_INVALID_ARG for window < 1 or
  * num_sinks < 0, PKV_ERR_UNSUPPORTED when max_blocks_per_seq * block_size
- * exceeds 2^31 - 256. */
+ * exceeds 2^31 - 65536. */
 pkv_status pkv_paged_attention_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
                                              const int32_t* block_tables, const int32_t* context_lens, float scale,
                                              int window, int num_sinks, int num_heads, int num_kv_heads,
@@ -565,7 +565,7 @@ size_t pkv_decode_scores_workspace_bytes(int num_seqs, int num_heads, int num_kv
  * pointers, budget < 1, num_sinks or num_recent < 0 or together more than
  * budget, strides, overlapping score arrays, max_context_len >
  * max_blocks_per_seq * block_size), UNSUPPORTED (head_dim, block_size, dtype,
- * num_seqs or num_kv_heads > 65535, a table longer than 2^31 - 256 tokens).
+ * num_seqs or num_kv_heads > 65535, a table longer than 2^31 - 65536 tokens).
  * Device - a context length outside [0, max_context_len] is clamped and sets
  * PKV_DEV_ERR_CONTEXT_LEN; a row whose source or destination block is outside
  * [0, num_blocks) is not moved and sets PKV_DEV_ERR_BLOCK_ID. num_seqs == 0

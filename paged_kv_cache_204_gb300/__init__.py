@@ -28,6 +28,7 @@ The host block manager (include/pkv_block_manager.h) is wrapped by
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -40,7 +41,14 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"paged_kv_cache_204_gb300: compiled library missing at {LIB_PATH}; "
                       "build it with `python -m paged_kv_cache_204_gb300.build`")
 
+if not os.path.exists(_build.BINDING):
+    raise ImportError(f"paged_kv_cache_204_gb300: compiled binding missing at {_build.BINDING}; "
+                      "build it with `python -m paged_kv_cache_204_gb300.build`")
+
 lib = ctypes.CDLL(LIB_PATH)
+_binding_spec = importlib.util.spec_from_file_location("_pkv_torch", _build.BINDING)
+_binding = importlib.util.module_from_spec(_binding_spec)
+_binding_spec.loader.exec_module(_binding)
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA, PKV_ERR_OUT_OF_BLOCKS = range(6)
 DEV_ERR_BLOCK_ID, DEV_ERR_SLOT, DEV_ERR_CONTEXT_LEN, DEV_ERR_TIMEOUT, DEV_ERR_PAIR = 1, 2, 4, 8, 16
@@ -360,68 +368,6 @@ def new_scores_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_
     return ws
 
 
-def _want(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, what: str) -> int:
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor) -> torch.device:
-    """The pools' device, which every other tensor of the call has to be on."""
-    dev = k_cache.device
-    if dev.type != "cuda":
-        raise ValueError(f"k_cache: need a CUDA tensor, got {dev}")
-    if k_cache.dim() != 4 or not k_cache.is_contiguous():
-        raise ValueError("k_cache: need a contiguous [num_blocks, Hkv, block_size, D] tensor")
-    _want(v_cache, k_cache.shape, k_cache.dtype, dev, "v_cache")
-    return dev
-
-
-def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, dev: torch.device) -> tuple[int, int, int, int]:
-    """(sequences, table width, address of the tables, address of the lengths)"""
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables: need [num_seqs, max_blocks_per_seq]")
-    B, MB = block_tables.shape
-    return (B, MB, _want(block_tables, (B, MB), torch.int32, dev, "block_tables"),
-            _want(context_lens, (B,), torch.int32, dev, "context_lens"))
-
-
-def _space(workspace: torch.Tensor, dev: torch.device) -> tuple[int, int]:
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _err_ptr(dev_err: torch.Tensor | None, dev: torch.device) -> int | None:
-    if dev_err is None:
-        return None
-    if dev_err.dtype != torch.int32 or dev_err.numel() < 1 or dev_err.device != dev:
-        raise ValueError(f"dev_err: need an int32 tensor on {dev}")
-    return dev_err.data_ptr()
-
-
-def _call(fn, what: str, dev: torch.device, stream, *args) -> None:
-    """Call `fn` with the tensors' device current and, unless one is given,
-    that device's current stream."""
-    if dev.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        status = fn(*args, s.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            s = torch.cuda.current_stream() if stream is None else stream
-            status = fn(*args, s.cuda_stream)
-    if status != PKV_OK:
-        raise PkvError(status, what)
-
-
-def _code(dtype: torch.dtype, what: str) -> int:
-    code = DTYPE_CODE.get(dtype)
-    if code is None:
-        raise ValueError(f"{what}: {dtype} is not a type of this library")
-    return code
-
-
 def paged_attention_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, window: int,
                                   num_sinks: int, max_context_len: int, workspace: torch.Tensor,
@@ -430,16 +376,8 @@ def paged_attention_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: t
     num_sinks tokens and its newest `window` (the query's own included).
     Block-table entries of blocks with no visible token are not read.
     workspace: new_window_workspace()."""
-    dev = _pools(k_cache, v_cache)
-    nb, Hkv, bs, D = k_cache.shape
-    B, MB, bt, cl = _tables(block_tables, context_lens, dev)
-    H = q.shape[1] if q.dim() == 3 else -1
-    qp = _want(q, (B, H, D), k_cache.dtype, dev, "q")
-    op = _want(out, (B, H, D), k_cache.dtype, dev, "out")
-    ws, nbytes = _space(workspace, dev)
-    _call(lib.pkv_paged_attention_decode_window, "pkv_paged_attention_decode_window", dev, stream, op, qp,
-          k_cache.data_ptr(), v_cache.data_ptr(), bt, cl, scale, window, num_sinks, H, Hkv, D, bs, B, MB, nb,
-          max_context_len, _code(q.dtype, "q"), ws, nbytes, _err_ptr(dev_err, dev))
+    _check(_binding.decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, window, num_sinks,
+                                  max_context_len, workspace, dev_err, stream), "pkv_paged_attention_decode_window")
 
 
 def paged_attention_prefill_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -448,22 +386,8 @@ def paged_attention_prefill_window(out: torch.Tensor, q: torch.Tensor, k_cache: 
                                    max_query_len: int, dev_err: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention_prefill in which the query at position P sees the tokens
     t <= P with t < num_sinks or t > P - window."""
-    dev = _pools(k_cache, v_cache)
-    nb, Hkv, bs, D = k_cache.shape
-    B, MB, bt, cl = _tables(block_tables, context_lens, dev)
-    N, H = q.shape[:2] if q.dim() == 3 else (-1, -1)
-    qp = _want(q, (N, H, D), k_cache.dtype, dev, "q")
-    op = _want(out, (N, H, D), k_cache.dtype, dev, "out")
-    qs = _want(query_start, (B + 1,), torch.int32, dev, "query_start")
-    _call(lib.pkv_paged_attention_prefill_window, "pkv_paged_attention_prefill_window", dev, stream, op, qp,
-          k_cache.data_ptr(), v_cache.data_ptr(), bt, cl, qs, scale, window, num_sinks, H, Hkv, D, bs, B, MB, nb,
-          max_query_len, _code(q.dtype, "q"), _err_ptr(dev_err, dev))
-
-
-def _score_rows(t: torch.Tensor, B: int, Hkv: int, dev: torch.device, what: str) -> tuple[int, int]:
-    """(address, stride of a row) of a score array [B, Hkv, n]."""
-    n = t.shape[2] if t.dim() == 3 else -1
-    return _want(t, (B, Hkv, n), torch.float32, dev, what), n
+    _check(_binding.prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, window,
+                                   num_sinks, max_query_len, dev_err, stream), "pkv_paged_attention_prefill_window")
 
 
 def paged_attention_decode_scores(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tensor,
@@ -476,18 +400,9 @@ def paged_attention_decode_scores(out: torch.Tensor, scores_out: torch.Tensor, q
     scores float32 [B, Hkv, n >= max_context_len]; scores None: zeros;
     scores_out may be scores (in place). The newest token starts from zero.
     workspace: new_scores_workspace()."""
-    dev = _pools(k_cache, v_cache)
-    nb, Hkv, bs, D = k_cache.shape
-    B, MB, bt, cl = _tables(block_tables, context_lens, dev)
-    H = q.shape[1] if q.dim() == 3 else -1
-    qp = _want(q, (B, H, D), k_cache.dtype, dev, "q")
-    op = _want(out, (B, H, D), k_cache.dtype, dev, "out")
-    so, stride = _score_rows(scores_out, B, Hkv, dev, "scores_out")
-    si = None if scores is None else _want(scores, scores_out.shape, torch.float32, dev, "scores")
-    ws, nbytes = _space(workspace, dev)
-    _call(lib.pkv_paged_attention_decode_scores, "pkv_paged_attention_decode_scores", dev, stream, op, so, si, stride,
-          qp, k_cache.data_ptr(), v_cache.data_ptr(), bt, cl, scale, H, Hkv, D, bs, B, MB, nb, max_context_len,
-          _code(q.dtype, "q"), ws, nbytes, _err_ptr(dev_err, dev))
+    _check(_binding.decode_scores(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                  max_context_len, workspace, scores, dev_err, stream),
+           "pkv_paged_attention_decode_scores")
 
 
 def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor, scores_out: torch.Tensor,
@@ -504,21 +419,6 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Ten
     blocks are each the same as in block_tables or in no row of it
     (BlockManager.shrink_batch). Pools of any cache type; head_dim for uint8
     pools of q4_0 rows."""
-    dev = _pools(k_cache, v_cache)
-    nb, Hkv, bs, row = k_cache.shape
-    B, MB, bt, cl = _tables(block_tables, context_lens, dev)
-    dst = _want(dst_block_tables, (B, MB), torch.int32, dev, "dst_block_tables")
-    nl = _want(new_context_lens, (B,), torch.int32, dev, "new_context_lens")
-    si, s_in = _score_rows(scores, B, Hkv, dev, "scores")
-    so, s_out = _score_rows(scores_out, B, Hkv, dev, "scores_out")
-    budget = kept.shape[2] if kept.dim() == 3 else -1
-    kp = _want(kept, (B, Hkv, budget), torch.int32, dev, "kept")
-    code = _code(k_cache.dtype, "k_cache")
-    D = row
-    if head_dim is not None and head_dim != row:
-        if k_cache.dtype != torch.uint8 or q4_0_row_bytes(head_dim) != row:
-            raise ValueError(f"rows of {row} {k_cache.dtype} are no rows of head_dim {head_dim}")
-        D, code = head_dim, PKV_Q4_0
-    _call(lib.pkv_evict_tokens, "pkv_evict_tokens", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), si, s_in, so,
-          s_out, bt, dst, cl, nl, kp, budget, num_sinks, num_recent, Hkv, D, bs, B, MB, nb, max_context_len, code,
-          _err_ptr(dev_err, dev))
+    _check(_binding.evict_tokens(k_cache, v_cache, scores, scores_out, block_tables, dst_block_tables, context_lens,
+                                 new_context_lens, kept, num_sinks, num_recent, max_context_len, head_dim, dev_err,
+                                 stream), "pkv_evict_tokens")

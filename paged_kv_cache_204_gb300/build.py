@@ -1,7 +1,9 @@
 """Build the CUDA library in-tree: every .cu under csrc/ is compiled for
 sm_103a (and every .cpp, host-only code, by nvcc's host compiler) in
 parallel and linked into _build/libpkv.so (CUDA runtime linked statically,
-so the library loads beside any PyTorch build)."""
+so the library loads beside any PyTorch build). csrc/torch_binding.cxx becomes
+the Python extension _build/_pkv_torch.so, compiled against this machine's
+PyTorch and linked to libpkv.so."""
 from __future__ import annotations
 
 import glob
@@ -16,6 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cxx")
+BINDING = os.path.join(OUT_DIR, "_pkv_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -33,14 +37,28 @@ def _sources() -> list[str]:
 
 def _deps() -> list[str]:
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _binding_flags() -> tuple[list[str], list[str]]:
+    """Compiler and linker flags of the Python extension."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda", "include")
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda, INCLUDE]
+    libs = os.path.join(home, "lib")
+    return ([f"-I{i}" for i in inc] + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+            [f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}", LIB,
+             "-Wl,-rpath,$ORIGIN"])
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
@@ -58,18 +76,35 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
+    binding_obj = os.path.join(OUT_DIR, "torch_binding.cxx.o")
+
+    def compile_binding() -> list[str]:
+        cflags, ldflags = _binding_flags()
+        r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", *cflags, "-c", BINDING_SRC, "-o", binding_obj],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+        return ldflags
+
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, srcs))
+        ldflags = binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in results]
+    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpkv.so", "-o", tmp] + [o for o, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, binding_obj, *ldflags], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -12,10 +12,11 @@
 
 namespace {
 
-// Segments are cut until about this many CTAs are there, in pieces of at
-// least kMinTiles tiles.
-constexpr int64_t kTargetCtas = 152 * 8;
-constexpr int kMinTiles = 8;
+// Pieces of a segment: long enough that its start and join do not count, many
+// enough that the last wave of CTAs is a small part of all (kWaveCtas: CTAs that
+// are resident at a time).
+constexpr int64_t kWaveCtas = 152 * 3, kWaves = 5;
+constexpr int kMinTiles = 4, kMaxTiles = 96;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool supported_shape(int head_dim, int block_size) {
@@ -54,9 +55,9 @@ WindowLayout window_layout(int num_seqs, int num_heads, int num_kv_heads, int he
   const size_t rows = (size_t)num_seqs * num_heads;  // at least as many as segments
   size_t off = align_up(rows * sizeof(int32_t), 256);
   w.ml = off;
-  off += align_up((size_t)pkv::kWinMaxPieces * 8 * sizeof(float2), 256);
+  off += align_up((size_t)pkv::kWinPieceRows * sizeof(float2), 256);
   w.o = off;
-  off += (size_t)pkv::kWinMaxPieces * 8 * head_dim * sizeof(float);
+  off += (size_t)pkv::kWinPieceRows * head_dim * sizeof(float);
   if (scores) {
     w.row_ml = off;
     off += align_up(rows * sizeof(float2), 256);
@@ -80,7 +81,7 @@ pkv_status check_args(const void* out, const void* q, const void* k_cache, const
   if ((dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16) || !supported_shape(head_dim, block_size))
     return PKV_ERR_UNSUPPORTED;
   // token positions are kept in 32 bits, with a tile to spare
-  if (num_seqs > 65535 || (int64_t)max_blocks_per_seq * block_size > 0x7fffff00LL) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || (int64_t)max_blocks_per_seq * block_size > 0x7fff0000LL) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
@@ -99,10 +100,10 @@ pkv_status launch_decode(pkv::WindowParams& p, float scale, int head_dim, pkv_dt
   const int64_t segments = (int64_t)p.num_seqs * p.num_kv_heads * hp.parts;
   const int64_t seen = std::min<int64_t>(p.max_context_len, (int64_t)p.window + p.sinks);
   const int64_t tiles = (seen + 15) / 16 + 2;
-  int64_t splits = std::min((kTargetCtas + segments - 1) / segments, tiles / kMinTiles);
-  splits = std::min(splits, pkv::kWinMaxPieces / segments);
+  const int64_t per = std::min<int64_t>(std::max<int64_t>(segments * tiles / (kWaves * kWaveCtas), kMinTiles), kMaxTiles);
+  const int64_t splits = std::min((tiles + per - 1) / per, pkv::kWinPieceRows / hp.heads / segments);
   p.splits = (int)std::max<int64_t>(splits, 1);
-  p.min_tiles = kMinTiles;
+  p.min_tiles = (int)per;
   p.counter = reinterpret_cast<int32_t*>(ws + lay.counter);
   p.piece_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.piece_o = reinterpret_cast<float*>(ws + lay.o);
@@ -134,6 +135,7 @@ pkv::WindowParams operands(void* out, const void* q, const void* k_cache, const 
   p.num_kv_heads = num_kv_heads;
   p.group = num_heads / num_kv_heads;
   p.block_size = block_size;
+  p.block_bits = block_size == 8 ? 3 : (block_size == 16 ? 4 : 5);
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.max_context_len = max_context_len;
@@ -292,7 +294,7 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores, i
   if ((dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_FP8_E4M3 && dtype != PKV_Q4_0) ||
       !supported_shape(head_dim, block_size))
     return PKV_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || num_kv_heads > 65535 || (int64_t)max_blocks_per_seq * block_size > 0x7fffff00LL)
+  if (num_seqs > 65535 || num_kv_heads > 65535 || (int64_t)max_blocks_per_seq * block_size > 0x7fff0000LL)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   if (!k_cache || !v_cache || !scores || !scores_out || !block_tables || !dst_block_tables || !context_lens ||

@@ -11,12 +11,16 @@
 // Work: one CTA per piece of a (sequence, kv head, head part) segment; a head
 // part is up to 8 query heads of one kv head (16-bit caches) or up to 4 (32-bit
 // caches), so a K/V row is read once for all of them. A segment's visible
-// tokens are cut into aligned tiles of kTile tokens: first those of the sinks,
-// then those of the window. A piece is a contiguous run of its tiles; warp w
-// of the CTA takes the tiles w, w + 4, ... of the run. Each warp keeps its own
-// running maximum, exponential sum and output (online softmax, base 2); the
-// CTA joins its warps in shared memory, and the last CTA of a segment to
-// finish joins the pieces (log-sum-exp), all in one launch.
+// tokens are cut into aligned tiles of 16: first those of the sinks, then those
+// of the window. A piece is a contiguous run of its tiles; warp w of the CTA
+// takes the tiles w, w + 4, ... of the run. Each warp keeps its own running
+// maximum, exponential sum and output (online softmax, base 2); the CTA joins its
+// warps in shared memory, and the last CTA of a segment to finish joins the
+// pieces in their order (log-sum-exp), all in one launch.
+// Many short pieces, handed to the SMs as they come free, rather than one equal
+// run of tiles per resident CTA across the segments' borders: with several CTAs
+// on an SM the start and the join of one lie under the loads of the others (128
+// sequences x 40 heads, window 1004: 290 us against 384 us).
 #pragma once
 
 #include <type_traits>
@@ -28,7 +32,7 @@ namespace pkv {
 
 constexpr int kWinWarps = 4;
 constexpr int kWinThreads = kWinWarps * 32;
-constexpr int kWinMaxPieces = 2048;  // pieces of split segments that a workspace holds
+constexpr int kWinPieceRows = 32768;  // partial results (pieces x heads) that a workspace holds
 
 struct WindowParams {
   void* out;
@@ -43,12 +47,12 @@ struct WindowParams {
   int num_seqs, num_heads, num_kv_heads, group;
   int parts;       // head parts of one kv head
   int part_heads;  // query heads of a part (the last part may have fewer)
-  int block_size, max_blocks_per_seq, num_blocks, max_context_len;
+  int block_size, block_bits, max_blocks_per_seq, num_blocks, max_context_len;  // block_size = 2^block_bits
   int splits;        // pieces a segment may be cut into
   int min_tiles;     // tiles a piece has at least (where the segment has as many)
   int32_t* counter;  // [segments], zero between calls (splits > 1)
-  float2* piece_ml;  // [segments * splits][8] (m, l)
-  float* piece_o;    // [segments * splits][8][D], o / l
+  float2* piece_ml;  // [segments * splits][part_heads] (m, l)
+  float* piece_o;    // [segments * splits][part_heads][D]
   float* logits;     // scores: [num_seqs][num_heads][logit_stride], base-2 logits
   int64_t logit_stride;
   float2* row_ml;    // scores: [num_seqs][num_heads] final (m, l)
@@ -94,13 +98,18 @@ __device__ __forceinline__ int checked_len(const WindowParams& p, int s) {
   return L;
 }
 
-// A streaming 16-byte read: used once, so it takes no room in L1.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+// 16-byte asynchronous copy to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+// The same with `bytes` 16, or zeros (and nothing read) with 0.
+__device__ __forceinline__ void copy16_or_zeros(uint32_t smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename T>
@@ -150,25 +159,46 @@ __device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16) {
 // 2^(x - m) where m may still be -inf (nothing but -inf seen so far): 0 then.
 __device__ __forceinline__ float exp2_from(float x, float m) { return exp2f(x - (m == -INFINITY ? 0.f : m)); }
 
-// Physical blocks of a warp's tiles, fetched 32 tiles at a time: lane i holds
-// those of the warp's tile 32 b + i, one block for each 8 tokens of the tile's
-// first 16 (a tile lies in one block when the block is as long as the tile).
-// Blocks without a visible token are neither read nor checked: their table
-// entries may name blocks that were given back.
-template <int TT>
-struct TileBlocks {
-  static constexpr int kIds = TT / 8;  // 8-token runs of a tile
-  int id[kIds], next[kIds];
+__device__ __forceinline__ bool token_seen(const WindowParams& p, int64_t tok, int L) {
+  return tok < L && (tok < p.sinks || tok >= (int64_t)L - p.window);
+}
 
-  __device__ __forceinline__ void fetch(const WindowParams& p, const int32_t* row, const TileRange& r, int L, int i,
-                                        int end) {
+// A warp's tiles of TT tokens, one after another, through a ring of kStages slots
+// in shared memory (K rows, then V rows), filled by 16-byte asynchronous copies
+// kStages - 1 tiles ahead. Nothing is waited for but the warp's own copies. A row
+// of a tile in which a token is not visible reads as zeros, so that whatever its
+// place holds never meets a product. 16-byte chunk c of row r lies at chunk
+// position c ^ (r & 7) of its 128 bytes: eight rows' chunks c fall into
+// eight different bank groups.
+//
+// The table entries of the tiles come 32 tiles at a time: lane i holds the blocks
+// of the warp's tile 32 b + i, one for each 8 tokens. Blocks without a visible token are neither
+// read nor checked: their entries may name blocks that were given back.
+template <int TT, int ROW, int kStages>
+struct TileRing {
+  static constexpr int kIds = TT / 8;           // 8-token runs of a tile
+  static constexpr int kTileBytes = TT * ROW;   // K or V
+  static constexpr int kSlotBytes = 2 * kTileBytes;
+  static constexpr int kBytes = kStages * kSlotBytes;
+  static constexpr int CPR = ROW / 16;          // chunks of a row
+  static constexpr int kPerRun = 8 * CPR / 32;  // copies of a lane for one run of K (or V)
+  static_assert(CPR % 8 == 0 && 8 * CPR % 32 == 0, "rows of whole 128-byte lines");
+
+  unsigned char* base;
+  const int32_t* row;
+  int id[kIds], next[kIds];
+  int L, kvh, lane, step, end;   // end: of the tile indexes of the piece
+  int issue_at, issued;          // next tile to copy, tiles copied so far
+  TileRange r;
+
+  __device__ __forceinline__ void fetch(const WindowParams& p, int i) {
 #pragma unroll
     for (int k = 0; k < kIds; ++k) {
       next[k] = 0;
       if (i < end) {
         const int64_t t = (int64_t)r.tile(i) * TT + 8 * k;
         if (t < L && (t < p.sinks || t + 8 > (int64_t)L - p.window)) {
-          int b = __ldg(row + t / p.block_size);
+          int b = __ldg(row + (t >> p.block_bits));
           if (b < 0 || b >= p.num_blocks) {
             set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
             b = 0;
@@ -178,42 +208,91 @@ struct TileBlocks {
       }
     }
   }
-  __device__ __forceinline__ void advance() {
+
+  // Tile issue_at into its slot; always commits a group.
+  __device__ __forceinline__ void issue(const WindowParams& p) {
+    if (issue_at < end) {
+      if ((issued & 31) == 0) {
 #pragma unroll
-    for (int k = 0; k < kIds; ++k) id[k] = next[k];
+        for (int k = 0; k < kIds; ++k) id[k] = next[k];
+        fetch(p, issue_at + (32 + lane) * step);
+      }
+      const int64_t t0 = (int64_t)r.tile(issue_at) * TT;
+      const uint32_t slot = smem_u32(base) + (issued % kStages) * kSlotBytes;
+      // the tile's tokens are all visible, or it is looked at row by row
+      const bool full = t0 + TT <= L && (t0 + TT <= p.sinks || t0 >= (int64_t)L - p.window);
+#pragma unroll
+      for (int k = 0; k < kIds; ++k) {
+        const int b = __shfl_sync(kFullMask, id[k], issued & 31);
+        const int64_t t = t0 + 8 * k;
+        const size_t at =
+            (((size_t)b * p.num_kv_heads + kvh) * p.block_size + (size_t)(t & (p.block_size - 1))) * ROW + lane * 16;
+        const char* kg = static_cast<const char*>(p.k_cache) + at;
+        const char* vg = static_cast<const char*>(p.v_cache) + at;
+#pragma unroll
+        for (int j = 0; j < kPerRun; ++j) {
+          const int e = j * 32 + lane, rr = e / CPR, c = e % CPR;
+          const uint32_t to = slot + (8 * k + rr) * ROW + (c ^ (rr & 7)) * 16;
+          if (full) {
+            copy16(to, kg + j * 512);
+            copy16(to + kTileBytes, vg + j * 512);
+          } else {
+            const int bytes = token_seen(p, t + rr, L) ? 16 : 0;
+            copy16_or_zeros(to, kg + j * 512, bytes);
+            copy16_or_zeros(to + kTileBytes, vg + j * 512, bytes);
+          }
+        }
+      }
+      issue_at += step;
+      ++issued;
+    }
+    copies_commit();
+  }
+
+  __device__ __forceinline__ void start(const WindowParams& p, unsigned char* ring, int s, int kv_head, int length,
+                                        const TileRange& range, int begin, int stop, int warp, int warps, int ln) {
+    base = ring;
+    row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    L = length;
+    kvh = kv_head;
+    r = range;
+    lane = ln;
+    step = warps;
+    end = stop;
+    issue_at = begin + warp;
+    issued = 0;
+    fetch(p, issue_at + lane * step);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(p);
   }
 };
 
 // ---- 16-bit caches: tensor-core tiles ----------------------------------------
-// Tiles of 16 tokens, read from global memory straight into the registers that
-// feed m16n8k16 MMAs (binary16 or bfloat16 operands, fp32 accumulation): a row
-// is used by one warp only, so shared memory would only add a copy.
+// Tiles of 16 tokens through m16n8k16 MMAs (binary16 or bfloat16 operands, fp32
+// accumulation): with at most 8 queries to a K/V row the work is bound by memory,
+// and these take the rows as the cache holds them.
 //
-// Scores, S^T = K q^T: tokens are M, head dims K, query heads N. The head dims
-// are permuted alike in K and q, which leaves the product as it is: lane
-// (g, t) = (lane / 4, lane % 4) takes 16-byte chunks t, t + 4, ... of token
-// rows g and g + 8, so the four lanes of a row read 64 contiguous bytes, and of
-// the row of head g. Words 0, 1 of a chunk make one k-step, words 2, 3 the next.
-// Output, O^T += V^T P^T: head dims are M, tokens K, query heads N. Lane (g, t)
-// reads chunks g, g + 8 of token rows 2t, 2t + 1, 2t + 8, 2t + 9; word w of a
-// chunk makes one m-tile, its low half row g and its high half row g + 8.
-// P^T comes from the score layout by 8 x 8 transposes.
+// Scores, S^T = K q^T: tokens are M, head dims K, query heads N. Output,
+// O^T += V^T P^T: head dims are M, tokens K, query heads N; V^T comes from V rows by
+// transposing matrix loads, P^T from the score layout by 8 x 8 transposes. Lane
+// (g, t) = (lane / 4, lane % 4) ends with head dims 16 m + g and 16 m + g + 8 of
+// the heads 2t, 2t + 1.
 // P enters as a 16-bit high part and a 16-bit remainder (16 significant bits or
-// more with either type), so that its rounding stays below the output's. With at most 4
-// heads the high parts fill columns 0-3 and the remainders columns 4-7 of one
-// MMA (kWide false); with 5-8 heads they take two.
+// more with either type), so that its rounding stays below the output's. With at
+// most 4 heads the high parts fill columns 0-3 and the remainders columns 4-7 of
+// one MMA (kWide false); with 5-8 heads they take two.
 template <typename T, int D, bool kWide, bool kLogits>
 struct MmaTile {
   static constexpr int TT = 16;
   static constexpr int kHeads = kWide ? 8 : 4;
-  static constexpr int NC = D / 32;  // chunks of a K row per lane
-  static constexpr int NV = D / 64;  // chunks of a V row per lane
+  static constexpr int KS = D / 16;  // k-steps of the scores, m-tiles of the output
   static constexpr int ROW = D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of ring per warp, three CTAs on an SM
+  using Ring = TileRing<TT, ROW, kStages>;
 
-  uint32_t qf[NC][4];
-  float m[2], l[2];       // heads 2t, 2t + 1 (of the lane's columns); l: this lane's tokens
-  float o[NV * 4][4];
-  uint4 kr[2][NC], vr[4][NV];
+  uint32_t qf[KS][2];
+  float m[2], l[2];  // heads 2t, 2t + 1 (of the lane's columns); l: this lane's tokens
+  float o[KS][4];
   int heads, g, t;
 
   __device__ __forceinline__ void init(const WindowParams& p, int s, int h0, int nheads, int lane) {
@@ -222,73 +301,45 @@ struct MmaTile {
     t = lane & 3;
     const int h = kWide ? g : (g & 3);
     const bool ok = h < nheads;
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p.q) +
-                                                    ((size_t)s * p.num_heads + h0 + (ok ? h : 0)) * ROW);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const char*>(p.q) +
+                                                          ((size_t)s * p.num_heads + h0 + (ok ? h : 0)) * ROW);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const uint4 u = ok ? __ldg(q + t + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-      qf[c][0] = u.x, qf[c][1] = u.y, qf[c][2] = u.z, qf[c][3] = u.w;
+    for (int k = 0; k < KS; ++k) {
+      qf[k][0] = ok ? __ldg(q + 8 * k + t) : 0u;
+      qf[k][1] = ok ? __ldg(q + 8 * k + 4 + t) : 0u;
     }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
 
-  static __device__ __forceinline__ bool seen(const WindowParams& p, int64_t tok, int L) {
-    return tok < L && (tok < p.sinks || tok >= (int64_t)L - p.window);
-  }
-
-  __device__ __forceinline__ void load_k(const WindowParams& p, int kvh, int64_t t0, int L, int b0, int b1) {
-    const char* base = static_cast<const char*>(p.k_cache);
+  __device__ __forceinline__ void consume(const WindowParams& p, int s, int h0, const unsigned char* slot, int64_t t0,
+                                          int L, int lane) {
+    const uint32_t ks = smem_u32(slot);
+    // K fragments: lane i gives row i % 16, chunk 2 k + i / 16
+    const uint32_t r = lane & 15, half = lane >> 4;
+    float a[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t tok = t0 + g + 8 * i;
-      const bool ok = seen(p, tok, L);
-      const char* row = base + (((size_t)(i ? b1 : b0) * p.num_kv_heads + kvh) * p.block_size +
-                                (int)(tok & (p.block_size - 1))) * ROW;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) kr[i][c] = ok ? ld_stream(row + 16 * (t + 4 * c)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < KS; ++k) {
+      uint32_t f[4];
+      ldsm_x4(ks + r * ROW + ((2 * k + half) ^ (r & 7)) * 16, f);
+      mma_16816<T>(a[k & 1], f[0], f[1], f[2], f[3], qf[k][0], qf[k][1]);
     }
-  }
-  __device__ __forceinline__ void load_v(const WindowParams& p, int kvh, int64_t t0, int L, int b0, int b1) {
-    const char* base = static_cast<const char*>(p.v_cache);
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t tok = t0 + 2 * t + (i & 1) + 8 * (i >> 1);
-      const bool ok = seen(p, tok, L);
-      const char* row = base + (((size_t)(i >> 1 ? b1 : b0) * p.num_kv_heads + kvh) * p.block_size +
-                                (int)(tok & (p.block_size - 1))) * ROW;
+    for (int i = 0; i < 4; ++i)
+      x[i] = token_seen(p, t0 + g + 8 * (i >> 1), L) ? (a[0][i] + a[1][i]) * p.scale_log2 : -INFINITY;
+    if constexpr (kLogits) {
 #pragma unroll
-      for (int c = 0; c < NV; ++c) vr[i][c] = ok ? ld_stream(row + 16 * (g + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i) {
+        const int h = 2 * t + (i & 1);
+        const int64_t tok = t0 + g + 8 * (i >> 1);
+        if (h < heads && (kWide || t < 2) && tok < L)
+          p.logits[((size_t)s * p.num_heads + h0 + h) * p.logit_stride + tok] = x[i];
+      }
     }
-  }
-
-  // Scores of the tile in kr, as base-2 logits; masked tokens -inf.
-  __device__ __forceinline__ void scores(const WindowParams& p, int64_t t0, int L, float (&x)[4]) {
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      mma_16816<T>(a, kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y, qf[c][0], qf[c][1]);
-      mma_16816<T>(a, kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w, qf[c][2], qf[c][3]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = seen(p, t0 + g + 8 * (i >> 1), L) ? a[i] * p.scale_log2 : -INFINITY;
-  }
-
-  __device__ __forceinline__ void store_logits(const WindowParams& p, int s, int h0, int64_t t0, int L,
-                                               const float (&x)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = 2 * t + (i & 1);
-      const int64_t tok = t0 + g + 8 * (i >> 1);
-      if (h < heads && (kWide || t < 2) && tok < L)
-        p.logits[((size_t)s * p.num_heads + h0 + h) * p.logit_stride + tok] = x[i];
-    }
-  }
-
-  // Running maximum and sums, then the P operand of the tile.
-  __device__ __forceinline__ void softmax(const float (&x)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+    // running maximum and sums, then the P operand
     float pr[4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -301,40 +352,37 @@ struct MmaTile {
       pr[c] = exp2_from(x[c], mn);
       pr[c + 2] = exp2_from(x[c + 2], mn);
       l[c] = l[c] * alpha + (pr[c] + pr[c + 2]);
+      if (__any_sync(kFullMask, alpha != 1.f)) {
 #pragma unroll
-      for (int i = 0; i < NV * 4; ++i) {
-        o[i][c] *= alpha;
-        o[i][c + 2] *= alpha;
+        for (int i = 0; i < KS; ++i) {
+          o[i][c] *= alpha;
+          o[i][c + 2] *= alpha;
+        }
       }
     }
+    uint32_t hi[2], lo[2];
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const uint32_t h = pack2(pr[2 * v], pr[2 * v + 1], T());
       const float2 f = unpack2(h, T());
-      const uint32_t r = pack2(pr[2 * v] - f.x, pr[2 * v + 1] - f.y, T());
+      const uint32_t rest = pack2(pr[2 * v] - f.x, pr[2 * v + 1] - f.y, T());
       if constexpr (kWide) {
         hi[v] = transpose8x8(h);
-        lo[v] = transpose8x8(r);
+        lo[v] = transpose8x8(rest);
       } else {
-        hi[v] = transpose8x8(t < 2 ? h : r);
+        hi[v] = transpose8x8(t < 2 ? h : rest);
       }
     }
-  }
-
-  __device__ __forceinline__ void accumulate(const uint32_t (&hi)[2], const uint32_t (&lo)[2]) {
+    // V^T fragments: matrices (dims 0-7, tokens 0-7), (dims 8-15, tokens 0-7), then
+    // tokens 8-15; lane i gives token row i % 8 + 8 (i / 16), chunk 2 m + (i / 8) % 2
+    const uint32_t vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+    const uint32_t vs = ks + Ring::kTileBytes + vr * ROW;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const uint32_t* r0 = reinterpret_cast<const uint32_t*>(&vr[0][c]);
-      const uint32_t* r1 = reinterpret_cast<const uint32_t*>(&vr[1][c]);
-      const uint32_t* r2 = reinterpret_cast<const uint32_t*>(&vr[2][c]);
-      const uint32_t* r3 = reinterpret_cast<const uint32_t*>(&vr[3][c]);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = __byte_perm(r0[w], r1[w], 0x5410), a1 = __byte_perm(r0[w], r1[w], 0x7632);
-        const uint32_t a2 = __byte_perm(r2[w], r3[w], 0x5410), a3 = __byte_perm(r2[w], r3[w], 0x7632);
-        mma_16816<T>(o[4 * c + w], a0, a1, a2, a3, hi[0], hi[1]);
-        if constexpr (kWide) mma_16816<T>(o[4 * c + w], a0, a1, a2, a3, lo[0], lo[1]);
-      }
+    for (int mt = 0; mt < KS; ++mt) {
+      uint32_t f[4];
+      ldsm_x4_trans(vs + ((2 * mt + vc) ^ (vr & 7)) * 16, f);
+      mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], hi[0], hi[1]);
+      if constexpr (kWide) mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], lo[0], lo[1]);
     }
   }
 
@@ -347,7 +395,7 @@ struct MmaTile {
     }
     if constexpr (!kWide) {  // high part plus remainder: columns 2t and 2t + 4
 #pragma unroll
-      for (int i = 0; i < NV * 4; ++i)
+      for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(kFullMask, o[i][e], 2);
     }
@@ -357,54 +405,11 @@ struct MmaTile {
         const int h = 2 * t + c;
         if (g == 0) sm_ml[h] = make_float2(m[c], l[c]);
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<float2*>(sm_o + h * D + (g + 8 * n) * 8 + 2 * w) =
-                make_float2(o[4 * n + w][c], o[4 * n + w][c + 2]);
-      }
-    }
-  }
-
-  // One tile after another; the next tile's K rows are asked for as soon as
-  // this tile's have been used, the V rows likewise.
-  __device__ __forceinline__ void walk(const WindowParams& p, int s, int kvh, int h0, int L, const TileRange& r,
-                                       int begin, int end, int warp, int lane) {
-    const int32_t* row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-    TileBlocks<TT> tb;
-    int i = begin + warp;
-    if (i >= end) return;
-    tb.fetch(p, row, r, L, i + lane * kWinWarps, end);
-    tb.advance();
-    tb.fetch(p, row, r, L, i + (32 + lane) * kWinWarps, end);
-    int64_t t0 = (int64_t)r.tile(i) * TT;
-    int b0 = __shfl_sync(kFullMask, tb.id[0], 0), b1 = __shfl_sync(kFullMask, tb.id[1], 0);
-    load_k(p, kvh, t0, L, b0, b1);
-    load_v(p, kvh, t0, L, b0, b1);
-    for (int n = 1;; ++n) {
-      const int in = i + kWinWarps;
-      const bool more = in < end;
-      int64_t t1 = t0;
-      if (more) {
-        if ((n & 31) == 0) {
-          tb.advance();
-          tb.fetch(p, row, r, L, in + (32 + lane) * kWinWarps, end);
+        for (int i = 0; i < KS; ++i) {
+          sm_o[h * D + 16 * i + g] = o[i][c];
+          sm_o[h * D + 16 * i + g + 8] = o[i][c + 2];
         }
-        t1 = (int64_t)r.tile(in) * TT;
-        b0 = __shfl_sync(kFullMask, tb.id[0], n & 31);
-        b1 = __shfl_sync(kFullMask, tb.id[1], n & 31);
       }
-      float x[4];
-      scores(p, t0, L, x);
-      if (more) load_k(p, kvh, t1, L, b0, b1);
-      if constexpr (kLogits) store_logits(p, s, h0, t0, L, x);
-      uint32_t hi[2], lo[2];
-      softmax(x, hi, lo);
-      accumulate(hi, lo);
-      if (!more) break;
-      load_v(p, kvh, t1, L, b0, b1);
-      i = in;
-      t0 = t1;
     }
   }
 };
@@ -415,12 +420,13 @@ struct MmaTile {
 // over the group with shuffles.
 template <int D, int kPart, bool kLogits>
 struct FmaTile {
-  static constexpr int RPG = D == 128 ? 2 : 4;  // rows of a tile per group
-  static constexpr int TT = 16;                 // two steps of 8 tokens at head_dim 128
-  static constexpr int kSteps = TT / (4 * RPG);
+  static constexpr int TT = D == 128 ? 8 : 16;  // 8 KB of K and V rows
+  static constexpr int RPG = TT / 4;            // rows of a tile per group
   static constexpr int kHeads = kPart;
   static constexpr int NC = D / 32;  // chunks of a row per lane
   static constexpr int ROW = D * 4;
+  static constexpr int kStages = 2;
+  using Ring = TileRing<TT, ROW, kStages>;
 
   float qf[kPart][NC * 4], o[kPart][NC * 4];
   float m[kPart], l[kPart];
@@ -447,85 +453,72 @@ struct FmaTile {
     }
   }
 
-  __device__ __forceinline__ void walk(const WindowParams& p, int s, int kvh, int h0, int L, const TileRange& r,
-                                       int begin, int end, int warp, int lane) {
-    const int32_t* row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-    TileBlocks<TT> tb;
-    if (begin + warp >= end) return;
-    tb.fetch(p, row, r, L, begin + warp + lane * kWinWarps, end);
-    for (int i = begin + warp, n = 0; i < end; i += kWinWarps, ++n) {
-      if ((n & 31) == 0) {
-        tb.advance();
-        tb.fetch(p, row, r, L, i + (32 + lane) * kWinWarps, end);
-      }
-      const int b0 = __shfl_sync(kFullMask, tb.id[0], n & 31), b1 = __shfl_sync(kFullMask, tb.id[1], n & 31);
+  __device__ __forceinline__ float4 chunk(const unsigned char* rows, int r, int c) const {
+    return *reinterpret_cast<const float4*>(rows + r * ROW + ((sub + 8 * c) ^ (r & 7)) * 16);
+  }
+
+  __device__ __forceinline__ void consume(const WindowParams& p, int s, int h0, const unsigned char* slot, int64_t t0,
+                                          int L, int) {
+    bool ok[RPG];
+    float x[kPart][RPG];
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const int64_t t0 = (int64_t)r.tile(i) * TT + st * 4 * RPG;
-        float4 kr[RPG][NC], vr[RPG][NC];
-        bool ok[RPG];
+    for (int j = 0; j < RPG; ++j) {
+      const int r = 4 * j + grp;
+      ok[j] = token_seen(p, t0 + r, L);
+      float4 k[NC];
 #pragma unroll
-        for (int j = 0; j < RPG; ++j) {
-          const int64_t tok = t0 + 4 * j + grp;
-          ok[j] = tok < L && (tok < p.sinks || tok >= (int64_t)L - p.window);
-          const int b = (tok & 8) ? b1 : b0;
-          const size_t at =
-              (((size_t)b * p.num_kv_heads + kvh) * p.block_size + (int)(tok & (p.block_size - 1))) * ROW;
+      for (int c = 0; c < NC; ++c) k[c] = chunk(slot, r, c);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
-            if (ok[j]) {
-              u = ld_stream(static_cast<const char*>(p.k_cache) + at + 16 * (sub + 8 * c));
-              v = ld_stream(static_cast<const char*>(p.v_cache) + at + 16 * (sub + 8 * c));
-            }
-            memcpy(&kr[j][c], &u, 16);
-            memcpy(&vr[j][c], &v, 16);
-          }
+      for (int h = 0; h < kPart; ++h) {
+        float a = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          a = fmaf(qf[h][4 * c], k[c].x, a);
+          a = fmaf(qf[h][4 * c + 1], k[c].y, a);
+          a = fmaf(qf[h][4 * c + 2], k[c].z, a);
+          a = fmaf(qf[h][4 * c + 3], k[c].w, a);
         }
+        a += __shfl_xor_sync(kFullMask, a, 1);
+        a += __shfl_xor_sync(kFullMask, a, 2);
+        a += __shfl_xor_sync(kFullMask, a, 4);
+        x[h][j] = ok[j] ? a * p.scale_log2 : -INFINITY;
+        if constexpr (kLogits) {
+          if (sub == 0 && h < heads && t0 + r < L)
+            p.logits[((size_t)s * p.num_heads + h0 + h) * p.logit_stride + t0 + r] = x[h][j];
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kPart; ++h) {
+      float mx = x[h][0];
+#pragma unroll
+      for (int j = 1; j < RPG; ++j) mx = fmaxf(mx, x[h][j]);
+      mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
+      const float mn = fmaxf(m[h], mx);
+      const float alpha = exp2_from(m[h], mn);
+      m[h] = mn;
+      l[h] *= alpha;
+#pragma unroll
+      for (int e = 0; e < NC * 4; ++e) o[h][e] *= alpha;
+#pragma unroll
+      for (int j = 0; j < RPG; ++j) {
+        x[h][j] = exp2_from(x[h][j], mn);
+        l[h] += x[h][j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RPG; ++j) {
+      const int r = 4 * j + grp;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float4 v = chunk(slot + Ring::kTileBytes, r, c);
 #pragma unroll
         for (int h = 0; h < kPart; ++h) {
-          float x[RPG], mx = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < RPG; ++j) {
-            float a = 0.f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              a = fmaf(qf[h][4 * c], kr[j][c].x, a);
-              a = fmaf(qf[h][4 * c + 1], kr[j][c].y, a);
-              a = fmaf(qf[h][4 * c + 2], kr[j][c].z, a);
-              a = fmaf(qf[h][4 * c + 3], kr[j][c].w, a);
-            }
-            a += __shfl_xor_sync(kFullMask, a, 1);
-            a += __shfl_xor_sync(kFullMask, a, 2);
-            a += __shfl_xor_sync(kFullMask, a, 4);
-            x[j] = ok[j] ? a * p.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, x[j]);
-            if constexpr (kLogits) {
-              const int64_t tok = t0 + 4 * j + grp;
-              if (sub == 0 && h < heads && tok < L)
-                p.logits[((size_t)s * p.num_heads + h0 + h) * p.logit_stride + tok] = x[j];
-            }
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
-          const float mn = fmaxf(m[h], mx);
-          const float alpha = exp2_from(m[h], mn);
-          m[h] = mn;
-          l[h] *= alpha;
-#pragma unroll
-          for (int e = 0; e < NC * 4; ++e) o[h][e] *= alpha;
-#pragma unroll
-          for (int j = 0; j < RPG; ++j) {
-            const float w = exp2_from(x[j], mn);
-            l[h] += w;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              o[h][4 * c] = fmaf(w, vr[j][c].x, o[h][4 * c]);
-              o[h][4 * c + 1] = fmaf(w, vr[j][c].y, o[h][4 * c + 1]);
-              o[h][4 * c + 2] = fmaf(w, vr[j][c].z, o[h][4 * c + 2]);
-              o[h][4 * c + 3] = fmaf(w, vr[j][c].w, o[h][4 * c + 3]);
-            }
-          }
+          o[h][4 * c] = fmaf(x[h][j], v.x, o[h][4 * c]);
+          o[h][4 * c + 1] = fmaf(x[h][j], v.y, o[h][4 * c + 1]);
+          o[h][4 * c + 2] = fmaf(x[h][j], v.z, o[h][4 * c + 2]);
+          o[h][4 * c + 3] = fmaf(x[h][j], v.w, o[h][4 * c + 3]);
         }
       }
     }
@@ -561,14 +554,27 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
   }
 }
 
-// Join of n partial results (m_j, l_j, o_j): M = max m_j, l = sum l_j 2^(m_j - M),
-// o = sum o_j w_j; an empty part has m_j = -inf and l_j = 0.
+// Join of partial results (m_j, l_j, o_j): M = max m_j, l = sum l_j 2^(m_j - M),
+// o = sum o_j 2^(m_j - M); an empty part has m_j = -inf, l_j = 0 and o_j = 0.
+struct Join {
+  float l, a[4];
+  __device__ __forceinline__ void clear() { l = a[0] = a[1] = a[2] = a[3] = 0.f; }
+  __device__ __forceinline__ void add(float2 ml, float4 o, float M) {
+    const float f = exp2_from(ml.x, M);
+    l += ml.y * f;
+    a[0] = fmaf(o.x, f, a[0]), a[1] = fmaf(o.y, f, a[1]), a[2] = fmaf(o.z, f, a[2]), a[3] = fmaf(o.w, f, a[3]);
+  }
+};
+
 template <typename T, int D, typename Tile, bool kLogits>
 __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowParams p) {
   constexpr int HP = Tile::kHeads;
-  __shared__ __align__(16) float sm_o[kWinWarps][HP * D];
+  using Ring = typename Tile::Ring;
+  extern __shared__ __align__(128) unsigned char rings[];  // one per warp; its result replaces it at the end
   __shared__ float2 sm_ml[kWinWarps][HP];
   __shared__ int sm_last;
+  static_assert(Ring::kBytes >= HP * D * (int)sizeof(float), "room for a warp's result");
+  if constexpr (kLogits) grid_launch_dependents();
 
   const int piece = blockIdx.x % p.splits;
   const int seg = blockIdx.x / p.splits;
@@ -583,39 +589,48 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   // pieces of this segment: none is shorter than min_tiles where that can be
   const int pieces = max(1, min(p.splits, r.n / p.min_tiles));
   if (piece >= pieces) return;
-  const int begin = (int)((int64_t)r.n * piece / pieces), end = (int)((int64_t)r.n * (piece + 1) / pieces);
+  // in whole rounds of the warps
+  const int rounds = (r.n + kWinWarps - 1) / kWinWarps;
+  const int begin = (int)((int64_t)rounds * piece / pieces) * kWinWarps;
+  const int end = min((int)((int64_t)rounds * (piece + 1) / pieces) * kWinWarps, r.n);
 
+  unsigned char* mine = rings + warp * Ring::kBytes;
+  Ring ring;
   Tile tile;
+  ring.start(p, mine, s, kvh, L, r, begin, end, warp, kWinWarps, lane);
   tile.init(p, s, h0, heads, lane);
-  tile.walk(p, s, kvh, h0, L, r, begin, end, warp, lane);
-  tile.finish(sm_o[warp], sm_ml[warp]);
+  for (int i = begin + warp, n = 0; i < end; i += kWinWarps, ++n) {
+    copies_wait<Tile::kStages - 2>();
+    __syncwarp();  // tile n has landed for all lanes, and all are done with the slot refilled now
+    ring.issue(p);
+    tile.consume(p, s, h0, mine + (n % Tile::kStages) * Ring::kSlotBytes, (int64_t)r.tile(i) * Tile::TT, L, lane);
+  }
+  __syncwarp();
+  tile.finish(reinterpret_cast<float*>(mine), sm_ml[warp]);
   __syncthreads();
 
   // join the warps: a thread takes 4 dims of a head
   T* out = static_cast<T*>(p.out) + ((size_t)s * p.num_heads + h0) * D;
-  const size_t slot = ((size_t)seg * p.splits + piece) * HP;
+  const size_t first = (size_t)seg * p.splits * p.part_heads;
+  const size_t slot = first + (size_t)piece * p.part_heads;
   for (int i = threadIdx.x; i < heads * (D / 4); i += kWinThreads) {
     const int h = i / (D / 4), d = 4 * (i % (D / 4));
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWinWarps; ++w) M = fmaxf(M, sm_ml[w][h].x);
-    float l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+    Join t;
+    t.clear();
 #pragma unroll
-    for (int w = 0; w < kWinWarps; ++w) {
-      const float2 ml = sm_ml[w][h];
-      const float f = exp2_from(ml.x, M);
-      const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][h * D + d]);
-      l += ml.y * f;
-      a[0] = fmaf(v.x, f, a[0]), a[1] = fmaf(v.y, f, a[1]), a[2] = fmaf(v.z, f, a[2]), a[3] = fmaf(v.w, f, a[3]);
-    }
+    for (int w = 0; w < kWinWarps; ++w)
+      t.add(sm_ml[w][h], reinterpret_cast<const float4*>(rings + w * Ring::kBytes)[(h * D + d) / 4], M);
     if (pieces == 1) {
       // no token: zeros; a row whose every logit is -inf: 0 / 0, as the formula has it
-      const float inv = L > 0 ? 1.f / l : 0.f;
-      store4(out + h * D + d, a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-      if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, l);
+      const float inv = L > 0 ? 1.f / t.l : 0.f;
+      store4(out + h * D + d, t.a[0] * inv, t.a[1] * inv, t.a[2] * inv, t.a[3] * inv);
+      if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, t.l);
     } else {
-      __stcg(reinterpret_cast<float4*>(p.piece_o + (slot + h) * D + d), make_float4(a[0], a[1], a[2], a[3]));
-      if (d == 0) __stcg(p.piece_ml + slot + h, make_float2(M, l));
+      __stcg(reinterpret_cast<float4*>(p.piece_o + (slot + h) * D + d), make_float4(t.a[0], t.a[1], t.a[2], t.a[3]));
+      if (d == 0) __stcg(p.piece_ml + slot + h, make_float2(M, t.l));
     }
   }
   if (pieces == 1) return;
@@ -623,31 +638,27 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   // the last piece of the segment joins them all
   __syncthreads();  // the partial's writes precede the release below
   if (threadIdx.x == 0) {
-    __threadfence();
     const int prev = atomic_add_acq_rel_gpu(p.counter + seg, 1);
     sm_last = prev == pieces - 1;
     if (prev == pieces - 1) p.counter[seg] = 0;  // all have counted: zero for the next call
   }
   __syncthreads();
   if (!sm_last) return;
-  __threadfence();
-  const size_t first = (size_t)seg * p.splits * HP;
   for (int i = threadIdx.x; i < heads * (D / 4); i += kWinThreads) {
     const int h = i / (D / 4), d = 4 * (i % (D / 4));
     float M = -INFINITY;
-    for (int j = 0; j < pieces; ++j) M = fmaxf(M, __ldcg(p.piece_ml + first + (size_t)j * HP + h).x);
-    float l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
+    for (int j = 0; j < pieces; ++j) M = fmaxf(M, __ldcg(p.piece_ml + first + (size_t)j * p.part_heads + h).x);
+    Join t;
+    t.clear();
+#pragma unroll 8
     for (int j = 0; j < pieces; ++j) {
-      const float2 ml = __ldcg(p.piece_ml + first + (size_t)j * HP + h);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.piece_o + (first + (size_t)j * HP + h) * D + d));
-      const float f = exp2_from(ml.x, M);
-      l += ml.y * f;
-      a[0] = fmaf(v.x, f, a[0]), a[1] = fmaf(v.y, f, a[1]), a[2] = fmaf(v.z, f, a[2]), a[3] = fmaf(v.w, f, a[3]);
+      const size_t at = first + (size_t)j * p.part_heads + h;
+      t.add(__ldcg(p.piece_ml + at), __ldcg(reinterpret_cast<const float4*>(p.piece_o + at * D + d)), M);
     }
-    const float inv = 1.f / l;
-    store4(out + h * D + d, a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-    if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, l);
+    const float inv = 1.f / t.l;
+    store4(out + h * D + d, t.a[0] * inv, t.a[1] * inv, t.a[2] * inv, t.a[3] * inv);
+    if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, t.l);
   }
 }
 

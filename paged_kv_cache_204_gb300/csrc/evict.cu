@@ -7,19 +7,24 @@
 // 0 .. n - 1 in their order.
 //
 // Two launches: evict_select_kernel, one CTA per (sequence, kv head), finds the
-// kept positions and moves the scores; evict_move_kernel moves the rows.
+// kept positions and moves the scores; evict_move_kernel moves the rows. The
+// second is a programmatic dependent of the first: it is set up while the
+// first runs and waits for it.
 #include "evict.h"
 
-#include "common.cuh"
+#include <type_traits>
+
+#include "tc.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelPer = 4;  // scores per thread of an ordered pass
+constexpr int kBins = 2048;
+constexpr int kListMost = 512;          // candidates that are ranked one against all
+constexpr int kScoresInSmem = 32768;    // scores of a row that are kept in shared memory
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;  // vectors per thread in flight
+constexpr int kMoveUnroll = 8;          // vectors per thread and chunk
 
 __device__ __forceinline__ int evict_len(const EvictParams& p, int s) {
   int L = p.context_lens[s];
@@ -38,38 +43,33 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// Exclusive sum over the block of one value per thread; total gets the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* scratch, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(kFullMask, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // scratch free again
-  if (lane == 31) scratch[warp] = x;
-  __syncthreads();
-  uint32_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSelThreads / 32; ++i) {
-    const uint32_t t = scratch[i];
-    if (i < warp) before += t;
-    total += t;
-  }
-  return before + x - v;
+// A token's rank among the candidates as one number, larger first: its score's
+// key, then the lower position. No two tokens have the same.
+__device__ __forceinline__ uint64_t rank_of(uint32_t key, int t) {
+  return ((uint64_t)key << 32) | (uint32_t)~(uint32_t)t;
 }
 
-// The k-th largest key by radix selection, 11 + 11 + 10 bits, then one ordered
-// pass over the positions: with G keys above the k-th and r = k - G of those
-// equal to it wanted, a kept position's place is (kept above before it) +
-// min(equal before it, r).
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  __shared__ uint32_t hist[2048];
-  __shared__ uint32_t scratch[kSelThreads / 32];
-  __shared__ uint32_t sh_bin, sh_left;
-  const int g = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+// Selection: the k-th largest rank. The interval that holds it is cut into 2048
+// bins of equal width (a power of two), the candidates are counted into them and
+// the bin that holds the k-th is the next interval; the width of the first comes
+// from the smallest and the largest score, so that the counts spread over the
+// bins whatever the scores' scale is (radix digits of the score's bits put most
+// scores of one magnitude into a few counters, whose atomics then queue: 50 us
+// instead of 15 for 256 rows of 16k-32k scores). Once at most kListMost candidates are left
+// each is compared with all others. Then one ordered pass: a warp counts the kept
+// tokens of its stretch by ballots, the counts of the warps before it give its
+// first place.
+template <int NT>
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, int smem_scores) {
+  constexpr int NW = NT / 32;
+  extern __shared__ float sm[];  // smem_scores scores
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint64_t list[kListMost];
+  __shared__ uint32_t warp_sum[NW];
+  __shared__ uint32_t sh_min, sh_max, sh_bin, sh_left, sh_count, sh_n;
+  __shared__ uint64_t sh_rank;
+  grid_launch_dependents();
+  const int g = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = evict_len(p, s);
   const size_t rowi = (size_t)s * p.num_kv_heads + g;
   const float* row = p.scores + rowi * p.score_stride;
@@ -77,160 +77,308 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int32_t* kept = p.kept + rowi * p.budget;
 
   if (L <= p.budget) {
-    for (int t = tid; t < L; t += kSelThreads) {
+    for (int t = tid; t < L; t += NT) {
       kept[t] = t;
       if (out != row) out[t] = row[t];
     }
     return;
   }
-  const int lo = p.sinks, hi = L - p.recent;
-  uint32_t left = (uint32_t)(p.budget - p.sinks - p.recent);  // still to choose, of `prefix`'s keys
-  uint32_t prefix = 0xffffffffu;                              // no key is above or equal to it
+  const int first = p.sinks, last = L - p.recent;  // candidates are [first, last)
+  uint32_t left = (uint32_t)(p.budget - p.sinks - p.recent);
+  const bool whole = L <= smem_scores;
+  if (tid == 0) {
+    sh_min = 0xffffffffu;
+    sh_max = 0u;
+    sh_n = 0u;
+  }
+  for (int i = tid; i < kBins; i += NT) hist[i] = 0u;
+  __syncthreads();
+  uint32_t kmin = 0xffffffffu, kmax = 0u;
+#pragma unroll 8
+  for (int t = tid; t < L; t += NT) {
+    const float x = row[t];
+    if (whole) sm[t] = x;
+    if (t >= first && t < last) {
+      const uint32_t k = score_key(x);
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+    }
+  }
+  const float* from = whole ? sm : row;
+  uint64_t threshold = ~0ull;  // above every rank: no candidate is kept
   if (left > 0) {
-    prefix = 0;
-    uint32_t mask = 0;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digit = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t k = score_key(row[t]);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+    kmin = __reduce_min_sync(kFullMask, kmin);
+    kmax = __reduce_max_sync(kFullMask, kmax);
+    if (lane == 0) {
+      atomicMin(&sh_min, kmin);
+      atomicMax(&sh_max, kmax);
+    }
+    __syncthreads();
+    uint64_t lo = (uint64_t)sh_min << 32, hi = ((uint64_t)sh_max << 32) | 0xffffffffu;
+    for (;;) {
+      const int width = 64 - __clzll((long long)(hi - lo));
+      const int shift = width > 11 ? width - 11 : 0;
+#pragma unroll 4
+      for (int t = first + tid; t < last; t += NT) {
+        const uint64_t r = rank_of(score_key(from[t]), t);
+        if (r >= lo && r <= hi) atomicAdd(&hist[(uint32_t)((r - lo) >> shift)], 1u);
       }
       __syncthreads();
-      // thread i owns bins 2047 - 4 i .. 2044 - 4 i: from the largest down
-      uint32_t c[4], sum = 0, total;
+      // a thread sums the bins kBins - 1 - (tid * P + j), from the largest down
+      constexpr int P = kBins / NT;
+      uint32_t c[P], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] = hist[2047 - 4 * tid - j];
+      for (int j = 0; j < P; ++j) {
+        c[j] = hist[kBins - 1 - (tid * P + j)];
         sum += c[j];
       }
-      uint32_t above = block_scan(sum, scratch, total);
+      uint32_t above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kFullMask, above, o);
+        if (lane >= o) above += y;
+      }
+      if (lane == 31) warp_sum[warp] = above;
+      __syncthreads();
+      above -= sum;
+#pragma unroll
+      for (int i = 0; i < NW; ++i)
+        if (i < warp) above += warp_sum[i];
       if (above < left && left <= above + sum) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < P; ++j) {
           if (above < left && left <= above + c[j]) {
-            sh_bin = 2047u - 4u * tid - j;
+            sh_bin = (uint32_t)(kBins - 1 - (tid * P + j));
             sh_left = left - above;
+            sh_count = c[j];
           }
           above += c[j];
         }
       }
       __syncthreads();
-      prefix |= sh_bin << shift;
-      mask |= digit << shift;
       left = sh_left;
+      lo += (uint64_t)sh_bin << shift;
+      const uint64_t top = lo + (((uint64_t)1 << shift) - 1);
+      hi = top < hi ? top : hi;
+      if (sh_count <= kListMost) break;
+      for (int i = tid; i < kBins; i += NT) hist[i] = 0u;
       __syncthreads();
     }
+    const int n = (int)sh_count;
+#pragma unroll 4
+    for (int t = first + tid; t < last; t += NT) {
+      const uint64_t r = rank_of(score_key(from[t]), t);
+      if (r >= lo && r <= hi) list[atomicAdd(&sh_n, 1u)] = r;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) {
+      const uint64_t r = list[i];
+      uint32_t larger = 0;
+      for (int j = 0; j < n; ++j) larger += list[j] > r;
+      if (larger == left - 1) sh_rank = r;
+    }
+    __syncthreads();
+    threshold = sh_rank;
   }
 
-  uint32_t base_g = 0, base_e = 0;
-  for (int64_t c0 = 0; c0 < L; c0 += kSelThreads * kSelPer) {
-    float v[kSelPer];
-    uint32_t above[kSelPer], equal[kSelPer], cnt = 0;
-    const int64_t t0 = c0 + tid * kSelPer;
-#pragma unroll
-    for (int j = 0; j < kSelPer; ++j) {
-      const int64_t t = t0 + j;
-      above[j] = equal[j] = 0;
-      if (t < L) {
-        v[j] = row[t];
-        const bool mid = t >= lo && t < hi;
-        const uint32_t k = score_key(v[j]);
-        above[j] = !mid || k > prefix;
-        equal[j] = mid && k == prefix;
-        cnt += above[j] + (equal[j] << 16);
-      }
+  // ordered pass, a stretch of smem_scores tokens at a time: its scores are all
+  // in shared memory before a place in it may be overwritten (scores in place)
+  int base = 0;
+  for (int64_t c0 = 0; c0 < L; c0 += smem_scores) {
+    const int m = (int)min((int64_t)smem_scores, L - c0);
+    if (!whole) {
+#pragma unroll 8
+      for (int t = tid; t < m; t += NT) sm[t] = row[c0 + t];
     }
-    uint32_t total;
-    const uint32_t before = block_scan(cnt, scratch, total);  // every score of the chunk has been read
-    uint32_t ng = base_g + (before & 0xffffu), ne = base_e + (before >> 16);
+    __syncthreads();
+    const int per = (m + NT - 1) / NT * 32;  // tokens of a warp
+    const int w0 = min(warp * per, m), w1 = min(w0 + per, m);
+    auto keeps = [&](int i) {
+      const int t = (int)c0 + i;
+      return t < first || t >= last || rank_of(score_key(sm[i]), t) >= threshold;
+    };
+    int count = 0;
+    for (int i = w0; i < w1; i += 32) count += __popc(__ballot_sync(kFullMask, i + lane < w1 && keeps(i + lane)));
+    if (lane == 0) warp_sum[warp] = (uint32_t)count;
+    __syncthreads();
+    int at = base;
 #pragma unroll
-    for (int j = 0; j < kSelPer; ++j) {
-      if (above[j] || (equal[j] && ne < left)) {
-        const uint32_t at = ng + min(ne, left);
-        kept[at] = (int)(t0 + j);
-        out[at] = v[j];
-      }
-      ng += above[j];
-      ne += equal[j];
+    for (int i = 0; i < NW; ++i) {
+      const int v = (int)warp_sum[i];
+      if (i < warp) at += v;
+      base += v;
     }
-    base_g += total & 0xffffu;
-    base_e += total >> 16;
+    for (int i = w0; i < w1; i += 32) {
+      const bool k = i + lane < w1 && keeps(i + lane);
+      const uint32_t b = __ballot_sync(kFullMask, k);
+      if (k) {
+        const int to = at + __popc(b & ((1u << lane) - 1u));
+        kept[to] = (int)c0 + i + lane;
+        out[to] = sm[i + lane];
+      }
+      at += __popc(b);
+    }
+    __syncthreads();
   }
 }
 
-// grid = (K or V and column slice, kv head, sequence). A CTA moves its columns
-// of the kept rows in ascending order, a chunk at a time: a row's new place is
-// never behind its old one, so a chunk's stores, made once its loads and all
-// earlier ones are done, overwrite nothing that is still to be read, and rows
-// may move within the blocks they lie in.
-template <typename V>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int slices) {
-  const int g = blockIdx.y, s = blockIdx.z;
-  const int slice = blockIdx.x >> 1;
-  char* pool = static_cast<char*>((blockIdx.x & 1) ? p.v_cache : p.k_cache);
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// grid.x = (K or V, CTA of the cluster), y = kv head, z = sequence. The cluster
+// (one CTA where there are many (sequence, head) pairs) moves the kept rows of its
+// pool in ascending order, a chunk per CTA at a time. A row's new place is never
+// behind its old one, so the stores of a step, made once the loads of it and of all
+// steps before are done, overwrite nothing that is still to be read: rows may move
+// within the blocks they lie in. The loads of the next step are asked for before
+// the stores of this one (its rows lie behind every place written now), the
+// addresses of the step after it before that.
+//   V: vector of a row, VPR: vectors per row
+template <typename V, int VPR>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int cluster) {
+  constexpr int NT = kMoveThreads, U = kMoveUnroll;
+  constexpr int RC = NT * U / VPR;  // rows of a chunk
+  __shared__ int64_t from[4][RC], to[4][RC];
+  const int g = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
+  const int rank = blockIdx.x % cluster;
+  V* pool = static_cast<V*>(blockIdx.x / cluster ? p.v_cache : p.k_cache);
   const int n = min(evict_len(p, s), p.budget);
-  const int vecs = p.row_bytes / (int)sizeof(V) / slices;  // of a row in this slice
   const int32_t* kept = p.kept + ((size_t)s * p.num_kv_heads + g) * p.budget;
   const int32_t* src_row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
   const int32_t* dst_row = p.dst_block_tables + (size_t)s * p.max_blocks_per_seq;
-  const int64_t items = (int64_t)n * vecs;
-  for (int64_t c0 = 0; c0 < items; c0 += kMoveThreads * kMoveUnroll) {
-    V v[kMoveUnroll];
-    char* to[kMoveUnroll];
-#pragma unroll
-    for (int j = 0; j < kMoveUnroll; ++j) {
-      const int64_t i = c0 + j * kMoveThreads + threadIdx.x;
-      to[j] = nullptr;
-      if (i < items) {
-        const int r = (int)(i / vecs);
-        const int col = (int)(i - (int64_t)r * vecs) + slice * vecs;
+  const int bits = __ffs(p.block_size) - 1, mask = p.block_size - 1;
+  const int steps = ((n + RC - 1) / RC + cluster - 1) / cluster;
+
+  auto find = [&](int step) {  // where the rows of a step's chunk are and go: -1 for none to move
+    const int64_t r0 = ((int64_t)step * cluster + rank) * RC;
+    for (int i = tid; i < RC; i += NT) {
+      const int64_t r = r0 + i;
+      int64_t a = -1, b = -1;
+      if (r < n) {
         const int t = kept[r];
-        const int a = src_row[t / p.block_size], b = dst_row[r / p.block_size];
-        if (a < 0 || a >= p.num_blocks || b < 0 || b >= p.num_blocks) {
+        const int x = __ldg(src_row + (t >> bits)), y = __ldg(dst_row + (r >> bits));
+        if (x < 0 || x >= p.num_blocks || y < 0 || y >= p.num_blocks) {
           set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
         } else {
-          char* from = pool + (((size_t)a * p.num_kv_heads + g) * p.block_size + t % p.block_size) * p.row_bytes +
-                       col * sizeof(V);
-          char* dst = pool + (((size_t)b * p.num_kv_heads + g) * p.block_size + r % p.block_size) * p.row_bytes +
-                      col * sizeof(V);
-          if (from != dst) {
-            v[j] = *reinterpret_cast<const V*>(from);
-            to[j] = dst;
-          }
+          a = ((int64_t)x * p.num_kv_heads + g) * p.block_size + (t & mask);
+          b = ((int64_t)y * p.num_kv_heads + g) * p.block_size + ((int)r & mask);
+          if (a == b) a = b = -1;
         }
       }
+      from[step & 3][i] = a;
+      to[step & 3][i] = b;
     }
-    __syncthreads();
+  };
+  V v[2][U];
+  auto load = [&](int step, V (&x)[U]) {
 #pragma unroll
-    for (int j = 0; j < kMoveUnroll; ++j)
-      if (to[j] != nullptr) *reinterpret_cast<V*>(to[j]) = v[j];
+    for (int j = 0; j < U; ++j) {
+      const int i = j * NT + tid, r = i / VPR;
+      const int64_t a = r < RC ? from[step & 3][r] : -1;
+      if (a >= 0) x[j] = pool[a * VPR + (i - r * VPR)];
+    }
+  };
+  auto store = [&](int step, const V (&x)[U]) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = j * NT + tid, r = i / VPR;
+      const int64_t b = r < RC ? to[step & 3][r] : -1;
+      if (b >= 0) pool[b * VPR + (i - r * VPR)] = x[j];
+    }
+  };
+  auto one = [&](int k, V (&now)[U], V (&next)[U]) {
+    if (k + 1 < steps) load(k + 1, next);
+    if (k + 2 < steps) find(k + 2);
+    if (cluster > 1)
+      cluster_barrier();
+    else
+      __syncthreads();
+    store(k, now);
+  };
+
+  grid_dependency_wait();  // the kept positions
+  if (steps > 0) {
+    find(0);
+    if (steps > 1) find(1);
+    __syncthreads();
+    load(0, v[0]);
+    for (int k = 0; k < steps; k += 2) {
+      one(k, v[0], v[1]);
+      if (k + 1 < steps) one(k + 1, v[1], v[0]);
+    }
   }
-  if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0) p.new_context_lens[s] = n;
+  if (blockIdx.x == 0 && g == 0 && tid == 0) p.new_context_lens[s] = n;
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_with(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster, bool dependent,
+                        Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int NT>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+  const int scores = p.cap < kScoresInSmem ? (p.cap > 0 ? p.cap : 1) : kScoresInSmem;
+  const size_t smem = (size_t)scores * sizeof(float);
+  static int configured[64] = {0};  // per device ordinal
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+    e = cudaFuncSetAttribute(evict_select_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kScoresInSmem * (int)sizeof(float));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+  }
+  return launch_with(evict_select_kernel<NT>, dim3(p.num_kv_heads, p.num_seqs), NT, smem, stream, 1, false, p, scores);
+}
+
+template <typename V, int VPR>
+cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
+  constexpr int64_t rows = kMoveThreads * kMoveUnroll / VPR;
+  const int64_t chains = (int64_t)p.num_seqs * p.num_kv_heads * 2;
+  const int64_t chunks = ((p.budget < p.cap ? p.budget : p.cap) + rows - 1) / rows;
+  // few (sequence, head, pool) triples: clusters of up to 8 CTAs share one, while
+  // that gives each SM no more than two CTAs and each CTA a chunk
+  int cluster = 1;
+  while (cluster < 8 && chains * cluster * 2 <= 304 && cluster < chunks) cluster *= 2;
+  return launch_with(evict_move_kernel<V, VPR>, dim3(2 * cluster, p.num_kv_heads, p.num_seqs), kMoveThreads, 0, stream,
+                     cluster, true, p, cluster);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-  evict_select_kernel<<<dim3(p.num_kv_heads, p.num_seqs), kSelThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = p.cap > 8192 ? launch_select<1024>(p, stream) : launch_select<512>(p, stream);
   if (e != cudaSuccess) return e;
-  // few (sequence, head) pairs: the columns of a row are cut into slices of at
-  // least 64 bytes
-  int slices = 1;
-  const int64_t ctas = (int64_t)p.num_seqs * p.num_kv_heads * 2;
-  while (ctas * slices < 304 && p.row_bytes % (slices * 2) == 0 && p.row_bytes / (slices * 2) >= 64) slices *= 2;
-  const dim3 grid(2 * slices, p.num_kv_heads, p.num_seqs);
-  if (p.row_bytes % 16 == 0)
-    evict_move_kernel<uint4><<<grid, kMoveThreads, 0, stream>>>(p, slices);
-  else if (p.row_bytes % 8 == 0)
-    evict_move_kernel<uint2><<<grid, kMoveThreads, 0, stream>>>(p, slices);
-  else
-    evict_move_kernel<uint32_t><<<grid, kMoveThreads, 0, stream>>>(p, slices);
-  return cudaGetLastError();
+  switch (p.row_bytes) {
+    case 36: return launch_move<uint32_t, 9>(p, stream);
+    case 64: return launch_move<uint4, 4>(p, stream);
+    case 72: return launch_move<uint2, 9>(p, stream);
+    case 128: return launch_move<uint4, 8>(p, stream);
+    case 256: return launch_move<uint4, 16>(p, stream);
+    case 512: return launch_move<uint4, 32>(p, stream);
+    default: return cudaErrorNotSupported;
+  }
 }
 
 }  // namespace pkv

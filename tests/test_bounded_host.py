@@ -25,7 +25,7 @@ def caller(fn, **defaults):
     return call
 
 
-BIG = (1 << 31) - 256
+
 
 
 def test_decode_window_refusals(pkv):
@@ -96,7 +96,7 @@ def test_evict_refusals(pkv):
 
 def test_workspace_sizes(pkv):
     a = lambda x: -(-x // 256) * 256
-    base = a(4 * 8 * 4) + a(2048 * 8 * 8) + 2048 * 8 * 128 * 4
+    base = a(4 * 8 * 4) + a(32768 * 8) + 32768 * 128 * 4
     assert pkv.decode_window_workspace_bytes(4, 8, 2, 128) == base
     assert pkv.decode_scores_workspace_bytes(4, 8, 2, 128, 1001) == base + a(4 * 8 * 8) + 4 * 8 * 1008 * 4
     assert pkv.decode_scores_workspace_bytes(65535, 128, 8, 128, 1 << 20) > 1 << 42  # no 32-bit overflow
