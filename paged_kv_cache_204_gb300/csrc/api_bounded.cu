@@ -8,7 +8,7 @@
 #include "decode_window.cuh"
 #include "evict.h"
 #include "pkv.h"
-#include "prefill.cuh"
+#include "prefill_window.cuh"
 
 namespace {
 
@@ -250,19 +250,18 @@ pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const vo
                  block_size, num_seqs, max_blocks_per_seq, num_blocks, 0, dtype, dev_err);
   if (st != PKV_OK || num_seqs == 0 || max_query_len == 0) return st;
   if (!query_start || !aligned(query_start, 4)) return PKV_ERR_INVALID_ARG;
-  if ((int64_t)num_seqs * num_heads > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  const pkv::PrefillLauncher launch = pkv::prefill_window_launcher(dtype == PKV_BF16 ? 1 : 0, head_dim);
+  const pkv::PrefillWindowLauncher launch = pkv::prefill_window_launcher(dtype == PKV_BF16 ? 1 : 0, head_dim);
   if (!launch) return PKV_ERR_UNSUPPORTED;
   const int longest = max_blocks_per_seq * block_size;  // fits: checked above
-  pkv::PrefillParams p{};
+  pkv::PrefillWindowParams p{};
   p.out = out;
   p.q = q;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.query_start = query_start;
   p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+  p.window = std::min(window, longest);
+  p.sinks = std::min(num_sinks, longest);
   p.num_seqs = num_seqs;
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
@@ -272,9 +271,7 @@ pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const vo
   p.num_blocks = num_blocks;
   p.dev_err = dev_err;
   p.wait_limit_ns = pkv_get_wait_timeout_ns();
-  p.window = std::min(window, longest);
-  p.sinks = std::min(num_sinks, longest);
-  return launch_status(launch(p, max_query_len, reinterpret_cast<cudaStream_t>(stream)));
+  return launch_status(launch(p, k_cache, v_cache, max_query_len, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores, int64_t score_stride,

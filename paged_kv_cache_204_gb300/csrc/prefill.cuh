@@ -19,12 +19,6 @@
 // the thread that owns that row's tensor-memory lane. For bfloat16 data P
 // is fed as a high and a low 16-bit part (two MMAs) so that the
 // probabilities keep ~16 significant bits; binary16 P (11 bits) goes as one.
-//
-// Windowed form (kWin): query position P sees the tokens t <= P with t < sinks
-// or t > P - window. A CTA walks only the tiles that hold a token one of its
-// queries sees (those of the sinks, then those from the first query's window
-// on); cache blocks that none of its queries sees are not read, so their
-// table entries may name blocks that were given back.
 #pragma once
 
 #include <type_traits>
@@ -53,7 +47,6 @@ struct PrefillParams {
   int num_seqs, num_heads, num_kv_heads, group, block_size, max_blocks_per_seq, num_blocks;
   int32_t* dev_err;
   uint64_t wait_limit_ns;  // limit of every wait on another role's progress
-  int window, sinks;       // kWin only: window >= 1, sinks >= 0
 };
 
 // 16-bit packing of two fp32 values (round to nearest) and its exact inverse.
@@ -153,7 +146,7 @@ struct PrefillShape {
 //            when it grows by more than kPfRescaleLog2, which leaves every
 //            P <= 2^kPfRescaleLog2 and the result exact (O and the row sum
 //            use the same base).
-template <typename T, int D, bool kWin = false>
+template <typename T, int D>
 __global__ void __launch_bounds__(kPfThreads, 2)
     pa_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const PrefillParams p) {
@@ -194,17 +187,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
   const int rows = min(kPfRows, n - row0);
   const int first_pos = L - n + row0;   // position of the tile's first query
   const int kv_end = first_pos + rows;  // tokens the tile's queries can see
-  // tiles the CTA walks: all up to kv_end, or (kWin) tiles [0, tfirst) of the
-  // sinks and [tfrom, end) of the windows; tile_at(j) is the j-th of them
-  const int tend = (kv_end + kPfTokens - 1) / kPfTokens;
-  int tfirst = 0, tfrom = 0, wlo = 0;  // wlo: first token in the first query's window
-  if constexpr (kWin) {
-    wlo = first_pos >= p.window ? first_pos - p.window + 1 : 0;
-    tfirst = (min(p.sinks, kv_end) + kPfTokens - 1) / kPfTokens;
-    tfrom = max(wlo / kPfTokens, tfirst);
-  }
-  const int ntiles = tfirst + (tend - tfrom);
-  auto tile_at = [&](int j) { return !kWin || j < tfirst ? j : j - tfirst + tfrom; };
+  const int ntiles = (kv_end + kPfTokens - 1) / kPfTokens;
   const int kvh = h / p.group;
   const int bs = p.block_size;
 
@@ -239,24 +222,17 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     const int oob_row = p.num_blocks * p.num_kv_heads * bs;  // first row past the pool: reads zeros
     const uint32_t box_bytes = (uint32_t)bs * 128u;
     int* ring = reinterpret_cast<int*>(sm + S::kRingOff);    // [8 tiles][8 blocks]
-    auto nblk_of = [&](int j) { return min(per_tile, (kv_end - tile_at(j) * kPfTokens + bs - 1) / bs); };
-    // whether a query of the CTA sees a token of block b of tile t
-    auto seen = [&](int t, int b) {
-      const int k = tile_at(t) * kPfTokens + b * bs;
-      return !kWin || k < p.sinks || k + bs > wlo;
-    };
+    auto nblk_of = [&](int j) { return min(per_tile, (kv_end - j * kPfTokens + bs - 1) / bs); };
     const int gt = lane >> 3, gb = lane & 7;  // this lane's tile in a group of four, block in the tile
     auto fetch_group = [&](int g) -> int {    // issues the load only
       const int t = 4 * g + gt;
-      return (t < ntiles && gb < nblk_of(t) && seen(t, gb)) ? __ldg(bt + tile_at(t) * per_tile + gb) : 0;
+      return (t < ntiles && gb < nblk_of(t)) ? __ldg(bt + t * per_tile + gb) : 0;
     };
     auto store_group = [&](int g, int id) {
       const int t = 4 * g + gt;
       if (t < ntiles && gb < nblk_of(t)) {
         int y = oob_row;
-        if (!seen(t, gb)) {
-          // reads as zeros
-        } else if (id >= 0 && id < p.num_blocks)
+        if (id >= 0 && id < p.num_blocks)
           y = (id * p.num_kv_heads + kvh) * bs;
         else
           set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
@@ -433,8 +409,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     for (int j = 0; j < ntiles; ++j) {
       const int b = j & 1;
       const uint32_t par = (j >> 1) & 1;
-      const int k0 = tile_at(j) * kPfTokens;   // first token of the tile
-      const int t0 = k0 + 32 * ch;             // first token of this thread's half
+      const int t0 = j * kPfTokens + 32 * ch;  // first token of this thread's half
       float x[32];
       float pm = -INFINITY;
       // every wait is made warp-uniform before the warp-collective
@@ -453,15 +428,6 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (i >= vis) x[i] = -INFINITY;
-        }
-        if constexpr (kWin) {
-          const int before = pos - p.window + 1 - t0;  // tokens of this half before the row's window
-          if (before > 0) {
-            const int kept = p.sinks - t0;  // of those, the sinks stay
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < before && i >= kept) x[i] = -INFINITY;
-          }
         }
         float m8[8];  // eight independent partial maxima, then a tree
 #pragma unroll
@@ -523,26 +489,14 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       tmem_st16(tbase + lane_base + 64 * b + 16 * ch, hi);
       if constexpr (kPParts == 2) tmem_st16(tbase + lane_base + 64 * b + 32 + 16 * ch, lo);
       tmem_wait_st();
-      // kWin: rows [hide0, hide1) of the tile lie behind the sinks and before
-      // every window of the CTA
-      int hide0 = 0, hide1 = 0;
-      if constexpr (kWin) {
-        hide0 = max(p.sinks - k0, 0);
-        hide1 = min(wlo - k0, kPfTokens);
-      }
-      if ((j == ntiles - 1 && kv_end < k0 + kPfTokens) || hide0 < hide1) {
+      if (j == ntiles - 1 && kv_end < j * kPfTokens + kPfTokens) {
         // V rows past the context may hold anything (a NaN would survive a
         // zero probability): zero them once the tile has landed
         if (__all_sync(kFullMask, mbar_wait_bounded(&full_v[b], par, p.wait_limit_ns))) {
-          const int z0 = kv_end - k0, per_row = S::kBlocksD * 8;
+          const int z0 = kv_end - j * kPfTokens, per_row = S::kBlocksD * 8;
           unsigned char* vd = sm + S::kVOff + b * S::kTileBytes;
           for (int i = tid; i < (kPfTokens - z0) * per_row; i += kPfSoftThreads) {
             const int row = z0 + i / per_row, rem = i % per_row;
-            *reinterpret_cast<uint4*>(vd + (rem >> 3) * S::kColBlock + row * 128 + (rem & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          for (int i = tid; i < (hide1 - hide0) * per_row; i += kPfSoftThreads) {
-            const int row = hide0 + i / per_row, rem = i % per_row;
             *reinterpret_cast<uint4*>(vd + (rem >> 3) * S::kColBlock + row * 128 + (rem & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
@@ -602,7 +556,7 @@ cudaError_t encode_pool_map(CUtensorMap* map, const void* base, const PrefillPar
                               std::is_same<T, __nv_bfloat16>::value);
 }
 
-template <typename T, int D, bool kWin = false>
+template <typename T, int D>
 cudaError_t launch_pa_prefill(const PrefillParams& p, int max_query_len, cudaStream_t stream) {
   using S = PrefillShape<D>;
   // the TMA row coordinate (and one box past the pool) must fit in int32
@@ -614,7 +568,7 @@ cudaError_t launch_pa_prefill(const PrefillParams& p, int max_query_len, cudaStr
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
-    e = cudaFuncSetAttribute(pa_prefill_kernel<T, D, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+    e = cudaFuncSetAttribute(pa_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
   }
@@ -625,12 +579,11 @@ cudaError_t launch_pa_prefill(const PrefillParams& p, int max_query_len, cudaStr
   if (e != cudaSuccess) return e;
   if ((max_query_len + kPfRows - 1) / kPfRows > 65535) return cudaErrorNotSupported;
   const dim3 grid(p.num_seqs * p.num_heads, (max_query_len + kPfRows - 1) / kPfRows);
-  pa_prefill_kernel<T, D, kWin><<<grid, kPfThreads, S::kSmemBytes, stream>>>(kmap, vmap, p);
+  pa_prefill_kernel<T, D><<<grid, kPfThreads, S::kSmemBytes, stream>>>(kmap, vmap, p);
   return cudaGetLastError();
 }
 
 using PrefillLauncher = cudaError_t (*)(const PrefillParams&, int, cudaStream_t);
 PrefillLauncher prefill_launcher(int is_bf16, int head_dim);
-PrefillLauncher prefill_window_launcher(int is_bf16, int head_dim);  // prefill_window.cu
 
 }  // namespace pkv

@@ -1,0 +1,806 @@
+// Paged prefill over the first tokens and a sliding window (sm_103a): the query at
+// position P of its sequence sees the tokens t <= P with t < sinks or
+// t > P - window.
+//
+// Work: the queries of a sequence against one kv head are n x group rows, row
+// m = i * group + j for new token i and the kv head's j-th query head, so that a
+// tile of 128 rows holds few tokens and K/V are read once for a whole group. One
+// CTA takes two such tiles, A and B, and walks the K/V tiles of 128 tokens that one
+// of their queries sees: those of the sinks, then those from the first query's
+// window on. On the fifth-generation tensor cores S = Q K^T and O += P V accumulate
+// in fp32 in tensor memory; a softmax warpgroup of its own serves each of A and B, a
+// row to a thread, so that one tile's exponentials run under the other's MMAs. A CTA
+// stays on its SM and takes one pair of query tiles after another; every role runs
+// ahead into the next pair as far as the barriers let it, so that the start of one
+// pair lies under the end of another.
+// Where there are few pairs, a cluster shares one: each of its CTAs walks a part
+// of the K/V tiles, and the parts are joined through the cluster's shared memory
+// (log-sum-exp).
+// P enters its product as one 16-bit part: its rounding, 2^-9 (bfloat16) or 2^-12 of
+// each weight at most and independent from weight to weight, adds less to a row's output than
+// the rounding of the output itself does, whose largest is the same.
+#pragma once
+
+#include <type_traits>
+
+#include "tc.cuh"
+
+namespace pkv {
+
+constexpr int kPwRows = 128;     // rows of a query tile = tensor-memory lanes
+constexpr int kPwTokens = 128;   // tokens of a K/V tile
+constexpr int kPwStages = 4;     // K and V tiles in shared memory, K and V in turn
+constexpr int kPwSoft = 256;     // 2 softmax warpgroups
+constexpr int kPwThreads = kPwSoft + 96;  // + MMA warp, TMA warp, query-loading and clearing warp
+constexpr uint32_t kPwTmemCols = 512;     // S of A and B (128 columns each), O of A and B
+constexpr float kPwRescaleLog2 = 8.f;     // base of the running max moves only when it grows by more
+constexpr int kPwMaxCluster = 4;
+
+struct PrefillWindowParams {
+  void* out;
+  const void* q;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  float scale_log2;  // scale * log2(e)
+  int window, sinks;  // window >= 1, sinks >= 0, no larger than the longest table
+  int num_seqs, num_heads, num_kv_heads, group, block_size, max_blocks_per_seq, num_blocks;
+  int pairs;    // of the longest sequence, per kv head
+  int cluster;  // CTAs that share a pair of query tiles
+  int32_t* dev_err;
+  uint64_t wait_limit_ns;  // limit of every wait on another role's progress
+};
+
+template <typename T>
+struct PwPack;
+template <>
+struct PwPack<__half> {
+  __device__ __forceinline__ static uint32_t pack(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+  }
+};
+template <>
+struct PwPack<__nv_bfloat16> {
+  __device__ __forceinline__ static uint32_t pack(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+  }
+};
+
+// 2^x by the hardware's approximate exponential (relative error about 2^-22, -inf
+// -> +0); what it gives is rounded to 16 bits afterwards.
+__device__ __forceinline__ float pw_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared memory of a CTA, from a 1024-byte aligned base: Q of A and B
+// ([D / 64 column blocks][128 rows][128 bytes] each), then the K/V stages (the same
+// with tokens as rows), barriers, tensor-memory address. The join of a cluster
+// reuses it from the start: O [2][128][D] in fp32, then (m, l).
+template <int D>
+struct PwShape {
+  static constexpr int kCB = D / 64;
+  static constexpr int kColBlock = 128 * 128;
+  static constexpr int kTile = kCB * kColBlock;  // a Q, K or V tile
+  static constexpr int kStageOff = 2 * kTile;
+  static constexpr int kBarOff = kStageOff + kPwStages * kTile;
+  static constexpr int kSlotOff = kBarOff + 24 * 8;
+  static constexpr int kUsed = kSlotOff + 16 + 1024;  // + alignment slack
+  // more than half of an SM's, so that one CTA has its tensor memory to itself
+  static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static constexpr int kJoinMl = 2 * kPwRows * D * 4;
+  static_assert(kJoinMl + 2 * kPwRows * 8 <= kBarOff, "room for the join");
+};
+
+__device__ __forceinline__ uint32_t pw_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void pw_cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of `saddr` in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t pw_remote(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 pw_remote_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 pw_remote_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// What a CTA walks: K/V tiles [0, first) hold the sinks, [from, end) the windows; its
+// part is the j-th of these for j in [j0, j1).
+struct PwWalk {
+  int first, from, j0, j1;
+  __device__ __forceinline__ int tile(int j) const { return j < first ? j : j - first + from; }
+};
+
+// The tokens that the queries of one query tile see: [0, min(sinks, end)) and [lo, end).
+struct PwSpan {
+  int lo, end;
+  __device__ __forceinline__ bool sees(int k0, int sinks) const {  // one of [k0, k0 + kPwTokens)
+    return k0 < end && (k0 < sinks || k0 + kPwTokens > lo);
+  }
+};
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pw_pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 pw_unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t pw_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pw_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The MMAs of kind::f16 with a descriptor's words apart (see mma_ss, mma_ts).
+__device__ __forceinline__ void pw_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void pw_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The lowest n bits set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+__device__ __forceinline__ float pw_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A pair of query tiles of one sequence and kv head, and the K/V tiles this CTA
+// walks for it.
+struct PwItem {
+  int s, kvh, L, q0, n, row0, rows;  // rows: query rows of the kv head
+  int active_a, active_b;            // rows of A and B
+  PwSpan span_a, span_b;
+  int kv_end, wlo;  // past the last token that a query sees; first token in the first query's window
+  PwWalk walk;
+
+  // The item with index `item`; false when it has no rows (or its lengths are wrong).
+  __device__ __forceinline__ bool load(const PrefillWindowParams& p, int item, uint32_t rank, bool report) {
+    const int columns = p.num_seqs * p.num_kv_heads;
+    const int pair = p.pairs - 1 - item / columns;  // later queries first: theirs are the longest walks
+    const int column = item % columns;
+    s = column / p.num_kv_heads;
+    kvh = column % p.num_kv_heads;
+    L = __ldg(p.context_lens + s);
+    q0 = __ldg(p.query_start + s);
+    n = __ldg(p.query_start + s + 1) - q0;
+    if (L < 0 || L > p.max_blocks_per_seq * p.block_size || n < 0 || n > L) {
+      if (report) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
+      return false;
+    }
+    rows = (int)min((int64_t)n * p.group, (int64_t)p.pairs * 2 * kPwRows);  // the launch covers no more
+    row0 = pair * 2 * kPwRows;
+    if (row0 >= rows) return false;
+    auto place = [&](int a, int& active, PwSpan& span) {
+      active = max(min(rows - a, kPwRows), 0);
+      const int t0 = a / p.group, t1 = (a + max(active, 1) - 1) / p.group;
+      const int p0 = L - n + t0;
+      span.lo = p0 >= p.window ? p0 - p.window + 1 : 0;
+      span.end = active > 0 ? L - n + t1 + 1 : 0;
+    };
+    place(row0, active_a, span_a);
+    place(row0 + kPwRows, active_b, span_b);
+    kv_end = max(span_a.end, span_b.end);
+    wlo = span_a.lo;
+    const int tend = (kv_end + kPwTokens - 1) / kPwTokens;
+    walk.first = (min(p.sinks, kv_end) + kPwTokens - 1) / kPwTokens;
+    walk.from = max(wlo / kPwTokens, walk.first);
+    const int all = walk.first + tend - walk.from;
+    walk.j0 = (int)((int64_t)all * rank / p.cluster);
+    walk.j1 = (int)((int64_t)all * (rank + 1) / p.cluster);
+    return true;
+  }
+  __device__ __forceinline__ PwSpan span(int x) const { return x ? span_b : span_a; }
+  // Rows [hide0, hide1) and from `tail` on of the K/V tile at k0 are seen by no query.
+  __device__ __forceinline__ bool hidden(const PrefillWindowParams& p, int k0, int& hide0, int& hide1,
+                                         int& tail) const {
+    hide0 = max(p.sinks - k0, 0);
+    hide1 = min(wlo - k0, kPwTokens);
+    tail = min(kv_end - k0, kPwTokens);
+    return hide0 < hide1 || tail < kPwTokens;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPwThreads, 1)
+    pa_prefill_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                             const PrefillWindowParams p) {
+  using S = PwShape<D>;
+  using P16 = PwPack<T>;
+  constexpr int kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+  constexpr int CB = S::kCB;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // Every barrier's phases follow one another in the order of the work (K/V tiles, or
+  // pairs of query tiles), and nobody who waits for a phase can fall two behind.
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
+  // The fills of the K/V stages are counted through: K and V of a tile in turn, fill f
+  // into stage f % 4. The MMAs hand back a V tile and the K tile behind it at once:
+  // fills 2 j - 1 and 2 j, hand-back j.
+  uint64_t* kv_full = bars;        // [4] fill landed
+  uint64_t* kv_empty = bars + 4;   // [2] hand-back j, of barrier j % 2
+  uint64_t* s_full = bars + 6;     // [A, B] S computed
+  uint64_t* p_half = bars + 8;     // [A, B] P of the first 64 tokens written (one arrival per softmax warp)
+  uint64_t* p_full = bars + 10;    // [A, B] all of P written
+  uint64_t* q_full = bars + 12;    // [A, B] query rows in place (one arrival per loading thread)
+  uint64_t* q_empty = bars + 14;   // [A, B] the pair's last S computed
+  uint64_t* o_full = bars + 16;    // [A, B] the pair's last O computed
+  uint64_t* to_clear = bars + 18;  // a V tile with rows that no query sees has landed 
+  uint64_t* cleared = bars + 19;   // those rows are set to zero
+  uint64_t* drained = bars + 20;   // every MMA of the CTA done
+  uint32_t* slot = reinterpret_cast<uint32_t*>(sm + S::kSlotOff);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cluster = p.cluster;
+  const uint32_t rank = cluster > 1 ? pw_cluster_rank() : 0u;
+  const int items = p.pairs * p.num_seqs * p.num_kv_heads;
+  const int item0 = blockIdx.x / cluster, step = gridDim.x / cluster;
+
+  // ---- set-up: barriers, tensor memory ----------------------------------------
+  if (tid == 0) {
+    for (int i = 0; i < 21; ++i) mbar_init(&bars[i], i >= 8 && i < 12 ? 4 : (i == 12 || i == 13 ? 32 : 1));
+    mbar_init_fence();
+  }
+  if (warp == 8) tmem_alloc(slot, kPwTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *slot;
+  bool bad = false;  // a wait ran out
+
+  if (warp == 9) {
+    // ---- TMA: K and V tiles, box by box (one box: 64 head dims of one cache block of
+    // the kv head); lane b holds the row of block b of the next tile in the pool
+    PwItem it;
+    const int per_tile = kPwTokens / p.block_size;  // <= 16 blocks
+    const int bs = p.block_size, bits = __ffs(bs) - 1;
+    const int zero_row = p.num_blocks * p.num_kv_heads * bs;  // first row past the pool: reads zeros
+    const uint32_t box_bytes = (uint32_t)bs * 128u;
+    uint32_t used = 0;  // stages filled so far
+    for (int item = item0; item < items && !bad; item += step) {
+      if (!it.load(p, item, rank, false)) continue;
+      const int32_t* bt = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
+      auto blocks_of = [&](int k0) { return min(per_tile, (it.kv_end - k0 + bs - 1) >> bits); };
+      auto seen = [&](int k) { return k < p.sinks || k + bs > it.wlo; };  // the block at token k, by a query
+      auto fetch = [&](int j) {  // issues the load only
+        if (j >= it.walk.j1) return -1;
+        const int k0 = it.walk.tile(j) * kPwTokens, k = k0 + lane * bs;
+        return lane < blocks_of(k0) && seen(k) ? __ldg(bt + (k >> bits)) : -1;
+      };
+      int id = fetch(it.walk.j0);
+      for (int j = it.walk.j0; j < it.walk.j1 && !bad; ++j) {
+        const int k0 = it.walk.tile(j) * kPwTokens, nblk = blocks_of(k0);
+        int y = zero_row;
+        if (lane < nblk && seen(k0 + lane * bs)) {
+          if (id >= 0 && id < p.num_blocks)
+            y = (id * p.num_kv_heads + it.kvh) * bs;
+          else
+            set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+        }
+        id = fetch(j + 1);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          // the stage of a V tile, fill f, was that of fill f - 4: hand-back (f - 3) / 2;
+          // that of the next K tile comes back with it
+          const uint32_t st = used % kPwStages, back = (used - 3) / 2;
+          if (v == 1 && used > kPwStages - 2 &&
+              !__all_sync(kFullMask, mbar_wait_bounded(&kv_empty[back & 1], (back >> 1) & 1, p.wait_limit_ns))) {
+            bad = true;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(nblk * CB) * box_bytes);
+          __syncwarp();
+          const int b = lane / CB, cb = lane % CB;
+          const int row = __shfl_sync(kFullMask, y, b);
+          if (lane < nblk * CB)
+            tma_load_2d(sm + S::kStageOff + st * S::kTile + cb * S::kColBlock + b * bs * 128, v ? &vmap : &kmap,
+                        cb * 64, row, &kv_full[st]);
+          ++used;
+        }
+      }
+    }
+    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    // every box must land, and the last hand-backs be over, before the CTA can leave
+    // (earlier phases are known to be over, since a later fill waited for them)
+    if (lane == 0) {
+      for (uint32_t st = 0; st < kPwStages; ++st)
+        if (used > st) {
+          const uint32_t last = st + kPwStages * ((used - 1 - st) / kPwStages);
+          mbar_wait_bounded(&kv_full[st], (last / kPwStages) & 1, kDrainLimitNs);
+        }
+      if (!bad && used > 0)
+        for (uint32_t back = used >= 4 ? used / 2 - 1 : 0; back <= used / 2; ++back)
+          mbar_wait_bounded(&kv_empty[back & 1], (back >> 1) & 1, p.wait_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---- MMA issue -----------------------------------------------------------------
+    // Order: S_A(0), S_B(0), then per tile O_A += P_A V, S_A of the next tile, and the
+    // same for B: in turn, so that A's softmax runs under B's MMAs and the other way round
+    // (with a warp for each of A and B both fell into step and the tensor pipe idled
+    // under both softmaxes). MMAs complete in that order, so S may take the place of a P that the
+    // MMA before it reads, and "S done" says that O holds every earlier tile.
+    // The whole warp walks and waits, one elected lane issues; what a step needs to know
+    // is worked out before its wait, since the pipe holds only a few MMAs ahead.
+    constexpr uint32_t id_s = mma_idesc_f16(kPwRows, kPwTokens, kBf16, 0);
+    constexpr uint32_t id_o = mma_idesc_f16(kPwRows, D, kBf16, 1);
+    const uint32_t tb = __shfl_sync(kFullMask, tbase, 0);
+    const uint32_t sb = __shfl_sync(kFullMask, smem_u32(sm), 0);
+    // of a descriptor only the start address in its low word moves (shared addresses stay
+    // below 256 KB, so the sums never carry out of the field)
+    const uint32_t qd = (uint32_t)smem_desc_sw128(sb, 16, 1024);
+    const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
+    const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, S::kColBlock, 1024);
+    const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
+    PwItem it;
+    uint32_t fill = 0, clears = 0, nth = 0;  // first fill of the pair, cleared tiles, pairs so far
+    uint32_t done[2] = {0, 0};                // P of A and B so far
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = __all_sync(kFullMask, mbar_wait_bounded(bar, parity, p.wait_limit_ns));
+      tc_fence_after();
+      return ok;
+    };
+    auto full = [&](uint32_t f) { return wait(&kv_full[f % kPwStages], (f / kPwStages) & 1); };
+    // within one elected region: S into the place of x's scores ...
+    auto mmas_s = [&](int x, uint32_t f, bool last) {
+      const uint32_t kb = kd + ((f % kPwStages) * S::kTile >> 4), qb = qd + (x * S::kTile >> 4);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
+        pw_mma_ss(tb + 128 * x, qb + off, kb + off, hi, id_s, ks > 0);
+      }
+      mma_commit(&s_full[x]);
+      if (last && cluster == 1) mma_commit(&q_empty[x]);
+    };
+    // ... and O += P V over the first (h 0) or last 64 tokens
+    auto mmas_o = [&](int x, uint32_t f, int h, bool first) {
+      const uint32_t vb = vd + ((f % kPwStages) * S::kTile >> 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int ks = 4 * h + k;
+        pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 8 * ks, vb + (ks * 2048 >> 4), hi, id_o,
+                  (ks > 0 || !first) ? 1u : 0u);
+      }
+    };
+    for (int item = item0; item < items && !bad; item += step) {
+      if (!it.load(p, item, rank, false)) continue;
+      const int tiles = it.walk.j1 - it.walk.j0;
+      int last[2];  // the last tile that A and B see, as a token position
+#pragma unroll
+      for (int x = 0; x < 2; ++x) last[x] = (it.span(x).end - 1) & ~(kPwTokens - 1);
+      bool opened[2] = {false, false}, sees[2] = {false, false};  // O holds something; the tile at hand is seen
+      // rows that no S of this part needs are in place before the pair ends all the same
+      bad = !wait(&q_full[0], nth & 1);
+      if (tiles > 0 && !bad) {
+        const int k0 = it.walk.tile(it.walk.j0) * kPwTokens;
+        sees[0] = it.span_a.sees(k0, p.sinks);
+        sees[1] = it.span_b.sees(k0, p.sinks);
+        bad = !full(fill);
+        if (!bad && sees[0] && elect_one()) mmas_s(0, fill, k0 == last[0]);
+        __syncwarp();
+        bad = bad || !wait(&q_full[1], nth & 1);
+        if (!bad && elect_one()) {
+          if (sees[1]) mmas_s(1, fill, k0 == last[1]);
+          mma_commit(&kv_empty[(fill / 2) & 1]);  // with the last V of the pair before
+        }
+        __syncwarp();
+      } else {
+        bad = bad || !wait(&q_full[1], nth & 1);
+      }
+      for (int i = 0; i < tiles && !bad; ++i) {
+        const uint32_t fv = fill + 2 * i + 1, fk = fv + 1;  // this V and the next K
+        const int k0 = it.walk.tile(it.walk.j0 + i) * kPwTokens;
+        const bool more = i + 1 < tiles;
+        const int k1 = more ? it.walk.tile(it.walk.j0 + i + 1) * kPwTokens : 0;
+        bool next[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) next[x] = more && it.span(x).sees(k1, p.sinks);
+        int h0, h1, tl;
+        bad = !full(fv) || (more && !full(fk));
+        if (!bad && it.hidden(p, k0, h0, h1, tl)) {
+          if (lane == 0) mbar_arrive(to_clear);
+          __syncwarp();
+          bad = !wait(cleared, clears++ & 1);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!bad && sees[x]) {
+            // (a pair's first P comes from warps that have read the O of the pair before)
+            bad = !wait(&p_half[x], done[x] & 1);
+            if (!bad && elect_one()) mmas_o(x, fv, 0, !opened[x]);
+            __syncwarp();
+            opened[x] = true;
+            bad = bad || !wait(&p_full[x], done[x] & 1);
+            ++done[x];
+          }
+          if (!bad && elect_one()) {
+            if (sees[x]) mmas_o(x, fv, 1, false);
+            if (next[x]) mmas_s(x, fk, k1 == last[x]);
+            if (x == 1 && more) mma_commit(&kv_empty[(fk / 2) & 1]);
+          }
+          __syncwarp();
+          sees[x] = next[x];
+        }
+      }
+      if (!bad && elect_one()) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (cluster == 1 && it.span(x).end == 0) mma_commit(&q_empty[x]);
+          mma_commit(&o_full[x]);
+        }
+      }
+      __syncwarp();
+      fill += 2 * tiles;
+      ++nth;
+    }
+    if (elect_one()) {
+      if (!bad && fill > 0) mma_commit(&kv_empty[(fill / 2) & 1]);  // the last V
+      // nothing may be torn down before the last MMA, after a timeout neither
+      mma_commit(drained);
+    }
+    __syncwarp();
+    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    mbar_wait_bounded(drained, 0, kDrainLimitNs);
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---- query rows, in 16-byte chunks, a row by two lanes; then the pair's V tiles that
+    // have hidden rows
+    constexpr int CPR = D / 8;
+    PwItem it;
+    const T* q = static_cast<const T*>(p.q);
+    uint32_t nth = 0, fill = 0, clears = 0;  // pairs so far, first fill of the pair, cleared tiles so far
+    for (int item = item0; item < items && !bad; item += step) {
+      if (!it.load(p, item, rank, false)) continue;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (nth > 0 && !__all_sync(kFullMask, mbar_wait_bounded(&q_empty[x], (nth + 1) & 1, p.wait_limit_ns))) {
+          bad = true;
+          break;
+        }
+        const int active = max(min(it.rows - it.row0 - x * kPwRows, kPwRows), 0);
+#pragma unroll
+        for (int rr = lane >> 1; rr < kPwRows; rr += 16) {
+          if (active == 0) break;
+          const bool in = rr < active;
+          const int g = it.row0 + x * kPwRows + rr, t = in ? g / p.group : 0, j = in ? g - t * p.group : 0;
+          const T* src = q + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D;
+          const uint32_t to = smem_u32(sm + x * S::kTile) + rr * 128, bytes = in ? 16 : 0;
+#pragma unroll
+          for (int c2 = 0; c2 < CPR / 2; ++c2) {
+            const int c = 2 * c2 + (lane & 1);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             to + (c >> 3) * S::kColBlock + (((c & 7) ^ (rr & 7)) << 4)),
+                         "l"(src + c * 8), "r"(bytes)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      if (bad) break;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(&q_full[0]);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(&q_full[1]);
+      ++nth;
+      // rows of V tiles that no query sees may hold anything (a NaN would survive a zero
+      // weight): zeros instead, once a tile has landed
+      const int tiles = it.walk.j1 - it.walk.j0;
+      for (int i = 0; i < tiles; ++i) {
+        int h0, h1, tail;
+        if (!it.hidden(p, it.walk.tile(it.walk.j0 + i) * kPwTokens, h0, h1, tail)) continue;
+        if (!__all_sync(kFullMask, mbar_wait_bounded(to_clear, clears & 1, p.wait_limit_ns))) {
+          bad = true;
+          break;
+        }
+        unsigned char* v = sm + S::kStageOff + (fill + 2 * i + 1) % kPwStages * S::kTile;
+        const int before = max(h1 - h0, 0), count = before + kPwTokens - tail;  // hidden rows
+        for (int e = lane; e < count * CB * 8; e += 32) {
+          const int i2 = e / (CB * 8), c = e % (CB * 8), r = i2 < before ? h0 + i2 : tail + i2 - before;
+          *reinterpret_cast<uint4*>(v + (c >> 3) * S::kColBlock + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cleared);
+        ++clears;
+      }
+      fill += 2 * tiles;
+    }
+    // the last pair's rows are handed back before the CTA can leave
+    if (!bad && nth > 0 && cluster == 1 && lane == 0)
+      for (int x = 0; x < 2; ++x) mbar_wait_bounded(&q_empty[x], (nth + 1) & 1, p.wait_limit_ns);
+    __syncwarp();
+    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+  } else {
+    // ---- softmax: warpgroup x serves query tile x, a row to a thread --------------------
+    PwItem it;
+    const int x = warp >> 2, r = tid & 127;
+    const uint32_t ts = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * x;  // S of this warp's lanes
+    const uint32_t to = ts + 256;                                              // and O
+    const bool pos_scale = p.scale_log2 > 0.f;
+    const float sc = pos_scale ? p.scale_log2 : 1.f;
+    uint32_t done = 0, nth = 0;  // tiles and pairs so far
+    int item = item0;
+    auto find = [&]() {  // the pair at `item` or the next that has rows
+      for (; item < items; item += step)
+        if (it.load(p, item, rank, tid == 0)) return true;
+      return false;
+    };
+    bool have = find();
+    while (have) {
+      const int active = x ? it.active_b : it.active_a;
+      const PwSpan span = it.span(x);
+      const int g = it.row0 + x * kPwRows + min(r, max(active - 1, 0));  // past the last row: any finite result
+      const int tok = g / p.group;
+      const int pos = it.L - it.n + tok;
+      float m_use = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = it.walk.j0; j < it.walk.j1; ++j) {
+        const int k0 = it.walk.tile(j) * kPwTokens;
+        if (!span.sees(k0, p.sinks)) continue;
+        const int vis = pos - k0 + 1;                // tokens of the tile up to the row's own
+        const int before = pos - p.window + 1 - k0;  // tokens of the tile before its window
+        const bool cut = __any_sync(kFullMask, vis < kPwTokens || before > 0 || !pos_scale);
+        // every wait is made warp-uniform before the warp-collective loads and stores
+        if (!__all_sync(kFullMask, mbar_wait_bounded(&s_full[x], done & 1, p.wait_limit_ns))) {
+          bad = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t u[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, u[c]);
+        tmem_wait_ld();
+        float* v = reinterpret_cast<float*>(&u[0][0]);
+        // raw scores: with a positive scale their maximum is the scaled scores'
+        if (cut) {
+          if (!pos_scale) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) v[i] *= p.scale_log2;
+          }
+          const int kept = p.sinks - k0;  // of those before the window, the sinks stay
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // the row's visible tokens of 32 as bits: [0, vis) without [kept, before)
+            const uint32_t hide = low_bits(before - 32 * c) & ~low_bits(kept - 32 * c);
+            const uint32_t see = low_bits(vis - 32 * c) & ~hide;
+            if (__any_sync(kFullMask, see != 0xffffffffu)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[32 * c + i] = (see >> i) & 1u ? v[32 * c + i] : -INFINITY;
+            }
+          }
+        }
+        float m4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+        for (int i = 8; i < 128; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = pw_max3(m4[e], v[i + e], v[i + e + 4]);
+        const float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // the base moves only when the maximum grows by more than kPwRescaleLog2: every
+        // P stays below 2^kPwRescaleLog2, and O and the row sum have the same base
+        const bool grow = mt > m_use + kPwRescaleLog2;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = exp2f(m_use - mt);  // 0 while nothing was visible
+          m_use = mt;
+        }
+        if (!first && __any_sync(kFullMask, grow)) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[16];
+            tmem_ld16(to + 16 * c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            tmem_st16(to + 16 * c, w);
+          }
+        }
+        first = false;
+        const float nbase = m_use == -INFINITY ? 0.f : -m_use;
+        const uint64_t sc2 = pw_pair(sc, sc), nb2 = pw_pair(nbase, nbase);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = pw_unpair(pw_fma2(pw_pair(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nb2));
+            e.x = pw_exp2(e.x);
+            e.y = pw_exp2(e.y);
+            sum[i & 1] = pw_add2(sum[i & 1], pw_pair(e.x, e.y));
+            w[i] = P16::pack(e.x, e.y);
+          }
+          tmem_st16(ts + 16 * c, w);
+          if (c & 1) {  // 64 tokens' P: their part of the product can begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_full[x]);
+          }
+        }
+        const float2 total = pw_unpair(pw_add2(sum[0], sum[1]));
+        l = l * alpha + (total.x + total.y);
+        ++done;
+      }
+      // what the output needs of this pair, then the next pair's place, then the wait
+      const bool mine = r < active;
+      T* og = static_cast<T*>(p.out) +
+              ((size_t)(it.q0 + tok) * p.num_heads + it.kvh * p.group + (g - tok * p.group)) * D;
+      item += step;
+      have = find();
+      if (!bad && !__all_sync(kFullMask, mbar_wait_bounded(&o_full[x], nth & 1, p.wait_limit_ns))) bad = true;
+      if (bad) break;
+      tc_fence_after();
+      if (cluster == 1) {
+        if (active > 0) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t w[32];
+            tmem_ld32(to + 32 * c, w);
+            tmem_wait_ld();
+            if (mine) {
+              uint4* dst = reinterpret_cast<uint4*>(og + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] =
+                    make_uint4(P16::pack(__uint_as_float(w[8 * i]) * inv, __uint_as_float(w[8 * i + 1]) * inv),
+                               P16::pack(__uint_as_float(w[8 * i + 2]) * inv, __uint_as_float(w[8 * i + 3]) * inv),
+                               P16::pack(__uint_as_float(w[8 * i + 4]) * inv, __uint_as_float(w[8 * i + 5]) * inv),
+                               P16::pack(__uint_as_float(w[8 * i + 6]) * inv, __uint_as_float(w[8 * i + 7]) * inv));
+            }
+          }
+        }
+        tc_fence_before();
+      } else {
+        // A cluster has one pair only. This part's O and (m, l) go into shared memory, in
+        // place of Q, K and V, once every MMA of both A and B, and so every copy that one
+        // reads, is over.
+        if (!__all_sync(kFullMask, mbar_wait_bounded(&o_full[x ^ 1], nth & 1, p.wait_limit_ns))) {
+          bad = true;
+          break;
+        }
+        float* so = reinterpret_cast<float*>(sm) + (size_t)(x * kPwRows + r) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
+          if (!first) {
+            tmem_ld32(to + 32 * c, w);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = 0u;
+          }
+          // 16-byte chunk k of the row at k ^ (r & 7): neighbouring rows' chunks fall into different banks
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(so + 4 * ((8 * c + i) ^ (r & 7))) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        reinterpret_cast<float2*>(sm + S::kJoinMl)[x * kPwRows + r] = make_float2(m_use, l);
+      }
+      ++nth;
+    }
+    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    __syncwarp();
+  }
+
+  // ---- a cluster joins its parts: each CTA its share of the rows --------------------------
+  if (cluster > 1) {
+    pw_cluster_barrier();
+    PwItem it;
+    if (it.load(p, item0, rank, false)) {
+      const int share = 2 * kPwRows / cluster;
+      const uint32_t base = smem_u32(sm);
+      for (int e = tid; e < share * (D / 4); e += kPwThreads) {
+        const int rr = (int)rank * share + e / (D / 4), k = e % (D / 4);
+        const int g = it.row0 + rr;
+        if (g >= it.rows) continue;
+        float2 ml[kPwMaxCluster];
+        float4 a[kPwMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kPwMaxCluster; ++c) {
+          ml[c] = make_float2(-INFINITY, 0.f);
+          a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < cluster) {
+            ml[c] = pw_remote_f2(pw_remote(base + S::kJoinMl + rr * 8, c));
+            a[c] = pw_remote_f4(pw_remote(base + (uint32_t)rr * D * 4 + 16 * (k ^ (rr & 7)), c));
+          }
+        }
+        float M = ml[0].x;
+#pragma unroll
+        for (int c = 1; c < kPwMaxCluster; ++c) M = fmaxf(M, ml[c].x);
+        const float nb = M == -INFINITY ? 0.f : M;
+        float lt = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kPwMaxCluster; ++c) {
+          const float f = exp2f(ml[c].x - nb);
+          lt += ml[c].y * f;
+          o[0] = fmaf(a[c].x, f, o[0]), o[1] = fmaf(a[c].y, f, o[1]);
+          o[2] = fmaf(a[c].z, f, o[2]), o[3] = fmaf(a[c].w, f, o[3]);
+        }
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const int t = g / p.group, j = g - t * p.group;
+        T* og = static_cast<T*>(p.out) + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 4 * k;
+        *reinterpret_cast<uint2*>(og) =
+            make_uint2(P16::pack(o[0] * inv, o[1] * inv), P16::pack(o[2] * inv, o[3] * inv));
+      }
+    }
+    pw_cluster_barrier();  // no CTA leaves while another reads its shared memory
+  }
+
+  // ---- tear-down: boxes have landed, MMAs have completed (bounded drains above) ------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kPwTmemCols);
+  }
+}
+
+using PrefillWindowLauncher = cudaError_t (*)(const PrefillWindowParams&, const void*, const void*, int, cudaStream_t);
+PrefillWindowLauncher prefill_window_launcher(int is_bf16, int head_dim);  // prefill_window.cu
+
+}  // namespace pkv

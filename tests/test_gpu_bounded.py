@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from bounded_helpers import DEV, TD, Cache, attend, check, eps_p, half_step, seen_by
+from bounded_helpers import DEV, TD, Cache, attend, check, eps_p, eps_prefill, half_step, seen_by
 
 pytestmark = pytest.mark.gpu
 
@@ -375,7 +375,7 @@ def test_prefill_window(pkv, combo, window, sinks):
             if i % 7 in (0, 3) or i in (127, 128, new[s] - 1):
                 want, _, bound, _ = attend(q[at + i], c.rows_k[s], c.rows_v[s],
                                            seen_by(L, L - new[s] + i, window, sinks), c.scale,
-                                           eps_p(c.dtype, 1 if dtype == "f16" else 2))
+                                           eps_prefill(c.dtype))
                 check(out[at + i], want, bound, f"L={L} n={new[s]} i={i}")
         at += new[s]
 
@@ -388,10 +388,16 @@ def test_prefill_window_last_query_sees_what_decode_shows(pkv):
     c.q = torch.stack([q[299], q[376]])
     ref = run_window(pkv, c, 128, 4)
     got = torch.stack([out[299], out[376]])
-    assert (got.float() - ref.float()).abs().max() <= 2 * half_step(c.dtype) * ref.float().abs().max()
+    # the prefill's weights are off by eps_prefill each (a sum of them, relative to the values'
+    # size, by no more), both outputs by their own rounding
+    size = torch.cat([v.abs().amax(1) for v in c.rows_v]).max().item()
+    assert (got.float() - ref.float()).abs().max() <= 2 * half_step(c.dtype) * ref.float().abs().max() \
+        + eps_prefill(c.dtype) * size
 
 
-def test_prefill_window_equals_prefill_when_all_is_seen(pkv):
+def test_prefill_window_agrees_with_prefill_when_all_is_seen(pkv):
+    """Both are within their bound of the same exact value: the window's
+    probabilities have one 16-bit part, the prefill's two."""
     c = Cache((900, 77), 2, 4, 128, 16, "bf16")
     new = [300, 77]
     q = torch.randn(sum(new), c.H, 128, device=DEV).to(c.dtype)
@@ -399,7 +405,55 @@ def test_prefill_window_equals_prefill_when_all_is_seen(pkv):
     ref = torch.empty_like(out)
     start = torch.tensor([0, 300, 377], dtype=torch.int32, device=DEV)
     pkv.paged_attention_prefill(ref, q, c.k, c.v, c.tables, c.context, start, c.scale, 300)
-    assert torch.equal(out, ref)
+    for row, s, P in ((0, 0, 600), (150, 0, 750), (299, 0, 899), (300, 1, 0), (376, 1, 76)):
+        want, _, bound, _ = attend(q[row], c.rows_k[s], c.rows_v[s], seen_by(c.lens[s], P, 1000, 0), c.scale,
+                                   eps_prefill(c.dtype))
+        check(out[row], want, bound, f"window {row}")
+        check(ref[row], want, bound, f"prefill {row}")
+
+
+def test_prefill_window_gives_up_on_a_wait(pkv):
+    """With a limit of 0 any wait not over at its first test gives up: the call
+    reports it and the next one works."""
+    c = Cache((900, 77), 2, 4, 128, 16, "bf16")
+    new = [300, 77]
+    q = torch.randn(sum(new), c.H, 128, device=DEV).to(c.dtype)
+    good = run_prefill(pkv, c, new, 100, 4, q)
+    old, err = pkv.get_wait_timeout_ns(), new_err()
+    try:
+        pkv.set_wait_timeout_ns(0)
+        run_prefill(pkv, c, new, 100, 4, q, err)
+        torch.cuda.synchronize()
+    finally:
+        pkv.set_wait_timeout_ns(old)
+    assert int(err.item()) == pkv.DEV_ERR_TIMEOUT
+    err.zero_()
+    assert torch.equal(run_prefill(pkv, c, new, 100, 4, q, err), good) and int(err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,D,bs,Hkv,G,lens,new", [
+    ("bf16", 128, 16, 8, 4, (2777,), (100,)),            # one chunk: clusters share its tiles
+    ("f16", 64, 8, 1, 1, (9000,), (130,)),
+    ("f16", 128, 32, 2, 7, (1500, 3, 4000), (5, 3, 17)),
+    ("bf16", 64, 16, 2, 3, (4000,) * 3, (1, 1, 1)),       # single queries
+    ("bf16", 128, 16, 20, 1, (600,) * 8, (600,) * 8),     # many tiles, none shared
+])
+@pytest.mark.parametrize("window,sinks", [(1024, 4), (100, 300), (1 << 30, 0)])
+def test_prefill_window_shapes(pkv, dtype, D, bs, Hkv, G, lens, new, window, sinks):
+    c = Cache(lens, Hkv, G, D, bs, dtype, seed=3)
+    q = torch.randn(sum(new), c.H, D, device=DEV).to(c.dtype)
+    err = new_err()
+    out = run_prefill(pkv, c, list(new), window, sinks, q, err)
+    assert int(err.item()) == 0
+    assert torch.equal(run_prefill(pkv, c, list(new), window, sinks, q, err), out)
+    at = 0
+    for s, L in enumerate(lens):
+        for i in sorted({0, 1, new[s] // 2, new[s] - 2, new[s] - 1} & set(range(new[s]))):
+            want, _, bound, _ = attend(q[at + i], c.rows_k[s], c.rows_v[s], seen_by(L, L - new[s] + i, window, sinks),
+                                       c.scale, eps_prefill(c.dtype))
+            check(out[at + i], want, bound, f"L={L} i={i}")
+        at += new[s]
+    assert torch.isfinite(out).all()
 
 
 def test_prefill_window_device_errors(pkv):
@@ -539,7 +593,7 @@ def test_session(pkv, dtype):
         users.append(u)
         model.append([torch.cat([sys_k, kk]).transpose(0, 1).contiguous(),
                       torch.cat([sys_v, vv]).transpose(0, 1).contiguous()])
-    scale, eps = 1.0 / 8.0, eps_p(td, 1 if dtype == "f16" else 2)
+    scale, eps = 1.0 / 8.0, eps_prefill(td)
     # the prompts, seen through a window
     bt, cl = bm.export(users, MB)
     q, start = norm(290, H, D), up(np.array([0, 200, 290], np.int32))
