@@ -21,7 +21,7 @@ namespace pkv {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kListMost = 512;          // candidates that are ranked one against all
+constexpr int kListMost = 128;          // candidates that are ranked one against all
 constexpr int kScoresInSmem = 32768;    // scores of a row that are kept in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;          // vectors per thread and chunk
@@ -62,7 +62,7 @@ __device__ __forceinline__ uint64_t rank_of(uint32_t key, int t) {
 template <int NT>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, int smem_scores) {
   constexpr int NW = NT / 32;
-  extern __shared__ float sm[];  // smem_scores scores
+  extern __shared__ float sm[];  // smem_scores (a multiple of 32) scores, then a bit for each
   __shared__ uint32_t hist[kBins];
   __shared__ uint64_t list[kListMost];
   __shared__ uint32_t warp_sum[NW];
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
   }
   const float* from = whole ? sm : row;
   uint64_t threshold = ~0ull;  // above every rank: no candidate is kept
+  uint32_t* kept_bits = reinterpret_cast<uint32_t*>(sm + smem_scores);  // of a stretch, a bit per token
   if (left > 0) {
     kmin = __reduce_min_sync(kFullMask, kmin);
     kmax = __reduce_max_sync(kFullMask, kmax);
@@ -115,13 +116,20 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
     }
     __syncthreads();
     uint64_t lo = (uint64_t)sh_min << 32, hi = ((uint64_t)sh_max << 32) | 0xffffffffu;
-    for (;;) {
+    for (bool every = true;; every = false) {  // every: [lo, hi] holds all candidates
       const int width = 64 - __clzll((long long)(hi - lo));
       const int shift = width > 11 ? width - 11 : 0;
+      if (every && shift >= 32) {  // the positions do not count yet
+        const uint32_t klo = (uint32_t)(lo >> 32);
+#pragma unroll 8
+        for (int t = first + tid; t < last; t += NT)
+          atomicAdd(&hist[(score_key(from[t]) - klo) >> (shift - 32)], 1u);
+      } else {
 #pragma unroll 4
-      for (int t = first + tid; t < last; t += NT) {
-        const uint64_t r = rank_of(score_key(from[t]), t);
-        if (r >= lo && r <= hi) atomicAdd(&hist[(uint32_t)((r - lo) >> shift)], 1u);
+        for (int t = first + tid; t < last; t += NT) {
+          const uint64_t r = rank_of(score_key(from[t]), t);
+          if (r >= lo && r <= hi) atomicAdd(&hist[(uint32_t)((r - lo) >> shift)], 1u);
+        }
       }
       __syncthreads();
       // a thread sums the bins kBins - 1 - (tid * P + j), from the largest down
@@ -165,10 +173,14 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
       __syncthreads();
     }
     const int n = (int)sh_count;
-#pragma unroll 4
+    const uint32_t klo = (uint32_t)(lo >> 32), khi = (uint32_t)(hi >> 32);
+#pragma unroll 8
     for (int t = first + tid; t < last; t += NT) {
-      const uint64_t r = rank_of(score_key(from[t]), t);
-      if (r >= lo && r <= hi) list[atomicAdd(&sh_n, 1u)] = r;
+      const uint32_t k = score_key(from[t]);
+      if (k >= klo && k <= khi) {
+        const uint64_t r = rank_of(k, t);
+        if (r >= lo && r <= hi) list[atomicAdd(&sh_n, 1u)] = r;
+      }
     }
     __syncthreads();
     for (int i = tid; i < n; i += NT) {
@@ -193,12 +205,20 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
     __syncthreads();
     const int per = (m + NT - 1) / NT * 32;  // tokens of a warp
     const int w0 = min(warp * per, m), w1 = min(w0 + per, m);
-    auto keeps = [&](int i) {
-      const int t = (int)c0 + i;
-      return t < first || t >= last || rank_of(score_key(sm[i]), t) >= threshold;
-    };
+    const uint32_t tkey = (uint32_t)(threshold >> 32), tpos = ~(uint32_t)threshold;
     int count = 0;
-    for (int i = w0; i < w1; i += 32) count += __popc(__ballot_sync(kFullMask, i + lane < w1 && keeps(i + lane)));
+#pragma unroll 4
+    for (int i = w0; i < w1; i += 32) {
+      const int t = (int)c0 + i + lane;
+      bool k = false;
+      if (i + lane < w1) {
+        const uint32_t key = score_key(sm[i + lane]);
+        k = t < first || t >= last || key > tkey || (key == tkey && (uint32_t)t <= tpos);
+      }
+      const uint32_t b = __ballot_sync(kFullMask, k);
+      if (lane == 0) kept_bits[i >> 5] = b;
+      count += __popc(b);
+    }
     if (lane == 0) warp_sum[warp] = (uint32_t)count;
     __syncthreads();
     int at = base;
@@ -208,10 +228,10 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
       if (i < warp) at += v;
       base += v;
     }
+#pragma unroll 4
     for (int i = w0; i < w1; i += 32) {
-      const bool k = i + lane < w1 && keeps(i + lane);
-      const uint32_t b = __ballot_sync(kFullMask, k);
-      if (k) {
+      const uint32_t b = kept_bits[i >> 5];
+      if (b >> lane & 1u) {
         const int to = at + __popc(b & ((1u << lane) - 1u));
         kept[to] = (int)c0 + i + lane;
         out[to] = sm[i + lane];
@@ -337,15 +357,15 @@ cudaError_t launch_with(K kernel, dim3 grid, int threads, size_t smem, cudaStrea
 
 template <int NT>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
-  const int scores = p.cap < kScoresInSmem ? (p.cap > 0 ? p.cap : 1) : kScoresInSmem;
-  const size_t smem = (size_t)scores * sizeof(float);
+  const int scores = p.cap < kScoresInSmem ? (p.cap / 32 + 1) * 32 : kScoresInSmem;
+  const size_t smem = (size_t)scores * 33 / 32 * sizeof(float);
   static int configured[64] = {0};  // per device ordinal
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
     e = cudaFuncSetAttribute(evict_select_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kScoresInSmem * (int)sizeof(float));
+                             kScoresInSmem / 32 * 33 * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
   }
