@@ -26,18 +26,26 @@ cudaError_t launch_prefill_window(const PrefillWindowParams& params, const void*
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) __atomic_store_n(&sms_of_device[dev], sms, __ATOMIC_RELEASE);
   }
+  // scores are taken raw, so the scale has to be positive: a negative one's sign goes
+  // into the queries, and 0 becomes a number that any score's product with is below rounding
+  p.flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+  p.scale_log2 = p.scale_log2 == 0.f ? 1e-37f : fabsf(p.scale_log2);
   CUtensorMap kmap, vmap;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   e = encode_pool_rows_map(&kmap, k_cache, (uint64_t)pool_rows, D, p.block_size, bf16);
   if (e != cudaSuccess) return e;
   e = encode_pool_rows_map(&vmap, v_cache, (uint64_t)pool_rows, D, p.block_size, bf16);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = ((int64_t)max_query_len * p.group + 2 * kPwRows - 1) / (2 * kPwRows);
+  const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;  // no sequence has more queries either
+  const int64_t queries = max_query_len < longest ? max_query_len : longest;
+  const int64_t pairs = (queries * p.group + 2 * kPwRows - 1) / (2 * kPwRows);
   const int64_t items = pairs * p.num_seqs * p.num_kv_heads;
   if (items > 0x3fffffff || pairs * 2 * kPwRows > 0x7fffffffLL) return cudaErrorNotSupported;
   p.pairs = (int)pairs;
+  p.by_columns.set((uint32_t)(p.num_seqs * p.num_kv_heads));
+  p.by_heads.set((uint32_t)p.num_kv_heads);
+  p.by_group.set((uint32_t)p.group);
   // K/V tiles of a walk, at most
-  const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
   const int64_t seen = (int64_t)p.window + p.sinks + 2 * kPwRows;
   const int64_t tiles = ((seen < longest ? seen : longest) + kPwTokens - 1) / kPwTokens;
   p.cluster = 1;

@@ -16,9 +16,9 @@
 // Where there are few pairs, a cluster shares one: each of its CTAs walks a part
 // of the K/V tiles, and the parts are joined through the cluster's shared memory
 // (log-sum-exp).
-// P enters its product as one 16-bit part: its rounding, 2^-9 (bfloat16) or 2^-12 of
-// each weight at most and independent from weight to weight, adds less to a row's output than
-// the rounding of the output itself does, whose largest is the same.
+// P enters its product as one 16-bit part: its rounding is 2^-8 (bfloat16) or 2^-11 of
+// each weight at most and independent from weight to weight, so that it adds no more to a
+// row's output than the rounding of the output itself, whose largest is the same.
 #pragma once
 
 #include <type_traits>
@@ -29,12 +29,27 @@ namespace pkv {
 
 constexpr int kPwRows = 128;     // rows of a query tile = tensor-memory lanes
 constexpr int kPwTokens = 128;   // tokens of a K/V tile
-constexpr int kPwStages = 4;     // K and V tiles in shared memory, K and V in turn
+constexpr int kPwStages = 4;     // tiles in shared memory: two links of a V and a K tile
 constexpr int kPwSoft = 256;     // 2 softmax warpgroups
 constexpr int kPwThreads = kPwSoft + 96;  // + MMA warp, TMA warp, query-loading and clearing warp
 constexpr uint32_t kPwTmemCols = 512;     // S of A and B (128 columns each), O of A and B
 constexpr float kPwRescaleLog2 = 8.f;     // base of the running max moves only when it grows by more
 constexpr int kPwMaxCluster = 4;
+
+// n / d for 0 <= n < 2^31 and 1 <= d < 2^31 as a product and a shift: with
+// 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d), n / d = n m >> (31 + s). (An integer
+// division takes some hundred cycles in a warp that comes by seldom, and the start of
+// a pair has several.)
+struct PwDivisor {
+  uint32_t d, m, s;
+  void set(uint32_t divisor) {
+    d = divisor;
+    s = 0;
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
+};
 
 struct PrefillWindowParams {
   void* out;
@@ -42,10 +57,12 @@ struct PrefillWindowParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_start;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;   // |scale| * log2(e), above 0
+  uint32_t flip;      // sign bits of a pair of query elements for a negative scale, else 0
   int window, sinks;  // window >= 1, sinks >= 0, no larger than the longest table
   int num_seqs, num_heads, num_kv_heads, group, block_size, max_blocks_per_seq, num_blocks;
   int pairs;    // of the longest sequence, per kv head
+  PwDivisor by_columns, by_heads, by_group;  // num_seqs * num_kv_heads, num_kv_heads, group
   int cluster;  // CTAs that share a pair of query tiles
   int32_t* dev_err;
   uint64_t wait_limit_ns;  // limit of every wait on another role's progress
@@ -92,7 +109,8 @@ struct PwShape {
   static constexpr int kStageOff = 2 * kTile;
   static constexpr int kBarOff = kStageOff + kPwStages * kTile;
   static constexpr int kSlotOff = kBarOff + 24 * 8;
-  static constexpr int kUsed = kSlotOff + 16 + 1024;  // + alignment slack
+  static constexpr int kOutOff = kSlotOff + 64;           // 4 KB per softmax warp: output rows on their way out
+  static constexpr int kUsed = kOutOff + 8 * 4096 + 1024;  // + alignment slack
   // more than half of an SM's, so that one CTA has its tensor memory to itself
   static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static constexpr int kJoinMl = 2 * kPwRows * D * 4;
@@ -204,6 +222,41 @@ __device__ __forceinline__ float pw_max3(float a, float b, float c) {
   return d;
 }
 
+// A warp's walk over the items `item`, `item` + step, .. < items that have query rows.
+// The grid is laid out for the longest sequence, so that in a ragged batch most may have
+// none: 32 are looked at together, one by a lane (8192 queries beside 63 sequences of one
+// query each: 203 us, 273 with a look at one item after another, 150 for the 8192 alone).
+struct PwScan {
+  int base;       // item of lane 0
+  uint32_t mask;  // lanes whose items are still to come
+  __device__ __forceinline__ void look(const PrefillWindowParams& p, int item, int step, int items, bool report) {
+    base = item;
+    const int i = item + (int)(threadIdx.x & 31) * step;
+    bool some = false;
+    if (i < items) {
+      const int row = p.by_columns.of(i), s = p.by_heads.of(i - row * (int)p.by_columns.d);
+      const int L = __ldg(p.context_lens + s), n = __ldg(p.query_start + s + 1) - __ldg(p.query_start + s);
+      if (L < 0 || L > p.max_blocks_per_seq * p.block_size || n < 0 || n > L) {
+        if (report) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
+      } else {
+        some = (p.pairs - 1 - row) * 2 * kPwRows < (int64_t)n * p.group;
+      }
+    }
+    mask = __ballot_sync(kFullMask, some);
+  }
+  __device__ __forceinline__ int ahead(int step) const { return base + (__ffs(mask) - 1) * step; }
+  // Moves `item` on to the next with rows; false past the last.
+  __device__ __forceinline__ bool next(const PrefillWindowParams& p, int step, int items, int& item) {
+    while (mask == 0u) {
+      if (items - base <= 32 * step) return false;
+      look(p, base + 32 * step, step, items, false);
+    }
+    item = ahead(step);
+    mask &= mask - 1;
+    return true;
+  }
+};
+
 // A pair of query tiles of one sequence and kv head, and the K/V tiles this CTA
 // walks for it.
 struct PwItem {
@@ -213,26 +266,21 @@ struct PwItem {
   int kv_end, wlo;  // past the last token that a query sees; first token in the first query's window
   PwWalk walk;
 
-  // The item with index `item`; false when it has no rows (or its lengths are wrong).
-  __device__ __forceinline__ bool load(const PrefillWindowParams& p, int item, uint32_t rank, bool report) {
-    const int columns = p.num_seqs * p.num_kv_heads;
-    const int pair = p.pairs - 1 - item / columns;  // later queries first: theirs are the longest walks
-    const int column = item % columns;
-    s = column / p.num_kv_heads;
-    kvh = column % p.num_kv_heads;
+  // The item with index `item`, which has rows (its lengths come from the first-level
+  // cache, where the scan left them, and in registers that a warp shares).
+  __device__ __forceinline__ void load(const PrefillWindowParams& p, int item, uint32_t rank) {
+    const int row = p.by_columns.of(item), column = item - row * (int)p.by_columns.d;
+    const int pair = p.pairs - 1 - row;  // later queries first: theirs are the longest walks
+    s = p.by_heads.of(column);
+    kvh = column - s * p.num_kv_heads;
     L = __ldg(p.context_lens + s);
     q0 = __ldg(p.query_start + s);
     n = __ldg(p.query_start + s + 1) - q0;
-    if (L < 0 || L > p.max_blocks_per_seq * p.block_size || n < 0 || n > L) {
-      if (report) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
-      return false;
-    }
     rows = (int)min((int64_t)n * p.group, (int64_t)p.pairs * 2 * kPwRows);  // the launch covers no more
     row0 = pair * 2 * kPwRows;
-    if (row0 >= rows) return false;
     auto place = [&](int a, int& active, PwSpan& span) {
       active = max(min(rows - a, kPwRows), 0);
-      const int t0 = a / p.group, t1 = (a + max(active, 1) - 1) / p.group;
+      const int t0 = p.by_group.of(a), t1 = p.by_group.of(a + max(active, 1) - 1);
       const int p0 = L - n + t0;
       span.lo = p0 >= p.window ? p0 - p.window + 1 : 0;
       span.end = active > 0 ? L - n + t1 + 1 : 0;
@@ -245,9 +293,8 @@ struct PwItem {
     walk.first = (min(p.sinks, kv_end) + kPwTokens - 1) / kPwTokens;
     walk.from = max(wlo / kPwTokens, walk.first);
     const int all = walk.first + tend - walk.from;
-    walk.j0 = (int)((int64_t)all * rank / p.cluster);
-    walk.j1 = (int)((int64_t)all * (rank + 1) / p.cluster);
-    return true;
+    walk.j0 = p.cluster == 1 ? 0 : (int)((int64_t)all * rank / p.cluster);
+    walk.j1 = p.cluster == 1 ? all : (int)((int64_t)all * (rank + 1) / p.cluster);
   }
   __device__ __forceinline__ PwSpan span(int x) const { return x ? span_b : span_a; }
   // Rows [hide0, hide1) and from `tail` on of the K/V tile at k0 are seen by no query.
@@ -263,7 +310,7 @@ struct PwItem {
 template <typename T, int D>
 __global__ void __launch_bounds__(kPwThreads, 1)
     pa_prefill_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                             const PrefillWindowParams p) {
+                             const __grid_constant__ PrefillWindowParams p) {
   using S = PwShape<D>;
   using P16 = PwPack<T>;
   constexpr int kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
@@ -273,20 +320,19 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   // Every barrier's phases follow one another in the order of the work (K/V tiles, or
   // pairs of query tiles), and nobody who waits for a phase can fall two behind.
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
-  // The fills of the K/V stages are counted through: K and V of a tile in turn, fill f
-  // into stage f % 4. The MMAs hand back a V tile and the K tile behind it at once:
-  // fills 2 j - 1 and 2 j, hand-back j.
-  uint64_t* kv_full = bars;        // [4] fill landed
-  uint64_t* kv_empty = bars + 4;   // [2] hand-back j, of barrier j % 2
-  uint64_t* s_full = bars + 6;     // [A, B] S computed
-  uint64_t* p_half = bars + 8;     // [A, B] P of the first 64 tokens written (one arrival per softmax warp)
-  uint64_t* p_full = bars + 10;    // [A, B] all of P written
-  uint64_t* q_full = bars + 12;    // [A, B] query rows in place (one arrival per loading thread)
-  uint64_t* q_empty = bars + 14;   // [A, B] the pair's last S computed
-  uint64_t* o_full = bars + 16;    // [A, B] the pair's last O computed
-  uint64_t* to_clear = bars + 18;  // a V tile with rows that no query sees has landed 
-  uint64_t* cleared = bars + 19;   // those rows are set to zero
-  uint64_t* drained = bars + 20;   // every MMA of the CTA done
+  // K and V tiles come as links of a chain: the V of one tile with the K of the next,
+  // which the MMAs of one step need together (a pair of query tiles of n K/V tiles
+  // has n + 1 links: the first without V, the last without K). Link c is in stages
+  // 2 (c % 2) (K) and 2 (c % 2) + 1 (V).
+  uint64_t* full = bars;         // [2] the link landed
+  uint64_t* ready = bars + 2;    // [2] and rows of its V that no query sees are cleared
+  uint64_t* empty = bars + 4;    // [2] the MMAs are done with it
+  uint64_t* s_full = bars + 6;   // [A, B] S computed
+  uint64_t* p_full = bars + 8;   // [A, B] P written (one arrival per softmax warp)
+  uint64_t* q_full = bars + 10;  // [A, B] query rows in place (one arrival per loading thread)
+  uint64_t* q_empty = bars + 12; // [A, B] the pair's last S computed
+  uint64_t* o_full = bars + 14;  // [A, B] the pair's last O computed
+  uint64_t* drained = bars + 16; // every MMA of the CTA done
   uint32_t* slot = reinterpret_cast<uint32_t*>(sm + S::kSlotOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -297,7 +343,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   // ---- set-up: barriers, tensor memory ----------------------------------------
   if (tid == 0) {
-    for (int i = 0; i < 21; ++i) mbar_init(&bars[i], i >= 8 && i < 12 ? 4 : (i == 12 || i == 13 ? 32 : 1));
+    for (int i = 0; i < 17; ++i) mbar_init(&bars[i], i == 8 || i == 9 ? 4 : (i == 10 || i == 11 ? 32 : 1));
     mbar_init_fence();
   }
   if (warp == 8) tmem_alloc(slot, kPwTmemCols);
@@ -311,13 +357,15 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     // ---- TMA: K and V tiles, box by box (one box: 64 head dims of one cache block of
     // the kv head); lane b holds the row of block b of the next tile in the pool
     PwItem it;
+    PwScan scan;
+    scan.look(p, item0, step, items, false);
     const int per_tile = kPwTokens / p.block_size;  // <= 16 blocks
     const int bs = p.block_size, bits = __ffs(bs) - 1;
     const int zero_row = p.num_blocks * p.num_kv_heads * bs;  // first row past the pool: reads zeros
     const uint32_t box_bytes = (uint32_t)bs * 128u;
-    uint32_t used = 0;  // stages filled so far
-    for (int item = item0; item < items && !bad; item += step) {
-      if (!it.load(p, item, rank, false)) continue;
+    uint32_t link = 0;  // links so far
+    for (int item; !bad && scan.next(p, step, items, item);) {
+      it.load(p, item, rank);
       const int32_t* bt = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
       auto blocks_of = [&](int k0) { return min(per_tile, (it.kv_end - k0 + bs - 1) >> bits); };
       auto seen = [&](int k) { return k < p.sinks || k + bs > it.wlo; };  // the block at token k, by a query
@@ -327,50 +375,43 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         return lane < blocks_of(k0) && seen(k) ? __ldg(bt + (k >> bits)) : -1;
       };
       int id = fetch(it.walk.j0);
-      for (int j = it.walk.j0; j < it.walk.j1 && !bad; ++j) {
-        const int k0 = it.walk.tile(j) * kPwTokens, nblk = blocks_of(k0);
-        int y = zero_row;
-        if (lane < nblk && seen(k0 + lane * bs)) {
+      int y = zero_row, nblk = 0;  // of the tile whose V is next
+      for (int j = it.walk.j0; j <= it.walk.j1 && it.walk.j0 < it.walk.j1; ++j, ++link) {  // K of tile j, V of tile j - 1
+        const uint32_t c = link & 1;
+        const int k0 = j < it.walk.j1 ? it.walk.tile(j) * kPwTokens : 0;
+        const int nk = j < it.walk.j1 ? blocks_of(k0) : 0;
+        int yk = zero_row;
+        if (lane < nk && seen(k0 + lane * bs)) {
           if (id >= 0 && id < p.num_blocks)
-            y = (id * p.num_kv_heads + it.kvh) * bs;
+            yk = (id * p.num_kv_heads + it.kvh) * bs;
           else
             set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
         }
         id = fetch(j + 1);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          // the stage of a V tile, fill f, was that of fill f - 4: hand-back (f - 3) / 2;
-          // that of the next K tile comes back with it
-          const uint32_t st = used % kPwStages, back = (used - 3) / 2;
-          if (v == 1 && used > kPwStages - 2 &&
-              !__all_sync(kFullMask, mbar_wait_bounded(&kv_empty[back & 1], (back >> 1) & 1, p.wait_limit_ns))) {
-            bad = true;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(nblk * CB) * box_bytes);
-          __syncwarp();
-          const int b = lane / CB, cb = lane % CB;
-          const int row = __shfl_sync(kFullMask, y, b);
-          if (lane < nblk * CB)
-            tma_load_2d(sm + S::kStageOff + st * S::kTile + cb * S::kColBlock + b * bs * 128, v ? &vmap : &kmap,
-                        cb * 64, row, &kv_full[st]);
-          ++used;
+        if (link >= 2 &&
+            !__all_sync(kFullMask, mbar_wait_bounded(&empty[c], ((link >> 1) + 1) & 1, p.wait_limit_ns))) {
+          bad = true;
+          break;
         }
+        if (lane == 0) mbar_arrive_expect_tx(&full[c], (uint32_t)((nk + nblk) * CB) * box_bytes);
+        __syncwarp();
+        const int b = lane / CB, cb = lane % CB;
+        const int row_k = __shfl_sync(kFullMask, yk, b), row_v = __shfl_sync(kFullMask, y, b);
+        unsigned char* at = sm + S::kStageOff + 2 * c * S::kTile + cb * S::kColBlock + b * bs * 128;
+        if (lane < nblk * CB) tma_load_2d(at + S::kTile, &vmap, cb * 64, row_v, &full[c]);
+        if (lane < nk * CB) tma_load_2d(at, &kmap, cb * 64, row_k, &full[c]);
+        y = yk;
+        nblk = nk;
       }
     }
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-    // every box must land, and the last hand-backs be over, before the CTA can leave
-    // (earlier phases are known to be over, since a later fill waited for them)
-    if (lane == 0) {
-      for (uint32_t st = 0; st < kPwStages; ++st)
-        if (used > st) {
-          const uint32_t last = st + kPwStages * ((used - 1 - st) / kPwStages);
-          mbar_wait_bounded(&kv_full[st], (last / kPwStages) & 1, kDrainLimitNs);
-        }
-      if (!bad && used > 0)
-        for (uint32_t back = used >= 4 ? used / 2 - 1 : 0; back <= used / 2; ++back)
-          mbar_wait_bounded(&kv_empty[back & 1], (back >> 1) & 1, p.wait_limit_ns);
-    }
+    // the last links must land and come back before the CTA can leave (earlier ones are
+    // known to have)
+    if (lane == 0)
+      for (uint32_t c = link >= 2 ? link - 2 : 0; c < link; ++c) {
+        mbar_wait_bounded(&full[c & 1], (c >> 1) & 1, kDrainLimitNs);
+        if (!bad) mbar_wait_bounded(&empty[c & 1], (c >> 1) & 1, p.wait_limit_ns);
+      }
     __syncwarp();
   } else if (warp == 8) {
     // ---- MMA issue -----------------------------------------------------------------
@@ -389,20 +430,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     // below 256 KB, so the sums never carry out of the field)
     const uint32_t qd = (uint32_t)smem_desc_sw128(sb, 16, 1024);
     const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
-    const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, S::kColBlock, 1024);
+    const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
     const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
-    PwItem it;
-    uint32_t fill = 0, clears = 0, nth = 0;  // first fill of the pair, cleared tiles, pairs so far
-    uint32_t done[2] = {0, 0};                // P of A and B so far
+    uint32_t link = 0, nth = 0;  // links and pairs so far
+    uint32_t done = 0;           // parities of the P of A and B so far, as bits
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool ok = __all_sync(kFullMask, mbar_wait_bounded(bar, parity, p.wait_limit_ns));
       tc_fence_after();
       return ok;
     };
-    auto full = [&](uint32_t f) { return wait(&kv_full[f % kPwStages], (f / kPwStages) & 1); };
     // within one elected region: S into the place of x's scores ...
-    auto mmas_s = [&](int x, uint32_t f, bool last) {
-      const uint32_t kb = kd + ((f % kPwStages) * S::kTile >> 4), qb = qd + (x * S::kTile >> 4);
+    auto mmas_s = [&](int x, uint32_t c, bool last) {
+      const uint32_t kb = kd + (c * (2 * S::kTile) >> 4), qb = qd + (x * S::kTile >> 4);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
@@ -411,75 +450,55 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       mma_commit(&s_full[x]);
       if (last && cluster == 1) mma_commit(&q_empty[x]);
     };
-    // ... and O += P V over the first (h 0) or last 64 tokens
-    auto mmas_o = [&](int x, uint32_t f, int h, bool first) {
-      const uint32_t vb = vd + ((f % kPwStages) * S::kTile >> 4);
+    // ... and O += P V
+    auto mmas_o = [&](int x, uint32_t c, bool first) {
+      const uint32_t vb = vd + (c * (2 * S::kTile) >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int ks = 4 * h + k;
+      for (int ks = 0; ks < kPwTokens / 16; ++ks)
         pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 8 * ks, vb + (ks * 2048 >> 4), hi, id_o,
                   (ks > 0 || !first) ? 1u : 0u);
-      }
     };
-    for (int item = item0; item < items && !bad; item += step) {
-      if (!it.load(p, item, rank, false)) continue;
+    PwItem it;
+    PwScan scan;
+    scan.look(p, item0, step, items, false);
+    for (int item; !bad && scan.next(p, step, items, item);) {
+      it.load(p, item, rank);
       const int tiles = it.walk.j1 - it.walk.j0;
-      int last[2];  // the last tile that A and B see, as a token position
-#pragma unroll
-      for (int x = 0; x < 2; ++x) last[x] = (it.span(x).end - 1) & ~(kPwTokens - 1);
-      bool opened[2] = {false, false}, sees[2] = {false, false};  // O holds something; the tile at hand is seen
+      // the last tiles that A and B see, as token positions; bits x: the tile at hand is
+      // seen, O holds something
+      const int last_a = (it.span_a.end - 1) & ~(kPwTokens - 1), last_b = (it.span_b.end - 1) & ~(kPwTokens - 1);
+      uint32_t sees = 0, opened = 0;
       // rows that no S of this part needs are in place before the pair ends all the same
-      bad = !wait(&q_full[0], nth & 1);
-      if (tiles > 0 && !bad) {
-        const int k0 = it.walk.tile(it.walk.j0) * kPwTokens;
-        sees[0] = it.span_a.sees(k0, p.sinks);
-        sees[1] = it.span_b.sees(k0, p.sinks);
-        bad = !full(fill);
-        if (!bad && sees[0] && elect_one()) mmas_s(0, fill, k0 == last[0]);
-        __syncwarp();
-        bad = bad || !wait(&q_full[1], nth & 1);
-        if (!bad && elect_one()) {
-          if (sees[1]) mmas_s(1, fill, k0 == last[1]);
-          mma_commit(&kv_empty[(fill / 2) & 1]);  // with the last V of the pair before
-        }
-        __syncwarp();
-      } else {
-        bad = bad || !wait(&q_full[1], nth & 1);
-      }
-      for (int i = 0; i < tiles && !bad; ++i) {
-        const uint32_t fv = fill + 2 * i + 1, fk = fv + 1;  // this V and the next K
-        const int k0 = it.walk.tile(it.walk.j0 + i) * kPwTokens;
-        const bool more = i + 1 < tiles;
-        const int k1 = more ? it.walk.tile(it.walk.j0 + i + 1) * kPwTokens : 0;
-        bool next[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) next[x] = more && it.span(x).sees(k1, p.sinks);
-        int h0, h1, tl;
-        bad = !full(fv) || (more && !full(fk));
-        if (!bad && it.hidden(p, k0, h0, h1, tl)) {
-          if (lane == 0) mbar_arrive(to_clear);
-          __syncwarp();
-          bad = !wait(cleared, clears++ & 1);
-        }
-#pragma unroll
+      bad = !wait(&q_full[0], nth & 1) || !wait(&q_full[1], nth & 1);
+      int k1 = 0;  // the tile whose S is next
+      uint32_t next = 0;
+      auto look = [&](int i) {
+        k1 = i < tiles ? it.walk.tile(it.walk.j0 + i) * kPwTokens : 0;
+        next = i < tiles ? (uint32_t)it.span_a.sees(k1, p.sinks) | (uint32_t)it.span_b.sees(k1, p.sinks) << 1 : 0u;
+      };
+      look(0);
+      for (int i = tiles > 0 ? 0 : 1; i <= tiles && !bad; ++i, ++link) {  // O of tile i - 1, S of tile i
+        const uint32_t c = link & 1;
+        bad = !wait(&ready[c], (link >> 1) & 1);
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          if (!bad && sees[x]) {
-            // (a pair's first P comes from warps that have read the O of the pair before)
-            bad = !wait(&p_half[x], done[x] & 1);
-            if (!bad && elect_one()) mmas_o(x, fv, 0, !opened[x]);
-            __syncwarp();
-            opened[x] = true;
-            bad = bad || !wait(&p_full[x], done[x] & 1);
-            ++done[x];
+          const bool o = sees >> x & 1, sx = next >> x & 1;
+          // (a pair's first P comes from warps that have read the O of the pair before)
+          if (!bad && o) {
+            bad = !wait(&p_full[x], done >> x & 1);
+            done ^= 1u << x;
           }
           if (!bad && elect_one()) {
-            if (sees[x]) mmas_o(x, fv, 1, false);
-            if (next[x]) mmas_s(x, fk, k1 == last[x]);
-            if (x == 1 && more) mma_commit(&kv_empty[(fk / 2) & 1]);
+            if (o) mmas_o(x, c, !(opened >> x & 1));
+            if (sx) mmas_s(x, c, k1 == (x ? last_b : last_a));
+            // the link comes back with B's S (the softmax sees to that), or here
+            if (x == 1 && !sx) mma_commit(&empty[c]);
           }
           __syncwarp();
-          sees[x] = next[x];
         }
+        opened |= sees;
+        sees = next;
+        look(i + 1);
       }
       if (!bad && elect_one()) {
 #pragma unroll
@@ -489,27 +508,23 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
       }
       __syncwarp();
-      fill += 2 * tiles;
       ++nth;
     }
-    if (elect_one()) {
-      if (!bad && fill > 0) mma_commit(&kv_empty[(fill / 2) & 1]);  // the last V
-      // nothing may be torn down before the last MMA, after a timeout neither
-      mma_commit(drained);
-    }
+    // nothing may be torn down before the last MMA, after a timeout neither
+    if (elect_one()) mma_commit(drained);
     __syncwarp();
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
     mbar_wait_bounded(drained, 0, kDrainLimitNs);
     __syncwarp();
   } else if (warp == 10) {
-    // ---- query rows, in 16-byte chunks, a row by two lanes; then the pair's V tiles that
-    // have hidden rows
-    constexpr int CPR = D / 8;
+    // ---- query rows, in 16-byte chunks, 128 bytes by 8 lanes; then the pair's links
     PwItem it;
+    PwScan scan;
+    scan.look(p, item0, step, items, false);
     const T* q = static_cast<const T*>(p.q);
-    uint32_t nth = 0, fill = 0, clears = 0;  // pairs so far, first fill of the pair, cleared tiles so far
-    for (int item = item0; item < items && !bad; item += step) {
-      if (!it.load(p, item, rank, false)) continue;
+    uint32_t nth = 0, link = 0;  // pairs and links so far
+    for (int item; !bad && scan.next(p, step, items, item);) {
+      it.load(p, item, rank);
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         if (nth > 0 && !__all_sync(kFullMask, mbar_wait_bounded(&q_empty[x], (nth + 1) & 1, p.wait_limit_ns))) {
@@ -517,54 +532,73 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           break;
         }
         const int active = max(min(it.rows - it.row0 - x * kPwRows, kPwRows), 0);
-#pragma unroll
-        for (int rr = lane >> 1; rr < kPwRows; rr += 16) {
+        const int ch = lane & 7;
+#pragma unroll 4
+        for (int rr = lane >> 3; rr < kPwRows; rr += 4) {
           if (active == 0) break;
           const bool in = rr < active;
-          const int g = it.row0 + x * kPwRows + rr, t = in ? g / p.group : 0, j = in ? g - t * p.group : 0;
-          const T* src = q + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D;
-          const uint32_t to = smem_u32(sm + x * S::kTile) + rr * 128, bytes = in ? 16 : 0;
+          const int g = it.row0 + x * kPwRows + rr, t = in ? p.by_group.of(g) : 0, j = in ? g - t * p.group : 0;
+          const T* src = q + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 8 * ch;
+          const uint32_t to = smem_u32(sm + x * S::kTile) + rr * 128 + ((ch ^ (rr & 7)) << 4), bytes = in ? 16 : 0;
 #pragma unroll
-          for (int c2 = 0; c2 < CPR / 2; ++c2) {
-            const int c = 2 * c2 + (lane & 1);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             to + (c >> 3) * S::kColBlock + (((c & 7) ^ (rr & 7)) << 4)),
-                         "l"(src + c * 8), "r"(bytes)
+          for (int cb = 0; cb < CB; ++cb)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + cb * S::kColBlock),
+                         "l"(src + cb * 64), "r"(bytes)
                          : "memory");
-          }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
       if (bad) break;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (p.flip != 0u) {  // a negative scale: the queries change their sign instead
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        for (int e = lane; e < 2 * S::kTile / 4; e += 32) reinterpret_cast<uint32_t*>(sm)[e] ^= p.flip;
+        __syncwarp();
+      }
       fence_async_smem();
       mbar_arrive(&q_full[0]);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_async_smem();
       mbar_arrive(&q_full[1]);
       ++nth;
-      // rows of V tiles that no query sees may hold anything (a NaN would survive a zero
-      // weight): zeros instead, once a tile has landed
-      const int tiles = it.walk.j1 - it.walk.j0;
-      for (int i = 0; i < tiles; ++i) {
-        int h0, h1, tail;
-        if (!it.hidden(p, it.walk.tile(it.walk.j0 + i) * kPwTokens, h0, h1, tail)) continue;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(to_clear, clears & 1, p.wait_limit_ns))) {
+      // the links: rows of a V tile that no query sees may hold anything (a NaN would
+      // survive a zero weight), they become zeros
+      for (int j = it.walk.j0; j <= it.walk.j1 && it.walk.j0 < it.walk.j1; ++j, ++link) {
+        const uint32_t c = link & 1;
+        if (!__all_sync(kFullMask, mbar_wait_bounded(&full[c], (link >> 1) & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
-        unsigned char* v = sm + S::kStageOff + (fill + 2 * i + 1) % kPwStages * S::kTile;
-        const int before = max(h1 - h0, 0), count = before + kPwTokens - tail;  // hidden rows
-        for (int e = lane; e < count * CB * 8; e += 32) {
-          const int i2 = e / (CB * 8), c = e % (CB * 8), r = i2 < before ? h0 + i2 : tail + i2 - before;
-          *reinterpret_cast<uint4*>(v + (c >> 3) * S::kColBlock + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        int h0, h1, tail;
+        if (j > it.walk.j0 && it.hidden(p, it.walk.tile(j - 1) * kPwTokens, h0, h1, tail)) {
+          unsigned char* v = sm + S::kStageOff + (2 * c + 1) * S::kTile;
+          const int before = max(h1 - h0, 0), count = before + kPwTokens - tail;  // hidden rows
+          for (int e = lane; e < count * CB * 8; e += 32) {
+            const int i2 = e / (CB * 8), ch = e % (CB * 8), r = i2 < before ? h0 + i2 : tail + i2 - before;
+            *reinterpret_cast<uint4*>(v + (ch >> 3) * S::kColBlock + r * 128 + (ch & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(cleared);
-        ++clears;
+        if (lane == 0) mbar_arrive(&ready[c]);
+        // in passing, the next pair's query rows into L2 (a hint only)
+        if (j == it.walk.j0 + 1 && scan.mask != 0u) {
+          const int next = scan.ahead(step);
+          const int row = p.by_columns.of(next), column = next - row * (int)p.by_columns.d;
+          const int of = p.by_heads.of(column), head = (column - of * p.num_kv_heads) * p.group;
+          const int q0 = __ldg(p.query_start + of), n = __ldg(p.query_start + of + 1) - q0;
+          const int g0 = (p.pairs - 1 - row) * 2 * kPwRows;
+          const int rows = (int)min((int64_t)n * p.group - g0, (int64_t)2 * kPwRows);
+#pragma unroll 4
+          for (int e = lane; e < rows * CB; e += 32) {
+            const int g = g0 + e / CB, t = p.by_group.of(g);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                q + ((size_t)(q0 + t) * p.num_heads + head + g - t * p.group) * D + e % CB * 64));
+          }
+        }
       }
-      fill += 2 * tiles;
     }
     // the last pair's rows are handed back before the CTA can leave
     if (!bad && nth > 0 && cluster == 1 && lane == 0)
@@ -577,13 +611,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int x = warp >> 2, r = tid & 127;
     const uint32_t ts = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * x;  // S of this warp's lanes
     const uint32_t to = ts + 256;                                              // and O
-    const bool pos_scale = p.scale_log2 > 0.f;
-    const float sc = pos_scale ? p.scale_log2 : 1.f;
-    uint32_t done = 0, nth = 0;  // tiles and pairs so far
+    const float sc = p.scale_log2;  // > 0
+    uint32_t done = 0, nth = 0, link = 0;  // tiles, pairs and links so far
     int item = item0;
     auto find = [&]() {  // the pair at `item` or the next that has rows
-      for (; item < items; item += step)
-        if (it.load(p, item, rank, tid == 0)) return true;
+      for (; item < items; item += 32 * step) {
+        PwScan scan;  // (no registers to spare for one that is kept)
+        scan.look(p, item, step, items, warp == 0);
+        if (scan.mask == 0u) continue;
+        item = scan.ahead(step);
+        it.load(p, item, rank);
+        return true;
+      }
       return false;
     };
     bool have = find();
@@ -591,7 +630,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const int active = x ? it.active_b : it.active_a;
       const PwSpan span = it.span(x);
       const int g = it.row0 + x * kPwRows + min(r, max(active - 1, 0));  // past the last row: any finite result
-      const int tok = g / p.group;
+      const int tok = p.by_group.of(g);
       const int pos = it.L - it.n + tok;
       float m_use = -INFINITY, l = 0.f;
       bool first = true;
@@ -600,24 +639,22 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         if (!span.sees(k0, p.sinks)) continue;
         const int vis = pos - k0 + 1;                // tokens of the tile up to the row's own
         const int before = pos - p.window + 1 - k0;  // tokens of the tile before its window
-        const bool cut = __any_sync(kFullMask, vis < kPwTokens || before > 0 || !pos_scale);
+        const bool cut = __any_sync(kFullMask, vis < kPwTokens || before > 0);
         // every wait is made warp-uniform before the warp-collective loads and stores
         if (!__all_sync(kFullMask, mbar_wait_bounded(&s_full[x], done & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
         tc_fence_after();
+        // B's S is the last MMA that reads its link
+        if (warp == 4 && lane == 0) mbar_arrive(&empty[(link + (j - it.walk.j0)) & 1]);
         uint32_t u[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, u[c]);
         tmem_wait_ld();
         float* v = reinterpret_cast<float*>(&u[0][0]);
-        // raw scores: with a positive scale their maximum is the scaled scores'
+        // (raw scores: their maximum is the scaled scores', the scale being positive)
         if (cut) {
-          if (!pos_scale) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i) v[i] *= p.scale_log2;
-          }
           const int kept = p.sinks - k0;  // of those before the window, the sinks stay
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -647,7 +684,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           m_use = mt;
         }
         if (!first && __any_sync(kFullMask, grow)) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t w[16];
             tmem_ld16(to + 16 * c, w);
@@ -673,19 +710,17 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             w[i] = P16::pack(e.x, e.y);
           }
           tmem_st16(ts + 16 * c, w);
-          if (c & 1) {  // 64 tokens' P: their part of the product can begin
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_full[x]);
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
         const float2 total = pw_unpair(pw_add2(sum[0], sum[1]));
         l = l * alpha + (total.x + total.y);
         ++done;
       }
       // what the output needs of this pair, then the next pair's place, then the wait
-      const bool mine = r < active;
+      link += it.walk.j0 < it.walk.j1 ? it.walk.j1 - it.walk.j0 + 1 : 0;
       T* og = static_cast<T*>(p.out) +
               ((size_t)(it.q0 + tok) * p.num_heads + it.kvh * p.group + (g - tok * p.group)) * D;
       item += step;
@@ -696,21 +731,36 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (cluster == 1) {
         if (active > 0) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t w[32];
-            tmem_ld32(to + 32 * c, w);
-            tmem_wait_ld();
-            if (mine) {
-              uint4* dst = reinterpret_cast<uint4*>(og + 32 * c);
+          // 64 dims at a time through the warp's 4 KB (16-byte chunk k of row r at k ^ (r & 7)),
+          // so that a store covers whole lines: a row to a lane, each store touched 32
+          // lines and the pair's stores kept the memory pipe for 4000 cycles
+          unsigned char* stage = sm + S::kOutOff + warp * 4096;
+          const uint64_t mine = reinterpret_cast<uint64_t>(og);
+#pragma unroll 1
+          for (int half = 0; half < CB; ++half) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[32];
+              tmem_ld32(to + 64 * half + 32 * c, w);
+              tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] =
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4)) =
                     make_uint4(P16::pack(__uint_as_float(w[8 * i]) * inv, __uint_as_float(w[8 * i + 1]) * inv),
                                P16::pack(__uint_as_float(w[8 * i + 2]) * inv, __uint_as_float(w[8 * i + 3]) * inv),
                                P16::pack(__uint_as_float(w[8 * i + 4]) * inv, __uint_as_float(w[8 * i + 5]) * inv),
                                P16::pack(__uint_as_float(w[8 * i + 6]) * inv, __uint_as_float(w[8 * i + 7]) * inv));
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3), ch = lane & 7;
+              const uint64_t row = __shfl_sync(kFullMask, mine, rr);
+              if (32 * (warp & 3) + rr < active)
+                reinterpret_cast<uint4*>(row)[8 * half + ch] =
+                    *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+            }
+            __syncwarp();
           }
         }
         tc_fence_before();
@@ -750,8 +800,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   // ---- a cluster joins its parts: each CTA its share of the rows --------------------------
   if (cluster > 1) {
     pw_cluster_barrier();
-    PwItem it;
-    if (it.load(p, item0, rank, false)) {
+    PwScan scan;
+    scan.look(p, item0, step, items, false);
+    if (scan.mask != 0u) {
+      PwItem it;
+      it.load(p, item0, rank);
       const int share = 2 * kPwRows / cluster;
       const uint32_t base = smem_u32(sm);
       for (int e = tid; e < share * (D / 4); e += kPwThreads) {
@@ -782,7 +835,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           o[2] = fmaf(a[c].z, f, o[2]), o[3] = fmaf(a[c].w, f, o[3]);
         }
         const float inv = lt > 0.f ? 1.f / lt : 0.f;
-        const int t = g / p.group, j = g - t * p.group;
+        const int t = p.by_group.of(g), j = g - t * p.group;
         T* og = static_cast<T*>(p.out) + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 4 * k;
         *reinterpret_cast<uint2*>(og) =
             make_uint2(P16::pack(o[0] * inv, o[1] * inv), P16::pack(o[2] * inv, o[3] * inv));

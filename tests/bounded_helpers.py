@@ -121,10 +121,8 @@ def eps_p(dtype, parts=2):
 
 
 def eps_prefill(dtype):
-    """The prefill's probabilities have one 16-bit part; part of the exponentials
-    come from a polynomial of relative error 1.02e-4 (bfloat16) or 2.9e-6
-    (binary16), once in a weight and once in the sum that divides it."""
-    return eps_p(dtype, 1) + 2 * (1.02e-4 if dtype == torch.bfloat16 else 2.9e-6)
+    """The windowed prefill's probabilities have one 16-bit part."""
+    return eps_p(dtype, 1)
 
 
 def check(got, want, bound, what):

@@ -380,6 +380,57 @@ def test_prefill_window(pkv, combo, window, sinks):
         at += new[s]
 
 
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 3.0])
+def test_scales_of_either_sign(pkv, scale):
+    """A negative scale turns the order of the scores, zero makes them equal."""
+    c = Cache((300, 40), 1, 2, 64, 16, "f16", seed=9)
+    c.scale = scale
+    new = [140, 40]
+    q = torch.randn(sum(new), c.H, 64, device=DEV).half()
+    out = run_prefill(pkv, c, new, 130, 4, q)
+    dec = run_window(pkv, c, 130, 4)
+    for s, L in enumerate(c.lens):
+        for i in (0, 1, new[s] - 1):
+            want, _, bound, _ = attend(q[140 * s + i], c.rows_k[s], c.rows_v[s],
+                                       seen_by(L, L - new[s] + i, 130, 4), scale, eps_prefill(c.dtype))
+            check(out[140 * s + i], want, bound, f"prefill {s} {i}")
+    check_window(c, dec, 130, 4, "decode")
+
+
+@pytest.mark.parametrize("at", [0, 29, 59])
+def test_prefill_window_one_long_among_short(pkv, at):
+    """A grid for the longest sequence, in which most work items have no rows; one
+    sequence's lengths are wrong, a bound far above every length changes nothing."""
+    lens = [5 + (7 * s) % 40 for s in range(60)]
+    lens[at] = 1400
+    c = Cache(lens, 4, 4, 64, 16, "bf16", seed=at)
+    new = [1 + s % 3 for s in range(60)]
+    new[at] = 1400
+    wrong = 30
+    c.context[wrong] = -1
+    q = torch.randn(sum(new), c.H, 64, device=DEV).to(c.dtype)
+    start = [sum(new[:s]) for s in range(61)]
+    outs = []
+    for bound in (1400, 1 << 30):
+        err = new_err()
+        out = torch.full_like(q, 7.0)
+        pkv.paged_attention_prefill_window(out, q, c.k, c.v, c.tables, c.context,
+                                           torch.tensor(start, dtype=torch.int32, device=DEV), c.scale, 100, 4,
+                                           bound, err)
+        assert err.item() == pkv.DEV_ERR_CONTEXT_LEN
+        outs.append(out)
+    assert torch.equal(*outs)
+    for s, L in enumerate(lens):
+        got = outs[0][start[s]:start[s + 1]]
+        if s == wrong:
+            assert (got == 7.0).all()
+            continue
+        for i in sorted({0, new[s] // 2, new[s] - 1}):
+            want, _, bound, _ = attend(q[start[s] + i], c.rows_k[s], c.rows_v[s],
+                                       seen_by(L, L - new[s] + i, 100, 4), c.scale, eps_prefill(c.dtype))
+            check(got[i], want, bound, f"{s} {i}")
+
+
 def test_prefill_window_last_query_sees_what_decode_shows(pkv):
     c = Cache((900, 77), 2, 4, 128, 16, "bf16")
     new = [300, 77]
