@@ -14,8 +14,12 @@ namespace {
 
 // Pieces of a segment: long enough that its start and join do not count, many
 // enough that the last wave of CTAs is a small part of all (kWaveCtas: CTAs that
-// are resident at a time).
-constexpr int64_t kWaveCtas = 152 * 3, kWaves = 5;
+// are resident at a time). 64 sequences, window 4096 / 8 sequences of up to 32768
+// with scores: 170 / 142 us with 4 waves, 173 / 141 with 3, 175 / 145 with 5, 181 / 148 with 6.
+// At least kMinTiles: one sequence, window 1024: 7.5 us, 10.5 with 16. At most kMaxTiles,
+// for the one long sequence of a batch that is sized by its length (131072 tokens beside
+// 127 x 100: 227 us with 16 pieces, 1295 with the 2 that an equal share of tiles gives).
+constexpr int64_t kWaveCtas = 152 * 3, kWaves = 4;
 constexpr int kMinTiles = 4, kMaxTiles = 96;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -41,7 +45,7 @@ HeadParts head_parts(int group, bool f32) {
 
 struct WindowLayout {
   size_t counter = 0, ml = 0, o = 0, row_ml = 0, logits = 0, total = 0;
-  int64_t logit_stride = 0;
+  int64_t logit_stride = 0, pieces = 0;
 };
 
 // Counters of the segments, the pieces' partial results, and (scores) the
@@ -54,10 +58,11 @@ WindowLayout window_layout(int num_seqs, int num_heads, int num_kv_heads, int he
     return w;
   const size_t rows = (size_t)num_seqs * num_heads;  // at least as many as segments
   size_t off = align_up(rows * sizeof(int32_t), 256);
+  w.pieces = std::min(std::max(pkv::kWinRowPieces * (int64_t)rows, pkv::kWinPiecesLeast), pkv::kWinPiecesMost);
   w.ml = off;
-  off += align_up((size_t)pkv::kWinPieceRows * sizeof(float2), 256);
+  off += align_up((size_t)w.pieces * sizeof(float2), 256);
   w.o = off;
-  off += (size_t)pkv::kWinPieceRows * head_dim * sizeof(float);
+  off += (size_t)w.pieces * head_dim * sizeof(float);
   if (scores) {
     w.row_ml = off;
     off += align_up(rows * sizeof(float2), 256);
@@ -101,7 +106,7 @@ pkv_status launch_decode(pkv::WindowParams& p, float scale, int head_dim, pkv_dt
   const int64_t seen = std::min<int64_t>(p.max_context_len, (int64_t)p.window + p.sinks);
   const int64_t tiles = (seen + 15) / 16 + 2;
   const int64_t per = std::min<int64_t>(std::max<int64_t>(segments * tiles / (kWaves * kWaveCtas), kMinTiles), kMaxTiles);
-  const int64_t splits = std::min((tiles + per - 1) / per, pkv::kWinPieceRows / hp.heads / segments);
+  const int64_t splits = std::min((tiles + per - 1) / per, lay.pieces / hp.heads / segments);
   p.splits = (int)std::max<int64_t>(splits, 1);
   p.min_tiles = (int)per;
   p.counter = reinterpret_cast<int32_t*>(ws + lay.counter);

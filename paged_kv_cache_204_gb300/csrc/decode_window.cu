@@ -45,7 +45,10 @@ __global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const ScorePara
   const int s = blockIdx.z, g = blockIdx.y;
   const int L = min(max(__ldg(p.context_lens + s), 0), p.cap);
   const int64_t t0 = (int64_t)blockIdx.x * (kAddThreads * kAddTokens) + threadIdx.x;
-  if ((int64_t)blockIdx.x * (kAddThreads * kAddTokens) >= L) return;
+  if ((int64_t)blockIdx.x * (kAddThreads * kAddTokens) >= L) {
+    grid_dependency_wait();  // what follows in the stream waits for this grid only
+    return;
+  }
   const size_t row = (size_t)s * p.num_kv_heads + g;
   float sum[kAddTokens], old[kAddTokens];
 #pragma unroll

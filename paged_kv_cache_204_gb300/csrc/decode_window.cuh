@@ -17,10 +17,22 @@
 // maximum, exponential sum and output (online softmax, base 2); the CTA joins its
 // warps in shared memory, and the last CTA of a segment to finish joins the
 // pieces in their order (log-sum-exp), all in one launch.
-// Many short pieces, handed to the SMs as they come free, rather than one equal
-// run of tiles per resident CTA across the segments' borders: with several CTAs
-// on an SM the start and the join of one lie under the loads of the others (128
-// sequences x 40 heads, window 1004: 290 us against 384 us).
+//
+// Bound by memory: K and V of the visible tokens are read once, 4 to 32 operations to an
+// element. What keeps the reads coming (times of 128 sequences of up to 2048 tokens, 40
+// heads, window 1000 / 64 sequences of up to 32768, 64 query and 8 kv heads, window
+// 4096; bfloat16, head_dim 128):
+//  - asynchronous copies into shared-memory rings, 16 KB a warp, two tiles deep, three CTAs
+//    on an SM: 280 / 173 us. Three tiles and two CTAs: 288 / 180; rows from registers
+//    straight into the MMAs: 290 / 185.
+//  - pieces handed to the SMs as they come free, rather than one equal run of tiles per
+//    resident CTA across the segments' borders (307 / 175, and 10.3 instead of 7.4 us for one
+//    sequence): SMs differ in speed, and the start and the join of one CTA lie
+//    under the loads of the two beside it.
+//  - first pieces first and longest, so that the last ones to start are short: 173 -> 171,
+//    and 8 sequences of up to 32768 with scores 147 -> 143 us.
+// 280 us are 7.1 TB/s and 171 us 6.4 (a plain copy runs at 6.8). One sequence of 7001
+// tokens, window 1024: 7.4 us, the latency of table, rows, join and launch.
 #pragma once
 
 #include <type_traits>
@@ -32,7 +44,12 @@ namespace pkv {
 
 constexpr int kWinWarps = 4;
 constexpr int kWinThreads = kWinWarps * 32;
-constexpr int kWinPieceRows = 32768;  // partial results (pieces x heads) that a workspace holds
+constexpr float kWinFirst = 1.7f;     // length of a segment's first piece over the mean
+// Partial results (pieces x heads) that a workspace holds: kWinRowPieces for every query
+// head, within these bounds (16 to 128 MB at head_dim 128). Where one sequence is far longer
+// than the others it alone has to fill the GPU: 131072 tokens beside 127 sequences of
+// 100 take 141 us with 32 pieces, 227 with 16, 406 with 8 (124 on their own).
+constexpr int64_t kWinRowPieces = 32, kWinPiecesLeast = 32768, kWinPiecesMost = 262144;
 
 struct WindowParams {
   void* out;
@@ -576,8 +593,9 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   static_assert(Ring::kBytes >= HP * D * (int)sizeof(float), "room for a warp's result");
   if constexpr (kLogits) grid_launch_dependents();
 
-  const int piece = blockIdx.x % p.splits;
-  const int seg = blockIdx.x / p.splits;
+  const int segments = p.num_seqs * p.num_kv_heads * p.parts;
+  const int piece = blockIdx.x / segments;
+  const int seg = blockIdx.x - piece * segments;
   const int part = seg % p.parts;
   const int kvh = (seg / p.parts) % p.num_kv_heads;
   const int s = seg / p.parts / p.num_kv_heads;
@@ -591,8 +609,11 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   if (piece >= pieces) return;
   // in whole rounds of the warps
   const int rounds = (r.n + kWinWarps - 1) / kWinWarps;
-  const int begin = (int)((int64_t)rounds * piece / pieces) * kWinWarps;
-  const int end = min((int)((int64_t)rounds * (piece + 1) / pieces) * kWinWarps, r.n);
+  auto cut = [&](int j) {  // the lengths fall linearly, from kWinFirst to 2 - kWinFirst of their mean
+    const float x = (float)j / (float)pieces;
+    return j == pieces ? rounds : (int)((float)rounds * x * (kWinFirst - (kWinFirst - 1.f) * x));
+  };
+  const int begin = cut(piece) * kWinWarps, end = min(cut(piece + 1) * kWinWarps, r.n);
 
   unsigned char* mine = rings + warp * Ring::kBytes;
   Ring ring;

@@ -6,6 +6,13 @@
 // every number). The kept rows of K, V and the scores move to positions
 // 0 .. n - 1 in their order.
 //
+// Bound by memory: every score is read once and a kept one written, a kept row read and
+// written. With head_dim 128 in 16 bits: 64 sequences of 700 to 4000 tokens to 1001, 8 kv
+// heads: 106 us, 4.9 TB/s (8-token blocks: a row's neighbours in its block are 2 KB); 8 of
+// 16385 to 32768 to 8192, 32 kv heads: 396 us, 5.5 TB/s; of these the selection takes 16
+// and 47 us. One sequence of 2001 tokens to 1024: 8.7 us, the latency of two dependent
+// kernels.
+//
 // Two launches: evict_select_kernel, one CTA per (sequence, kv head), finds the
 // kept positions and moves the scores; evict_move_kernel moves the rows. The
 // second is a programmatic dependent of the first: it is set up while the
@@ -53,10 +60,9 @@ __device__ __forceinline__ uint64_t rank_of(uint32_t key, int t) {
 // bins of equal width (a power of two), the candidates are counted into them and
 // the bin that holds the k-th is the next interval; the width of the first comes
 // from the smallest and the largest score, so that the counts spread over the
-// bins whatever the scores' scale is (radix digits of the score's bits put most
-// scores of one magnitude into a few counters, whose atomics then queue: 50 us
-// instead of 15 for 256 rows of 16k-32k scores). Once at most kListMost candidates are left
-// each is compared with all others. Then one ordered pass: a warp counts the kept
+// bins whatever the scores' scale is (leading digits of the scores' bits put most
+// scores of one magnitude into a few counters, whose atomics then queue). Once at most kListMost candidates
+// are left each is compared with all others (64 to 512: no difference). Then one ordered pass: a warp counts the kept
 // tokens of its stretch by ballots, the counts of the warps before it give its
 // first place.
 template <int NT>
@@ -378,7 +384,8 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   const int64_t chains = (int64_t)p.num_seqs * p.num_kv_heads * 2;
   const int64_t chunks = ((p.budget < p.cap ? p.budget : p.cap) + rows - 1) / rows;
   // few (sequence, head, pool) triples: clusters of up to 8 CTAs share one, while
-  // that gives each SM no more than two CTAs and each CTA a chunk
+  // that gives each SM no more than two CTAs and each CTA a chunk (one sequence of
+  // 8 kv heads: 8.8 us, 9.9 with clusters of 4, 16.0 with none)
   int cluster = 1;
   while (cluster < 8 && chains * cluster * 2 <= 304 && cluster < chunks) cluster *= 2;
   return launch_with(evict_move_kernel<V, VPR>, dim3(2 * cluster, p.num_kv_heads, p.num_seqs), kMoveThreads, 0, stream,
@@ -388,6 +395,8 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+  // threads for a row's selection: 1024 / 512 for one row set of 2001 scores 10.3 / 8.7 us,
+  // for 512 rows of up to 4000 120 / 106 us, for 256 rows of up to 32768 396 / 404 us
   const cudaError_t e = p.cap > 8192 ? launch_select<1024>(p, stream) : launch_select<512>(p, stream);
   if (e != cudaSuccess) return e;
   switch (p.row_bytes) {
