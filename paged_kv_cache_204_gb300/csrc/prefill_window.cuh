@@ -19,6 +19,14 @@
 // P enters its product as one 16-bit part: its rounding is 2^-8 (bfloat16) or 2^-11 of
 // each weight at most and independent from weight to weight, so that it adds no more to a
 // row's output than the rounding of the output itself, whose largest is the same.
+// Bound by the MMAs for long walks: 8192 queries over a window of 2048 (32 query and 8 kv heads,
+// bfloat16, head_dim 128) take 213 us, 1130 TFLOP/s over the visible tokens (1956 are the
+// library product's). A step of 128 tokens for both A and B takes about 2900 cycles, 2048 of
+// them MMAs; what lies between is the way from S over the softmax (1400) and the waits to the
+// next MMA. Tiles that a row sees in part take twice as long, the start and the end
+// of a pair some 8000 cycles: of short walks they are most (8 sequences of up to
+// 1500 tokens, window 500, head_dim 64, 40 heads: 93 us). One chunk of 100 queries, window
+// 1024: 16 us.
 #pragma once
 
 #include <type_traits>
@@ -31,9 +39,12 @@ constexpr int kPwRows = 128;     // rows of a query tile = tensor-memory lanes
 constexpr int kPwTokens = 128;   // tokens of a K/V tile
 constexpr int kPwStages = 4;     // tiles in shared memory: two links of a V and a K tile
 constexpr int kPwSoft = 256;     // 2 softmax warpgroups
-constexpr int kPwThreads = kPwSoft + 96;  // + MMA warp, TMA warp, query-loading and clearing warp
+constexpr int kPwThreads = kPwSoft + 128;  // + MMA warp of A, TMA warp, clearing warp, MMA warp of B
 constexpr uint32_t kPwTmemCols = 512;     // S of A and B (128 columns each), O of A and B
-constexpr float kPwRescaleLog2 = 8.f;     // base of the running max moves only when it grows by more
+constexpr float kPwRescaleLog2 = 8.f;     // base of the running max moves only when it grows by more (with 0: 9 % slower)
+// CTAs to a cluster at most. One chunk of 100 queries, window 1024: 26 us with 1, 21 with 2,
+// 16 with 4; of clusters of 8 no more than 15 are resident at a time, so that 16 items
+// would take two rounds.
 constexpr int kPwMaxCluster = 4;
 
 // n / d for 0 <= n < 2^31 and 1 <= d < 2^31 as a product and a shift: with
@@ -116,6 +127,19 @@ struct PwShape {
   static constexpr int kJoinMl = 2 * kPwRows * D * 4;
   static_assert(kJoinMl + 2 * kPwRows * 8 <= kBarOff, "room for the join");
 };
+
+// mbar_wait_bounded with the clock left alone until the hardware's own wait has run out once
+// (two readings of the global timer before it made every wait that had to wait late).
+__device__ __forceinline__ bool pw_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_test_wait(bar, parity)) return true;
+  if (limit_ns == 0) return false;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (globaltimer_ns() - t0 < limit_ns);
+  return false;
+}
 
 __device__ __forceinline__ uint32_t pw_cluster_rank() {
   uint32_t r;
@@ -326,13 +350,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   // 2 (c % 2) (K) and 2 (c % 2) + 1 (V).
   uint64_t* full = bars;         // [2] the link landed
   uint64_t* ready = bars + 2;    // [2] and rows of its V that no query sees are cleared
-  uint64_t* empty = bars + 4;    // [2] the MMAs are done with it
+  uint64_t* empty = bars + 4;    // [2] the MMAs are done with it (A's and B's: two arrivals)
   uint64_t* s_full = bars + 6;   // [A, B] S computed
   uint64_t* p_full = bars + 8;   // [A, B] P written (one arrival per softmax warp)
-  uint64_t* q_full = bars + 10;  // [A, B] query rows in place (one arrival per loading thread)
-  uint64_t* q_empty = bars + 12; // [A, B] the pair's last S computed
-  uint64_t* o_full = bars + 14;  // [A, B] the pair's last O computed
-  uint64_t* drained = bars + 16; // every MMA of the CTA done
+  uint64_t* q_full = bars + 10;  // [A, B] query rows in place (one arrival per softmax warp)
+  uint64_t* o_full = bars + 12;  // [A, B] the pair's last O computed
+  uint64_t* drained = bars + 14; // every MMA of the CTA done (two arrivals)
+  uint64_t* turn = bars + 15;    // [A, B] the other's MMAs of a link are issued
   uint32_t* slot = reinterpret_cast<uint32_t*>(sm + S::kSlotOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -343,7 +367,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   // ---- set-up: barriers, tensor memory ----------------------------------------
   if (tid == 0) {
-    for (int i = 0; i < 17; ++i) mbar_init(&bars[i], i == 8 || i == 9 ? 4 : (i == 10 || i == 11 ? 32 : 1));
+    for (int i = 0; i < 17; ++i) mbar_init(&bars[i], i == 4 || i == 5 || i == 14 ? 2 : (i >= 8 && i < 12 ? 4 : 1));
     mbar_init_fence();
   }
   if (warp == 8) tmem_alloc(slot, kPwTmemCols);
@@ -389,7 +413,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
         id = fetch(j + 1);
         if (link >= 2 &&
-            !__all_sync(kFullMask, mbar_wait_bounded(&empty[c], ((link >> 1) + 1) & 1, p.wait_limit_ns))) {
+            !__all_sync(kFullMask, pw_wait(&empty[c], ((link >> 1) + 1) & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
@@ -410,48 +434,53 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (lane == 0)
       for (uint32_t c = link >= 2 ? link - 2 : 0; c < link; ++c) {
         mbar_wait_bounded(&full[c & 1], (c >> 1) & 1, kDrainLimitNs);
-        if (!bad) mbar_wait_bounded(&empty[c & 1], (c >> 1) & 1, p.wait_limit_ns);
+        if (!bad) pw_wait(&empty[c & 1], (c >> 1) & 1, p.wait_limit_ns);
       }
     __syncwarp();
-  } else if (warp == 8) {
-    // ---- MMA issue -----------------------------------------------------------------
-    // Order: S_A(0), S_B(0), then per tile O_A += P_A V, S_A of the next tile, and the
-    // same for B: in turn, so that A's softmax runs under B's MMAs and the other way round
-    // (with a warp for each of A and B both fell into step and the tensor pipe idled
-    // under both softmaxes). MMAs complete in that order, so S may take the place of a P that the
-    // MMA before it reads, and "S done" says that O holds every earlier tile.
-    // The whole warp walks and waits, one elected lane issues; what a step needs to know
-    // is worked out before its wait, since the pipe holds only a few MMAs ahead.
+  } else if (warp == 8 || warp == 11) {
+    // ---- MMA issue, a warp for each of A and B ------------------------------------------
+    // Per link: O += P V of one tile, S of the next. At head_dim 128 the two take turns, A
+    // first, so that A's softmax runs under B's MMAs and the other way round: without turns
+    // both fall into step and the tensor pipe idles under both softmaxes. The pipe holds no
+    // more than an MMA or two ahead, so that what comes between one's MMAs and the other's
+    // leaves it idle: each makes its waits, and works out its next step, under the other's
+    // MMAs (one warp for both: 224 us instead of 213 for 8192 queries, window 2048, 32 query
+    // and 8 kv heads). At head_dim 64 the MMAs are half as long as the exponentials, and both
+    // may go as they are ready (93 us, 96 with turns, for 8 sequences of 40 heads).
+    // MMAs of one thread complete in order, so S may take the place of a P that the MMA
+    // before it reads, and "S done" says that O holds every earlier tile.
+    // The whole warp walks and waits, one elected lane issues; what a step needs to know is
+    // worked out before its wait.
+    const int x = warp == 8 ? 0 : 1;
+    constexpr bool kTurns = D == 128;
     constexpr uint32_t id_s = mma_idesc_f16(kPwRows, kPwTokens, kBf16, 0);
     constexpr uint32_t id_o = mma_idesc_f16(kPwRows, D, kBf16, 1);
     const uint32_t tb = __shfl_sync(kFullMask, tbase, 0);
     const uint32_t sb = __shfl_sync(kFullMask, smem_u32(sm), 0);
     // of a descriptor only the start address in its low word moves (shared addresses stay
     // below 256 KB, so the sums never carry out of the field)
-    const uint32_t qd = (uint32_t)smem_desc_sw128(sb, 16, 1024);
+    const uint32_t qd = (uint32_t)smem_desc_sw128(sb + x * S::kTile, 16, 1024);
     const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
     const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
     const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
-    uint32_t link = 0, nth = 0;  // links and pairs so far
-    uint32_t done = 0;           // parities of the P of A and B so far, as bits
+    uint32_t link = 0, nth = 0, done = 0;  // links, pairs and P's so far
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool ok = __all_sync(kFullMask, mbar_wait_bounded(bar, parity, p.wait_limit_ns));
+      const bool ok = __all_sync(kFullMask, pw_wait(bar, parity, p.wait_limit_ns));
       tc_fence_after();
       return ok;
     };
-    // within one elected region: S into the place of x's scores ...
-    auto mmas_s = [&](int x, uint32_t c, bool last) {
-      const uint32_t kb = kd + (c * (2 * S::kTile) >> 4), qb = qd + (x * S::kTile >> 4);
+    // within one elected region: S into the place of the scores ...
+    auto mmas_s = [&](uint32_t c) {
+      const uint32_t kb = kd + (c * (2 * S::kTile) >> 4);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
-        pw_mma_ss(tb + 128 * x, qb + off, kb + off, hi, id_s, ks > 0);
+        pw_mma_ss(tb + 128 * x, qd + off, kb + off, hi, id_s, ks > 0);
       }
       mma_commit(&s_full[x]);
-      if (last && cluster == 1) mma_commit(&q_empty[x]);
     };
     // ... and O += P V
-    auto mmas_o = [&](int x, uint32_t c, bool first) {
+    auto mmas_o = [&](uint32_t c, bool first) {
       const uint32_t vb = vd + (c * (2 * S::kTile) >> 4);
 #pragma unroll
       for (int ks = 0; ks < kPwTokens / 16; ++ks)
@@ -464,48 +493,38 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     for (int item; !bad && scan.next(p, step, items, item);) {
       it.load(p, item, rank);
       const int tiles = it.walk.j1 - it.walk.j0;
-      // the last tiles that A and B see, as token positions; bits x: the tile at hand is
-      // seen, O holds something
-      const int last_a = (it.span_a.end - 1) & ~(kPwTokens - 1), last_b = (it.span_b.end - 1) & ~(kPwTokens - 1);
-      uint32_t sees = 0, opened = 0;
+      const PwSpan span = it.span(x);
+      bool sees = false, opened = false;                   // the tile at hand is seen, O holds something
       // rows that no S of this part needs are in place before the pair ends all the same
-      bad = !wait(&q_full[0], nth & 1) || !wait(&q_full[1], nth & 1);
+      bad = !wait(&q_full[x], nth & 1);
       int k1 = 0;  // the tile whose S is next
-      uint32_t next = 0;
+      bool next = false;
       auto look = [&](int i) {
         k1 = i < tiles ? it.walk.tile(it.walk.j0 + i) * kPwTokens : 0;
-        next = i < tiles ? (uint32_t)it.span_a.sees(k1, p.sinks) | (uint32_t)it.span_b.sees(k1, p.sinks) << 1 : 0u;
+        next = i < tiles && span.sees(k1, p.sinks);
       };
       look(0);
       for (int i = tiles > 0 ? 0 : 1; i <= tiles && !bad; ++i, ++link) {  // O of tile i - 1, S of tile i
         const uint32_t c = link & 1;
         bad = !wait(&ready[c], (link >> 1) & 1);
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const bool o = sees >> x & 1, sx = next >> x & 1;
-          // (a pair's first P comes from warps that have read the O of the pair before)
-          if (!bad && o) {
-            bad = !wait(&p_full[x], done >> x & 1);
-            done ^= 1u << x;
-          }
-          if (!bad && elect_one()) {
-            if (o) mmas_o(x, c, !(opened >> x & 1));
-            if (sx) mmas_s(x, c, k1 == (x ? last_b : last_a));
-            // the link comes back with B's S (the softmax sees to that), or here
-            if (x == 1 && !sx) mma_commit(&empty[c]);
-          }
-          __syncwarp();
+        if (kTurns && !bad && (x == 1 || link > 0)) bad = !wait(&turn[x], (link + (x ^ 1)) & 1);
+        // (a pair's first P comes from warps that have read the O of the pair before)
+        if (!bad && sees) bad = !wait(&p_full[x], done++ & 1);
+        if (!bad && elect_one()) {
+          if (sees) mmas_o(c, !opened);
+          if (next)
+            mmas_s(c);
+          else
+            mma_commit(&empty[c]);  // (with an S the softmax sees to that)
+          if (kTurns) mbar_arrive(&turn[x ^ 1]);
         }
+        __syncwarp();
         opened |= sees;
         sees = next;
         look(i + 1);
       }
       if (!bad && elect_one()) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (cluster == 1 && it.span(x).end == 0) mma_commit(&q_empty[x]);
-          mma_commit(&o_full[x]);
-        }
+        mma_commit(&o_full[x]);
       }
       __syncwarp();
       ++nth;
@@ -517,56 +536,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     mbar_wait_bounded(drained, 0, kDrainLimitNs);
     __syncwarp();
   } else if (warp == 10) {
-    // ---- query rows, in 16-byte chunks, 128 bytes by 8 lanes; then the pair's links
+    // ---- the links: rows of a V tile that no query sees may hold anything (a NaN would
+    // survive a zero weight), they become zeros
     PwItem it;
     PwScan scan;
     scan.look(p, item0, step, items, false);
     const T* q = static_cast<const T*>(p.q);
-    uint32_t nth = 0, link = 0;  // pairs and links so far
+    uint32_t link = 0;  // links so far
     for (int item; !bad && scan.next(p, step, items, item);) {
       it.load(p, item, rank);
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (nth > 0 && !__all_sync(kFullMask, mbar_wait_bounded(&q_empty[x], (nth + 1) & 1, p.wait_limit_ns))) {
-          bad = true;
-          break;
-        }
-        const int active = max(min(it.rows - it.row0 - x * kPwRows, kPwRows), 0);
-        const int ch = lane & 7;
-#pragma unroll 4
-        for (int rr = lane >> 3; rr < kPwRows; rr += 4) {
-          if (active == 0) break;
-          const bool in = rr < active;
-          const int g = it.row0 + x * kPwRows + rr, t = in ? p.by_group.of(g) : 0, j = in ? g - t * p.group : 0;
-          const T* src = q + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 8 * ch;
-          const uint32_t to = smem_u32(sm + x * S::kTile) + rr * 128 + ((ch ^ (rr & 7)) << 4), bytes = in ? 16 : 0;
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + cb * S::kColBlock),
-                         "l"(src + cb * 64), "r"(bytes)
-                         : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-      if (bad) break;
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      if (p.flip != 0u) {  // a negative scale: the queries change their sign instead
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-        for (int e = lane; e < 2 * S::kTile / 4; e += 32) reinterpret_cast<uint32_t*>(sm)[e] ^= p.flip;
-        __syncwarp();
-      }
-      fence_async_smem();
-      mbar_arrive(&q_full[0]);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      fence_async_smem();
-      mbar_arrive(&q_full[1]);
-      ++nth;
-      // the links: rows of a V tile that no query sees may hold anything (a NaN would
-      // survive a zero weight), they become zeros
       for (int j = it.walk.j0; j <= it.walk.j1 && it.walk.j0 < it.walk.j1; ++j, ++link) {
         const uint32_t c = link & 1;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(&full[c], (link >> 1) & 1, p.wait_limit_ns))) {
+        if (!__all_sync(kFullMask, pw_wait(&full[c], (link >> 1) & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
@@ -600,10 +581,6 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
       }
     }
-    // the last pair's rows are handed back before the CTA can leave
-    if (!bad && nth > 0 && cluster == 1 && lane == 0)
-      for (int x = 0; x < 2; ++x) mbar_wait_bounded(&q_empty[x], (nth + 1) & 1, p.wait_limit_ns);
-    __syncwarp();
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
   } else {
     // ---- softmax: warpgroup x serves query tile x, a row to a thread --------------------
@@ -625,7 +602,45 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
       return false;
     };
+    // The pair's query rows, 16 bytes a copy, 128 bytes of a row by 8 lanes. S of the pair before
+    // is over, so their place is free.
+    const uint32_t q_at = smem_u32(sm + x * S::kTile), q_row = 32 * (warp & 3) + (lane >> 3), ch = lane & 7;
+    auto copy_q = [&]() {
+      const T* q = static_cast<const T*>(p.q);
+      const int active = x ? it.active_b : it.active_a;
+#pragma unroll 4
+      for (int rr = q_row; rr < 32 * (warp & 3) + 32; rr += 4) {
+        const bool in = rr < active;
+        const int g = it.row0 + x * kPwRows + rr, t = in ? p.by_group.of(g) : 0, j = in ? g - t * p.group : 0;
+        const T* src = q + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 8 * ch;
+        const uint32_t to = q_at + rr * 128 + ((ch ^ (rr & 7)) << 4), bytes = in ? 16 : 0;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + cb * S::kColBlock),
+                       "l"(src + cb * 64), "r"(bytes)
+                       : "memory");
+      }
+    };
+    auto copied_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.flip != 0u) {  // a negative scale: the queries change their sign instead
+        for (int e = 0; e < 8 * CB; ++e) {
+          const int rr = q_row + 4 * (e / CB);
+          uint4* at = reinterpret_cast<uint4*>(sm + x * S::kTile + (e % CB) * S::kColBlock + rr * 128 +
+                                               ((ch ^ (rr & 7)) << 4));
+          const uint4 f = *at;
+          *at = make_uint4(f.x ^ p.flip, f.y ^ p.flip, f.z ^ p.flip, f.w ^ p.flip);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[x]);
+    };
     bool have = find();
+    if (have) {
+      copy_q();
+      copied_q();
+    }
     while (have) {
       const int active = x ? it.active_b : it.active_a;
       const PwSpan span = it.span(x);
@@ -641,13 +656,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const int before = pos - p.window + 1 - k0;  // tokens of the tile before its window
         const bool cut = __any_sync(kFullMask, vis < kPwTokens || before > 0);
         // every wait is made warp-uniform before the warp-collective loads and stores
-        if (!__all_sync(kFullMask, mbar_wait_bounded(&s_full[x], done & 1, p.wait_limit_ns))) {
+        if (!__all_sync(kFullMask, pw_wait(&s_full[x], done & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
         tc_fence_after();
-        // B's S is the last MMA that reads its link
-        if (warp == 4 && lane == 0) mbar_arrive(&empty[(link + (j - it.walk.j0)) & 1]);
+        // S is the query tile's last MMA that reads its link
+        if ((warp & 3) == 0 && lane == 0) mbar_arrive(&empty[(link + (j - it.walk.j0)) & 1]);
         uint32_t u[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, u[c]);
@@ -725,12 +740,15 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               ((size_t)(it.q0 + tok) * p.num_heads + it.kvh * p.group + (g - tok * p.group)) * D;
       item += step;
       have = find();
-      if (!bad && !__all_sync(kFullMask, mbar_wait_bounded(&o_full[x], nth & 1, p.wait_limit_ns))) bad = true;
+      if (have && !bad) copy_q();
+      if (!bad && !__all_sync(kFullMask, pw_wait(&o_full[x], nth & 1, p.wait_limit_ns))) bad = true;
       if (bad) break;
       tc_fence_after();
+      // (the issuing warp has had the rows of this pair)
+      if (have) copied_q();
       if (cluster == 1) {
         if (active > 0) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = 1.f / l;  // a row whose every logit is -inf: 0 / 0, as the formula has it
           // 64 dims at a time through the warp's 4 KB (16-byte chunk k of row r at k ^ (r & 7)),
           // so that a store covers whole lines: a row to a lane, each store touched 32
           // lines and the pair's stores kept the memory pipe for 4000 cycles
@@ -768,7 +786,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         // A cluster has one pair only. This part's O and (m, l) go into shared memory, in
         // place of Q, K and V, once every MMA of both A and B, and so every copy that one
         // reads, is over.
-        if (!__all_sync(kFullMask, mbar_wait_bounded(&o_full[x ^ 1], nth & 1, p.wait_limit_ns))) {
+        if (!__all_sync(kFullMask, pw_wait(&o_full[x ^ 1], nth & 1, p.wait_limit_ns))) {
           bad = true;
           break;
         }
@@ -794,6 +812,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       ++nth;
     }
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   }
 
@@ -834,7 +853,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           o[0] = fmaf(a[c].x, f, o[0]), o[1] = fmaf(a[c].y, f, o[1]);
           o[2] = fmaf(a[c].z, f, o[2]), o[3] = fmaf(a[c].w, f, o[3]);
         }
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = 1.f / lt;
         const int t = p.by_group.of(g), j = g - t * p.group;
         T* og = static_cast<T*>(p.out) + ((size_t)(it.q0 + t) * p.num_heads + it.kvh * p.group + j) * D + 4 * k;
         *reinterpret_cast<uint2*>(og) =

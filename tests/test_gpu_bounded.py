@@ -397,6 +397,24 @@ def test_scales_of_either_sign(pkv, scale):
     check_window(c, dec, 130, 4, "decode")
 
 
+@pytest.mark.parametrize("D,Hkv", [(64, 1), (128, 160)])  # a cluster shares a pair of query tiles, or none does
+def test_prefill_window_logits_of_infinity(pkv, D, Hkv):
+    """Logits of -inf have weight zero; where a query sees nothing else, 0 / 0."""
+    c = Cache((200,), Hkv, 1, D, 16, "f16")
+    c.rows_k[0][:, :35, 0] = float("-inf")
+    c.put(c.k, 0, torch.arange(200), c.rows_k[0])
+    q = torch.randn(200, c.H, D, device=DEV).half()
+    q[:, :, 0] = 1.0
+    out = run_prefill(pkv, c, [200], 20, 0, q)
+    assert torch.isnan(out[:35]).all()
+    for i in range(35, 200, 7):
+        seen = seen_by(200, i, 20, 0) & (torch.arange(200) >= 35)
+        want, _, bound, _ = attend(q[i], c.rows_k[0], c.rows_v[0], seen, c.scale, eps_prefill(c.dtype))
+        check(out[i], want, bound, f"query {i}")
+    c.q, c.lens[0], c.context[0] = q[29:30], 30, 30
+    assert torch.isnan(run_window(pkv, c, 20, 0)).all()
+
+
 @pytest.mark.parametrize("at", [0, 29, 59])
 def test_prefill_window_one_long_among_short(pkv, at):
     """A grid for the longest sequence, in which most work items have no rows; one
