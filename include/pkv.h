@@ -486,8 +486,11 @@ size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_heads, int num_kv
  * t < num_sinks or t > P - window, so the last query of a call sees what
  * pkv_paged_attention_decode_window would show it. Arguments and errors as in
  * pkv_paged_attention_prefill, plus PKV_ERR_INVALID_ARG for window < 1 or
- * num_sinks < 0. Block-table entries of blocks that no query of the call sees
- * need not be valid. V rows of tokens that some query of the call sees must
+ * num_sinks < 0. With R = min(max_query_len, tokens of a table) * num_heads /
+ * num_kv_heads: PKV_ERR_UNSUPPORTED for R above 2^31 - 256, or
+ * ceil(R / 256) * num_seqs * num_kv_heads above 2^30.
+ * Block-table entries of blocks that no query of the call sees need not be
+ * valid. V rows of tokens that some query of the call sees must
  * be finite (an infinity or a NaN there may also reach queries that do not
  * see the token); rows that no query sees may hold anything. */
 pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -508,8 +511,8 @@ pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const vo
  * with L == 0 (an idle row of a fixed batch) has none.
  *
  *   scores      float [num_seqs][num_kv_heads][score_stride], or NULL
- *   scores_out  the same shape; the same address as scores (in place) or no
- *               byte in common with it
+ *   scores_out  the same shape; the same address as scores (in place), or a
+ *               range (first to last row) that has no byte in common with it
  *   score_stride  >= max_context_len
  *   workspace   at least pkv_decode_scores_workspace_bytes() bytes; zeroing and
  *               sharing as for pkv_paged_attention_decode_window
@@ -548,7 +551,8 @@ size_t pkv_decode_scores_workspace_bytes(int num_seqs, int num_heads, int num_kv
  *                 max_context_len; read
  *   scores_out    float [num_seqs][num_kv_heads][out_stride], out_stride >=
  *                 min(budget, max_context_len); the same address and stride as
- *                 scores (in place) or no byte in common with it
+ *                 scores (in place), or a range (first to last row) that has no
+ *                 byte in common with it
  *   dst_block_tables  int32 [num_seqs][max_blocks_per_seq]: the blocks that hold
  *                 the result (the first ceil(n / block_size) entries of a row).
  *                 Each entry is the entry of block_tables at the same place, a

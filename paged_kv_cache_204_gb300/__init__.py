@@ -353,9 +353,12 @@ def decode_scores_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: i
 
 def new_window_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                          device="cuda") -> torch.Tensor:
-    """A zeroed workspace of paged_attention_decode_window."""
+    """A workspace of paged_attention_decode_window: its counters zeroed, the
+    room for partial results as it comes."""
     n = decode_window_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:4 * num_seqs * num_heads].zero_()
+    return ws
 
 
 def new_scores_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, max_context_len: int,

@@ -609,9 +609,12 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   if (piece >= pieces) return;
   // in whole rounds of the warps
   const int rounds = (r.n + kWinWarps - 1) / kWinWarps;
-  auto cut = [&](int j) {  // the lengths fall linearly, from kWinFirst to 2 - kWinFirst of their mean
-    const float x = (float)j / (float)pieces;
-    return j == pieces ? rounds : (int)((float)rounds * x * (kWinFirst - (kWinFirst - 1.f) * x));
+  // The lengths fall linearly, from kWinFirst to 2 - kWinFirst of their mean. One CTA's end
+  // has to be the next one's begin, so no operation may be fused into another.
+  auto cut = [&](int j) {
+    const float x = __fdiv_rn((float)j, (float)pieces);
+    const float part = __fmul_rn(x, __fsub_rn(kWinFirst, __fmul_rn(kWinFirst - 1.f, x)));
+    return j == pieces ? rounds : (int)__fmul_rn((float)rounds, part);
   };
   const int begin = cut(piece) * kWinWarps, end = min(cut(piece + 1) * kWinWarps, r.n);
 

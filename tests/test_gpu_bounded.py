@@ -724,3 +724,54 @@ def test_session(pkv, dtype):
     check(out[0], want, bound, "system prompt")
     assert int(err.item()) == 0
     bm.close()
+
+
+# ---- far blocks, calls at once ------------------------------------------------------------------
+
+
+def test_blocks_beyond_32_bit_offsets(pkv):
+    """Pools of more than 2^31 elements: the same rows in the last blocks give
+    what they give in a small pool, bit for bit."""
+    c = Cache((1000, 333), 8, 4, 128, 32, "bf16", seed=4)
+    far = 65536 + 200 - c.nb                              # 65736 blocks x 8 x 32 x 128 elements
+    k = torch.empty((far + c.nb, 8, 32, 128), dtype=c.dtype, device=DEV)
+    v = torch.empty_like(k)
+    assert k.numel() > 1 << 31
+    k[far:], v[far:] = c.k, c.v
+    near, tables = c.tables, torch.where(c.tables >= 0, c.tables + far, c.tables)
+    q = torch.randn(333 + 50, c.H, 128, device=DEV).to(c.dtype)
+    sc = [torch.zeros(2, 8, 1000, device=DEV) for _ in range(2)]
+    results, results_pools = [], [(c.k, c.v)]
+    for pools, table, score in (((c.k, c.v), near, sc[0]), ((k, v), tables, sc[1])):
+        c.k, c.v = pools
+        c.tables = table
+        res = [run_window(pkv, c, 300, 4), run_prefill(pkv, c, [333, 50], 300, 4, q)]
+        res.append(run_scores(pkv, c, None, score))
+        kept = torch.zeros(2, 8, 200, dtype=torch.int32, device=DEV)
+        new = torch.zeros(2, dtype=torch.int32, device=DEV)
+        pkv.evict_tokens(c.k, c.v, score, score, table, table, c.context, new, kept, 4, 50, 1000)
+        results.append(res + [score, kept, new])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    for small, large in ((results_pools[0][0], k), (results_pools[0][1], v)):
+        assert torch.equal(small.view(torch.int16), large[far:].view(torch.int16))
+
+
+def test_two_calls_at_once(pkv):
+    """Two streams, a workspace each: what each call gives by itself."""
+    c = [Cache((9000, 40, 2500), 2, 4, 128, 16, "f16", seed=s) for s in (5, 6)]
+    alone = [(run_window(pkv, x, 3000, 4), run_scores(pkv, x, None, torch.zeros(3, 2, 9000, device=DEV))) for x in c]
+    ws = [(pkv.new_window_workspace(3, x.H, 2, 128), pkv.new_scores_workspace(3, x.H, 2, 128, 9000)) for x in c]
+    sc = [torch.zeros(3, 2, 9000, device=DEV) for _ in c]
+    out = [(torch.zeros_like(x.q), torch.zeros_like(x.q)) for x in c]
+    streams = [torch.cuda.Stream() for _ in c]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, w, s, o, st in zip(c, ws, sc, out, streams):
+            pkv.paged_attention_decode_window(o[0], x.q, x.k, x.v, x.tables, x.context, x.scale, 3000, 4, 9000, w[0],
+                                              stream=st)
+            pkv.paged_attention_decode_scores(o[1], s, x.q, x.k, x.v, x.tables, x.context, x.scale, 9000, w[1],
+                                              stream=st)
+    torch.cuda.synchronize()
+    for o, a in zip(out, alone):
+        assert torch.equal(o[0], a[0]) and torch.equal(o[1], a[1])
