@@ -8,9 +8,9 @@
 //
 // Bound by memory: every score is read once and a kept one written, a kept row read and
 // written. With head_dim 128 in 16 bits: 64 sequences of 700 to 4000 tokens to 1001, 8 kv
-// heads: 106 us, 4.9 TB/s (8-token blocks: a row's neighbours in its block are 2 KB); 8 of
-// 16385 to 32768 to 8192, 32 kv heads: 396 us, 5.5 TB/s; of these the selection takes 16
-// and 47 us. One sequence of 2001 tokens to 1024: 8.7 us, the latency of two dependent
+// heads: 106 us, 5.0 TB/s (8-token blocks: a row's neighbours in its block are 2 KB); 8 of
+// 16385 to 32768 to 8192, 32 kv heads: 390 us, 5.6 TB/s; of these the selection takes 16
+// and 41 us. One sequence of 2001 tokens to 1024: 8.3 us, the latency of two dependent
 // kernels.
 //
 // Two launches: evict_select_kernel, one CTA per (sequence, kv head), finds the
@@ -30,6 +30,8 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kListMost = 128;          // candidates that are ranked one against all
 constexpr int kScoresInSmem = 32768;    // scores of a row that are kept in shared memory
+constexpr int kFewScores = 8192;         // rows up to this long: kSelectFew threads, else kSelectMost
+constexpr int kSelectFew = 512, kSelectMost = 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;          // vectors per thread and chunk
 
@@ -62,13 +64,13 @@ __device__ __forceinline__ uint64_t rank_of(uint32_t key, int t) {
 // from the smallest and the largest score, so that the counts spread over the
 // bins whatever the scores' scale is (leading digits of the scores' bits put most
 // scores of one magnitude into a few counters, whose atomics then queue). Once at most kListMost candidates
-// are left each is compared with all others (64 to 512: no difference). Then one ordered pass: a warp counts the kept
-// tokens of its stretch by ballots, the counts of the warps before it give its
-// first place.
+// are left each is compared with all others (64 to 512: no difference). The pass that lists
+// them also notes what lies above, a bit per token; a warp counts the bits of its
+// stretch, and the counts of the warps before it give its first place.
 template <int NT>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, int smem_scores) {
   constexpr int NW = NT / 32;
-  extern __shared__ float sm[];  // smem_scores (a multiple of 32) scores, then a bit for each
+  extern __shared__ __align__(16) float smem[];  // smem_scores (a multiple of 32) scores and 4 more, then a bit for each
   __shared__ uint32_t hist[kBins];
   __shared__ uint64_t list[kListMost];
   __shared__ uint32_t warp_sum[NW];
@@ -98,21 +100,45 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
     sh_n = 0u;
   }
   for (int i = tid; i < kBins; i += NT) hist[i] = 0u;
+  // the row in 16-byte loads, `head` scores before them; in shared memory as aligned as there
+  const int head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) >> 2, L);
+  float* sm = smem + ((4 - head) & 3);
+  const int quads = (L - head) >> 2;
   __syncthreads();
   uint32_t kmin = 0xffffffffu, kmax = 0u;
-#pragma unroll 8
-  for (int t = tid; t < L; t += NT) {
-    const float x = row[t];
-    if (whole) sm[t] = x;
+  auto look = [&](float x, int t) {
     if (t >= first && t < last) {
       const uint32_t k = score_key(x);
       kmin = min(kmin, k);
       kmax = max(kmax, k);
     }
+  };
+#pragma unroll 4
+  for (int i = tid; i < quads; i += NT) {
+    const int t = head + 4 * i;
+    const float4 x = *reinterpret_cast<const float4*>(row + t);
+    if (whole) *reinterpret_cast<float4*>(sm + t) = x;
+    look(x.x, t);
+    look(x.y, t + 1);
+    look(x.z, t + 2);
+    look(x.w, t + 3);
+  }
+  for (int i = tid; i < L - 4 * quads; i += NT) {  // at most 6: before the 16-byte loads and behind
+    const int t = i < head ? i : i + 4 * quads;
+    const float x = row[t];
+    if (whole) sm[t] = x;
+    look(x, t);
   }
   const float* from = whole ? sm : row;
   uint64_t threshold = ~0ull;  // above every rank: no candidate is kept
-  uint32_t* kept_bits = reinterpret_cast<uint32_t*>(sm + smem_scores);  // of a stretch, a bit per token
+  uint64_t lo = ~0ull, hi = ~0ull;
+  uint32_t* kept_bits = reinterpret_cast<uint32_t*>(smem + smem_scores + 4);  // of a stretch, a bit per token
+  // a warp's tokens of a stretch of m: [w0, w1)
+  auto mine = [&](int m, int& w0, int& w1) {
+    const int per = (m + NT - 1) / NT * 32;
+    w0 = min(warp * per, m);
+    w1 = min(w0 + per, m);
+  };
   if (left > 0) {
     kmin = __reduce_min_sync(kFullMask, kmin);
     kmax = __reduce_max_sync(kFullMask, kmax);
@@ -121,7 +147,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
       atomicMax(&sh_max, kmax);
     }
     __syncthreads();
-    uint64_t lo = (uint64_t)sh_min << 32, hi = ((uint64_t)sh_max << 32) | 0xffffffffu;
+    lo = (uint64_t)sh_min << 32, hi = ((uint64_t)sh_max << 32) | 0xffffffffu;
     for (bool every = true;; every = false) {  // every: [lo, hi] holds all candidates
       const int width = 64 - __clzll((long long)(hi - lo));
       const int shift = width > 11 ? width - 11 : 0;
@@ -178,8 +204,33 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
       for (int i = tid; i < kBins; i += NT) hist[i] = 0u;
       __syncthreads();
     }
-    const int n = (int)sh_count;
-    const uint32_t klo = (uint32_t)(lo >> 32), khi = (uint32_t)(hi >> 32);
+  } else {
+    __syncthreads();  // the scores are in place
+  }
+  const uint32_t klo = (uint32_t)(lo >> 32), khi = (uint32_t)(hi >> 32);
+  if (whole) {
+    int w0, w1;
+    mine(L, w0, w1);
+#pragma unroll 4
+    for (int i = w0; i < w1; i += 32) {
+      const int t = i + lane;
+      bool above = false;
+      if (t < w1) {
+        above = true;
+        if (t >= first && t < last) {
+          const uint32_t k = score_key(from[t]);
+          above = k > khi;
+          if (k >= klo && k <= khi) {
+            const uint64_t r = rank_of(k, t);
+            above = r > hi;
+            if (r >= lo && r <= hi) list[atomicAdd(&sh_n, 1u)] = r;
+          }
+        }
+      }
+      const uint32_t b = __ballot_sync(kFullMask, above);
+      if (lane == 0) kept_bits[i >> 5] = b;
+    }
+  } else if (left > 0) {
 #pragma unroll 8
     for (int t = first + tid; t < last; t += NT) {
       const uint32_t k = score_key(from[t]);
@@ -188,44 +239,59 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
         if (r >= lo && r <= hi) list[atomicAdd(&sh_n, 1u)] = r;
       }
     }
-    __syncthreads();
-    for (int i = tid; i < n; i += NT) {
-      const uint64_t r = list[i];
-      uint32_t larger = 0;
-      for (int j = 0; j < n; ++j) larger += list[j] > r;
-      if (larger == left - 1) sh_rank = r;
-    }
-    __syncthreads();
-    threshold = sh_rank;
   }
+  __syncthreads();
+  const int n = (int)sh_n;
+  for (int i = tid; i < n; i += NT) {
+    const uint64_t r = list[i];
+    uint32_t larger = 0;
+    for (int j = 0; j < n; ++j) larger += list[j] > r;
+    if (larger == left - 1) sh_rank = r;
+    if (whole && larger < left) {
+      const uint32_t t = ~(uint32_t)r;
+      atomicOr(&kept_bits[t >> 5], 1u << (t & 31));
+    }
+  }
+  __syncthreads();
+  if (left > 0) threshold = sh_rank;
 
-  // ordered pass, a stretch of smem_scores tokens at a time: its scores are all
-  // in shared memory before a place in it may be overwritten (scores in place)
+  // Ordered pass, a stretch of smem_scores tokens at a time: its scores are all
+  // in shared memory before a place in it may be overwritten (scores in place).
   int base = 0;
   for (int64_t c0 = 0; c0 < L; c0 += smem_scores) {
     const int m = (int)min((int64_t)smem_scores, L - c0);
+    int w0, w1;
+    mine(m, w0, w1);
     if (!whole) {
 #pragma unroll 8
       for (int t = tid; t < m; t += NT) sm[t] = row[c0 + t];
-    }
-    __syncthreads();
-    const int per = (m + NT - 1) / NT * 32;  // tokens of a warp
-    const int w0 = min(warp * per, m), w1 = min(w0 + per, m);
-    const uint32_t tkey = (uint32_t)(threshold >> 32), tpos = ~(uint32_t)threshold;
-    int count = 0;
+      __syncthreads();
+      const uint32_t tkey = (uint32_t)(threshold >> 32), tpos = ~(uint32_t)threshold;
 #pragma unroll 4
-    for (int i = w0; i < w1; i += 32) {
-      const int t = (int)c0 + i + lane;
-      bool k = false;
-      if (i + lane < w1) {
-        const uint32_t key = score_key(sm[i + lane]);
-        k = t < first || t >= last || key > tkey || (key == tkey && (uint32_t)t <= tpos);
+      for (int i = w0; i < w1; i += 32) {
+        const int t = (int)c0 + i + lane;
+        bool k = false;
+        if (i + lane < w1) {
+          const uint32_t key = score_key(sm[i + lane]);
+          k = t < first || t >= last || key > tkey || (key == tkey && (uint32_t)t <= tpos);
+        }
+        const uint32_t b = __ballot_sync(kFullMask, k);
+        if (lane == 0) kept_bits[i >> 5] = b;
       }
-      const uint32_t b = __ballot_sync(kFullMask, k);
-      if (lane == 0) kept_bits[i >> 5] = b;
-      count += __popc(b);
+      __syncwarp();
     }
-    if (lane == 0) warp_sum[warp] = (uint32_t)count;
+    // a lane's words of 32 tokens: their counts, and those of the lanes before it
+    static_assert((NT == kSelectMost ? kScoresInSmem : kFewScores) <= 32 * NT, "a word to a lane");
+    const bool has = w0 + 32 * lane < w1;
+    const uint32_t bits = has ? kept_bits[(w0 >> 5) + lane] : 0u;
+    int before = __popc(bits);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFullMask, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) warp_sum[warp] = (uint32_t)before;
+    before -= __popc(bits);
     __syncthreads();
     int at = base;
 #pragma unroll
@@ -236,13 +302,12 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictParams p, i
     }
 #pragma unroll 4
     for (int i = w0; i < w1; i += 32) {
-      const uint32_t b = kept_bits[i >> 5];
+      const uint32_t b = __shfl_sync(kFullMask, bits, (i - w0) >> 5);
+      const int to = at + __shfl_sync(kFullMask, before, (i - w0) >> 5) + __popc(b & ((1u << lane) - 1u));
       if (b >> lane & 1u) {
-        const int to = at + __popc(b & ((1u << lane) - 1u));
         kept[to] = (int)c0 + i + lane;
         out[to] = sm[i + lane];
       }
-      at += __popc(b);
     }
     __syncthreads();
   }
@@ -364,14 +429,14 @@ cudaError_t launch_with(K kernel, dim3 grid, int threads, size_t smem, cudaStrea
 template <int NT>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
   const int scores = p.cap < kScoresInSmem ? (p.cap / 32 + 1) * 32 : kScoresInSmem;
-  const size_t smem = (size_t)scores * 33 / 32 * sizeof(float);
+  const size_t smem = ((size_t)scores * 33 / 32 + 4) * sizeof(float);
   static int configured[64] = {0};  // per device ordinal
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
     e = cudaFuncSetAttribute(evict_select_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kScoresInSmem / 32 * 33 * (int)sizeof(float));
+                             (kScoresInSmem / 32 * 33 + 4) * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
   }
@@ -385,7 +450,7 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   const int64_t chunks = ((p.budget < p.cap ? p.budget : p.cap) + rows - 1) / rows;
   // few (sequence, head, pool) triples: clusters of up to 8 CTAs share one, while
   // that gives each SM no more than two CTAs and each CTA a chunk (one sequence of
-  // 8 kv heads: 8.8 us, 9.9 with clusters of 4, 16.0 with none)
+  // 8 kv heads: 8.3 us, 9.6 with clusters of 4, 15.7 with none)
   int cluster = 1;
   while (cluster < 8 && chains * cluster * 2 <= 304 && cluster < chunks) cluster *= 2;
   return launch_with(evict_move_kernel<V, VPR>, dim3(2 * cluster, p.num_kv_heads, p.num_seqs), kMoveThreads, 0, stream,
@@ -395,9 +460,10 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-  // threads for a row's selection: 1024 / 512 for one row set of 2001 scores 10.3 / 8.7 us,
-  // for 512 rows of up to 4000 120 / 106 us, for 256 rows of up to 32768 396 / 404 us
-  const cudaError_t e = p.cap > 8192 ? launch_select<1024>(p, stream) : launch_select<512>(p, stream);
+  // threads for a row's selection: 1024 for rows of up to kFewScores instead of 512 take 10.0
+  // us instead of 8.3 (one sequence of 2001) and 116 instead of 106 (64 of up to 4000); longer
+  // rows need them, a word of bits to a lane
+  const cudaError_t e = p.cap > kFewScores ? launch_select<kSelectMost>(p, stream) : launch_select<kSelectFew>(p, stream);
   if (e != cudaSuccess) return e;
   switch (p.row_bytes) {
     case 36: return launch_move<uint32_t, 9>(p, stream);

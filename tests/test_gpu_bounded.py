@@ -320,6 +320,30 @@ def test_evict_long_rows(pkv, values):
         assert torch.equal(flat(k)[:budget], flat(k0)[torch.tensor(keep, device=DEV)])
 
 
+@pytest.mark.parametrize("L", [8191, 8192, 8193, 32767, 32768, 32769])
+@pytest.mark.parametrize("recent", [0, 200])
+def test_evict_row_sizes(pkv, L, recent):
+    """Rows at the bounds of the selection's variants, at every alignment; with `recent`
+    the budget is spent, and no score decides."""
+    budget, Hkv = 204, 4
+    nb = -(-L // 32)
+    sc = torch.randn(1, Hkv, L + 1, device=DEV)              # a row begins 4 or more bytes off 16
+    want = [kept_of(sc[0, h].cpu().numpy(), L, budget, 4, recent) for h in range(Hkv)]
+    k = torch.randn(nb, Hkv, 32, 64, device=DEV).half()
+    v, k0 = k.clone(), k.clone()
+    tables = torch.arange(nb, dtype=torch.int32, device=DEV)[None]
+    kept = torch.zeros(1, Hkv, budget, dtype=torch.int32, device=DEV)
+    out = torch.zeros(1, Hkv, budget, device=DEV)
+    new = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.evict_tokens(k, v, sc, out, tables, tables, torch.tensor([L], dtype=torch.int32, device=DEV), new, kept, 4,
+                     recent, L)
+    for h in range(Hkv):
+        assert kept[0, h].tolist() == want[h]
+        at = torch.tensor(want[h], device=DEV)
+        assert torch.equal(out[0, h], sc[0, h, at])
+        assert torch.equal(k[:, h].reshape(-1, 64)[:budget], k0[:, h].reshape(-1, 64)[at])
+
+
 def test_evict_device_errors(pkv):
     c = Cache((300, 50), 2, 1, 64, 16, "f16")
     scores = torch.rand(2, 2, 300, device=DEV)
