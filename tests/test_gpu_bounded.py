@@ -190,6 +190,22 @@ def test_decode_scores(pkv, combo):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("n,off", [(1104, 0), (1104, 1), (1101, 0), (1101, 2)])
+@pytest.mark.parametrize("how", ["apart", "in_place"])
+def test_decode_scores_alignment(pkv, n, off, how):
+    """Score rows on and off 16 bytes, lengths that end anywhere in 4 tokens."""
+    c = Cache((1101, 1100, 1099, 1098, 1, 2, 0, 5), 2, 3, 64, 8, "bf16", seed=n)
+    rows = lambda: torch.full((8 * 2 * n + off,), float("nan"), device=DEV)[off:].view(8, 2, n)
+    old, new = rows(), rows()
+    for s, L in enumerate(c.lens):
+        old[s, :, :max(L - 1, 0)] = torch.rand(2, max(L - 1, 0), device=DEV)
+    before = old.clone()
+    if how == "in_place":
+        new = old
+    out = run_scores(pkv, c, old, new)
+    check_scores(c, out, before, new, how)
+
+
 @pytest.mark.parametrize("dtype,G", [("f16", 4), ("bf16", 7), ("f32", 1)])
 def test_decode_scores_long(pkv, dtype, G):
     c = Cache((20011, 0, 5000), 2, G, 128, 16, dtype, seed=8)
