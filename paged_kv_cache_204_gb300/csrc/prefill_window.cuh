@@ -16,17 +16,19 @@
 // Where there are few pairs, a cluster shares one: each of its CTAs walks a part
 // of the K/V tiles, and the parts are joined through the cluster's shared memory
 // (log-sum-exp).
-// P enters its product as one 16-bit part: its rounding is 2^-8 (bfloat16) or 2^-11 of
-// each weight at most and independent from weight to weight, so that it adds no more to a
-// row's output than the rounding of the output itself, whose largest is the same.
+// P enters its product as a 16-bit high part and a 16-bit remainder, two MMAs for one: 16
+// significant bits or more. One part, 2^-8 (bfloat16) or 2^-11 of each weight, would put an error
+// of its own beside the output's rounding (each is that fraction of the output, rms, whatever
+// the values' signs): 1.4 times the rounding's alone; it would take 218 us instead of 273 for
+// the 8192 queries below.
 // Bound by the MMAs for long walks: 8192 queries over a window of 2048 (32 query and 8 kv heads,
-// bfloat16, head_dim 128) take 213 us, 1130 TFLOP/s over the visible tokens (1956 are the
-// library product's). A step of 128 tokens for both A and B takes about 2900 cycles, 2048 of
-// them MMAs; what lies between is the way from S over the softmax (1400) and the waits to the
-// next MMA. Tiles that a row sees in part take twice as long, the start and the end
+// bfloat16, head_dim 128) take 273 us, 880 TFLOP/s over the visible tokens and 1320 with the
+// remainders' MMAs (1956 are the library product's). A step of 128 tokens for both A and B takes
+// about 3700 cycles, 3072 of them MMAs; what lies between is the way from S over the softmax and
+// the waits to the next MMA. Tiles that a row sees in part take longer, the start and the end
 // of a pair some 8000 cycles: of short walks they are most (8 sequences of up to
-// 1500 tokens, window 500, head_dim 64, 40 heads: 93 us). One chunk of 100 queries, window
-// 1024: 16 us.
+// 1500 tokens, window 500, head_dim 64, 40 heads: 115 us). One chunk of 100 queries, window
+// 1024: 20 us.
 #pragma once
 
 #include <type_traits>
@@ -89,6 +91,14 @@ struct PwPack<__half> {
     memcpy(&u, &h, 4);
     return u;
   }
+  // the high part of a pair of weights, packed, and what it stands for
+  __device__ __forceinline__ static uint32_t high(float2 e, float2& h) {
+    const __half2 r = __floats2half2_rn(e.x, e.y);
+    h = __half22float2(r);
+    uint32_t u;
+    memcpy(&u, &r, 4);
+    return u;
+  }
 };
 template <>
 struct PwPack<__nv_bfloat16> {
@@ -97,6 +107,13 @@ struct PwPack<__nv_bfloat16> {
     uint32_t u;
     memcpy(&u, &h, 4);
     return u;
+  }
+  // (cut off, which takes fewer instructions than rounding: the remainder is at most
+  // 2^-7 of the weight, its own rounding 2^-16)
+  __device__ __forceinline__ static uint32_t high(float2 e, float2& h) {
+    const uint32_t x = __float_as_uint(e.x), y = __float_as_uint(e.y);
+    h = make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u));
+    return __byte_perm(x, y, 0x7632);
   }
 };
 
@@ -483,9 +500,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     auto mmas_o = [&](uint32_t c, bool first) {
       const uint32_t vb = vd + (c * (2 * S::kTile) >> 4);
 #pragma unroll
-      for (int ks = 0; ks < kPwTokens / 16; ++ks)
-        pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 8 * ks, vb + (ks * 2048 >> 4), hi, id_o,
-                  (ks > 0 || !first) ? 1u : 0u);
+      for (int part = 0; part < 2; ++part)  // the high parts of P, then the remainders
+#pragma unroll
+        for (int ks = 0; ks < kPwTokens / 16; ++ks)
+          pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 64 * part + 8 * ks, vb + (ks * 2048 >> 4), hi, id_o,
+                    (part > 0 || ks > 0 || !first) ? 1u : 0u);
     };
     PwItem it;
     PwScan scan;
@@ -712,19 +731,24 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         first = false;
         const float nbase = m_use == -INFINITY ? 0.f : -m_use;
         const uint64_t sc2 = pw_pair(sc, sc), nb2 = pw_pair(nbase, nbase);
+        const uint64_t minus1 = pw_pair(-1.f, -1.f);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          uint32_t w[16], rest[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 e = pw_unpair(pw_fma2(pw_pair(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nb2));
             e.x = pw_exp2(e.x);
             e.y = pw_exp2(e.y);
             sum[i & 1] = pw_add2(sum[i & 1], pw_pair(e.x, e.y));
-            w[i] = P16::pack(e.x, e.y);
+            float2 h;
+            w[i] = P16::high(e, h);
+            h = pw_unpair(pw_fma2(pw_pair(h.x, h.y), minus1, pw_pair(e.x, e.y)));
+            rest[i] = P16::pack(h.x, h.y);
           }
           tmem_st16(ts + 16 * c, w);
+          tmem_st16(ts + 64 + 16 * c, rest);
         }
         tmem_wait_st();
         tc_fence_before();
