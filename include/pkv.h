@@ -462,9 +462,12 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_c
  *   window     >= 1; num_sinks >= 0 (may sum to more than a context)
  *   dtype      PKV_F32, PKV_F16 or PKV_BF16, of q, out and the caches
  *   workspace  at least pkv_decode_window_workspace_bytes() bytes; its first
- *              num_seqs * num_heads int32 must be zero before the first call and
- *              every call leaves them zero. Two calls that share a workspace
- *              must not overlap on the GPU.
+ *              PKV_WINDOW_COUNTER_BYTES must be zero before the first call (the
+ *              first num_seqs * num_heads int32 are enough where no later call
+ *              has more) and every call leaves them zero. One workspace
+ *              serves calls of any sizes that it is large enough for, of this
+ *              operator and of pkv_paged_attention_decode_scores, in any
+ *              order. Two calls that share a workspace must not overlap on the GPU.
  * All other arguments, layouts and errors as in pkv_paged_attention_decode,
  * but no wait can run out; PKV_ERR_INVALID_ARG for window < 1 or
  * num_sinks < 0, PKV_ERR_UNSUPPORTED when max_blocks_per_seq * block_size
@@ -475,6 +478,9 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* q, const voi
                                              int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
                                              int num_blocks, int max_context_len, pkv_dtype dtype, void* workspace,
                                              size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream);
+
+/* The counters at the start of a workspace of the window and score decode. */
+#define PKV_WINDOW_COUNTER_BYTES 524288
 
 /* Bytes of workspace pkv_paged_attention_decode_window needs. Pure host
  * function; 0 for non-positive sizes or num_heads not a multiple of

@@ -113,6 +113,7 @@ lib.pkv_paged_attention_decode_scores.restype = _I
 lib.pkv_evict_tokens.argtypes = [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                  _I, _I, _P, _P]
 lib.pkv_evict_tokens.restype = _I
+WINDOW_COUNTER_BYTES = 524288  # PKV_WINDOW_COUNTER_BYTES
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PKV_NOALLOC_SCRATCH_BYTES
 
 
@@ -354,20 +355,22 @@ def decode_scores_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: i
 def new_window_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                          device="cuda") -> torch.Tensor:
     """A workspace of paged_attention_decode_window: its counters zeroed, the
-    room for partial results as it comes."""
+    room for partial results as it comes. It serves calls of other sizes too, as
+    far as it is large enough for them."""
     n = decode_window_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:4 * num_seqs * num_heads].zero_()
+    ws[:WINDOW_COUNTER_BYTES].zero_()
     return ws
 
 
 def new_scores_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, max_context_len: int,
                          device="cuda") -> torch.Tensor:
     """A workspace of paged_attention_decode_scores: its counters zeroed, the
-    room for the logits as it comes."""
+    room for the logits as it comes. It serves calls of other sizes, and
+    paged_attention_decode_window, too, as far as it is large enough for them."""
     n = decode_scores_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:4 * num_seqs * num_heads].zero_()
+    ws[:WINDOW_COUNTER_BYTES].zero_()
     return ws
 
 

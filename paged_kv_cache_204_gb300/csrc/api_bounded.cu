@@ -50,7 +50,13 @@ struct WindowLayout {
 };
 
 // Counters of the segments, the pieces' partial results, and (scores) the
-// final maximum and sum of every row and its logits.
+// final maximum and sum of every row and its logits. The counters' place is the same in
+// every call, whatever its sizes, and nothing else is ever written there: they have to
+// be zero from one call to the next, also where a call of other sizes (or of the other operator)
+// lies between. A split segment has two pieces at least, so that there are never more of
+// them than kWinPiecesMost / 2.
+constexpr int64_t kCounterBytes = PKV_WINDOW_COUNTER_BYTES;
+static_assert(kCounterBytes == pkv::kWinPiecesMost / 2 * (int64_t)sizeof(int32_t), "a counter to a split segment");
 WindowLayout window_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim, bool scores,
                            int max_context_len) {
   WindowLayout w;
@@ -58,12 +64,14 @@ WindowLayout window_layout(int num_seqs, int num_heads, int num_kv_heads, int he
       max_context_len < 0)
     return w;
   const size_t rows = (size_t)num_seqs * num_heads;  // at least as many as segments
-  size_t off = align_up(rows * sizeof(int32_t), 256);
-  w.pieces = std::min(std::max(pkv::kWinRowPieces * (int64_t)rows, pkv::kWinPiecesLeast), pkv::kWinPiecesMost);
-  w.ml = off;
-  off += align_up((size_t)w.pieces * sizeof(float2), 256);
-  w.o = off;
-  off += (size_t)w.pieces * head_dim * sizeof(float);
+  const int64_t most = std::min(std::max(pkv::kWinRowPieces * (int64_t)rows, pkv::kWinPiecesLeast), pkv::kWinPiecesMost);
+  const size_t piece = sizeof(float2) + (size_t)head_dim * sizeof(float);
+  size_t off = align_up(rows * sizeof(int32_t), 256) + align_up((size_t)most * sizeof(float2), 256) +
+               (size_t)most * head_dim * sizeof(float);
+  // what the counters leave of that (a segment of one piece has no partial results)
+  w.pieces = std::min(most, std::max<int64_t>(((int64_t)off - kCounterBytes - 256) / (int64_t)piece, 0));
+  w.ml = kCounterBytes;
+  w.o = w.ml + align_up((size_t)w.pieces * sizeof(float2), 256);
   if (scores) {
     w.row_ml = off;
     off += align_up(rows * sizeof(float2), 256);

@@ -67,7 +67,7 @@ struct WindowParams {
   int block_size, block_bits, max_blocks_per_seq, num_blocks, max_context_len;  // block_size = 2^block_bits
   int splits;        // pieces a segment may be cut into
   int min_tiles;     // tiles a piece has at least (where the segment has as many)
-  int32_t* counter;  // [segments], zero between calls (splits > 1)
+  int32_t* counter;  // [segments], zero between calls (used where splits > 1)
   float2* piece_ml;  // [segments * splits][part_heads] (m, l)
   float* piece_o;    // [segments * splits][part_heads][D]
   float* logits;     // scores: [num_seqs][num_heads][logit_stride], base-2 logits
