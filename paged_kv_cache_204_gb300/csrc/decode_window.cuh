@@ -294,9 +294,12 @@ struct TileRing {
 // transposing matrix loads, P^T from the score layout by 8 x 8 transposes. Lane
 // (g, t) = (lane / 4, lane % 4) ends with head dims 16 m + g and 16 m + g + 8 of
 // the heads 2t, 2t + 1.
-// P enters as a 16-bit high part and a 16-bit remainder (16 significant bits or
-// more with either type), so that its rounding stays below the output's. With at
-// most 4 heads the high parts fill columns 0-3 and the remainders columns 4-7 of
+// P enters as a 16-bit high part and a 16-bit remainder, so that its rounding stays
+// below the output's: 16 significant bits or more in bfloat16, 22 in binary16. That type's
+// range is short, so its weights enter times 2^15 (the largest is 1): a weight
+// above 2^-18 keeps all bits, and below that the error is 2^-40 of the largest weight, so that
+// 2^20 tokens far below it lose no more than 2^-20 of the output. (As they are, weights below 2^-25
+// would be 0 in both parts and full in the sum that divides.) With at most 4 heads the high parts fill columns 0-3 and the remainders columns 4-7 of
 // one MMA (kWide false); with 5-8 heads they take two.
 template <typename T, int D, bool kWide, bool kLogits>
 struct MmaTile {
@@ -305,6 +308,8 @@ struct MmaTile {
   static constexpr int KS = D / 16;  // k-steps of the scores, m-tiles of the output
   static constexpr int ROW = D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of ring per warp, three CTAs on an SM
+  static constexpr bool kScaled = std::is_same<T, __half>::value;
+  static constexpr float kWeight = kScaled ? 32768.f : 1.f;  // factor of the weights in l and o until finish()
   using Ring = TileRing<TT, ROW, kStages>;
 
   uint32_t qf[KS][2];
@@ -368,6 +373,10 @@ struct MmaTile {
       m[c] = mn;
       pr[c] = exp2_from(x[c], mn);
       pr[c + 2] = exp2_from(x[c + 2], mn);
+      if constexpr (kScaled) {
+        pr[c] *= kWeight;
+        pr[c + 2] *= kWeight;
+      }
       l[c] = l[c] * alpha + (pr[c] + pr[c + 2]);
       if (__any_sync(kFullMask, alpha != 1.f)) {
 #pragma unroll
@@ -415,6 +424,13 @@ struct MmaTile {
       for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(kFullMask, o[i][e], 2);
+    }
+    if constexpr (kScaled) {  // a power of two: exact
+      l[0] *= 1.f / kWeight, l[1] *= 1.f / kWeight;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= 1.f / kWeight;
     }
     if (kWide || t < 2) {
 #pragma unroll

@@ -4,8 +4,8 @@ infinity."""
 import pytest
 import torch
 
-from bounded_helpers import DEV, Cache, seen_by
-from test_gpu_bounded import pkv, run_prefill  # noqa: F401  (pkv: the module's fixture)
+from bounded_helpers import DEV, Cache, attend, check, eps_p, seen_by
+from test_gpu_bounded import check_scores, check_window, pkv, run_prefill, run_scores, run_window  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,32 @@ def test_prefill_window_is_as_precise_as_its_type(pkv, dtype, D, bs, Hkv, G, L, 
     want = torch.cat([exact_rows(c, 0, q[a:a + 100], range(L - n + a, min(L, L - n + a + 100)), window, sinks)
                       for a in range(0, n, 100)])
     assert rms(out - want) <= 1.1 * rms(want.to(c.dtype) - want)
+
+
+# ---- one large weight, many far below it ---------------------------------------------------------
+
+
+def one_large(dtype, D, Hkv, G, L, bits):
+    """Token 0 has a logit above all others by `bits` (base 2), and values of 0 in the even head dims: what
+    an even dim of the output holds comes from the many small weights alone."""
+    c = Cache((L, 700), Hkv, G, D, 16, dtype, seed=int(10 * bits))
+    for s, n in enumerate(c.lens):
+        c.rows_k[s].zero_()
+        c.rows_k[s][:, 0, 0] = bits * 0.6931472 * D ** 0.5 / 16.0
+        c.rows_v[s].abs_()
+        c.rows_v[s][:, 0, ::2] = 0.0
+        c.put(c.k, s, torch.arange(n), c.rows_k[s])
+        c.put(c.v, s, torch.arange(n), c.rows_v[s])
+    c.q.zero_()
+    c.q[:, :, 0] = 16.0
+    return c
+
+
+@pytest.mark.parametrize("bits", [16.0, 23.0, 25.5, 27.0])
+@pytest.mark.parametrize("dtype,D,Hkv,G", [("f16", 64, 2, 1), ("f16", 128, 1, 8), ("bf16", 128, 2, 4)])
+def test_decode_keeps_small_weights(pkv, dtype, D, Hkv, G, bits):
+    c = one_large(dtype, D, Hkv, G, 20011, bits)
+    check_window(c, run_window(pkv, c, 15000, 1), 15000, 1, f"{bits} bits")
+    new = torch.full((2, Hkv, c.max_len), float("nan"), device=DEV)
+    out = run_scores(pkv, c, None, new)
+    check_scores(c, out, None, new, f"{bits} bits")
