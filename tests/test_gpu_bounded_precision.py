@@ -73,3 +73,19 @@ def test_decode_keeps_small_weights(pkv, dtype, D, Hkv, G, bits):
     new = torch.full((2, Hkv, c.max_len), float("nan"), device=DEV)
     out = run_scores(pkv, c, None, new)
     check_scores(c, out, None, new, f"{bits} bits")
+
+
+@pytest.mark.parametrize("bits", [16.0, 23.0, 25.5, 27.0])
+@pytest.mark.parametrize("dtype,D,Hkv,G", [("f16", 64, 2, 1), ("f16", 128, 1, 8), ("bf16", 128, 2, 4)])
+def test_prefill_window_keeps_small_weights(pkv, dtype, D, Hkv, G, bits):
+    """Few queries (clusters share a walk) and many (they do not)."""
+    c = one_large(dtype, D, Hkv, G, 3000, bits)
+    for n in (3, 700):
+        q = c.q[:1].expand(2 * n, -1, -1).contiguous()
+        out = run_prefill(pkv, c, [n, n], 2500, 1, q)
+        for s, L in enumerate(c.lens):
+            for i in sorted({0, 2, n // 2, n - 1}):
+                P = L - n + i
+                want, _, bound, _ = attend(q[0], c.rows_k[s], c.rows_v[s], seen_by(L, P, 2500, 1), c.scale,
+                                           eps_p(c.dtype))
+                check(out[s * n + i], want, bound, f"{bits} bits L={L} P={P}")
