@@ -457,7 +457,8 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_c
  *     out[s][h][:] = sum over the visible t of softmax(x)_t * v_t,
  * x_t as in pkv_paged_attention_decode. L == 0 gives an all-zero row. K and V
  * rows of tokens that are not visible are never read, nor are block-table
- * entries of blocks without a visible token.
+ * entries of blocks without a visible token. An infinity in a visible V row
+ * gives an infinity (two of either sign, or a NaN, a NaN) in its head dim alone.
  *
  *   window     >= 1; num_sinks >= 0 (may sum to more than a context)
  *   dtype      PKV_F32, PKV_F16 or PKV_BF16, of q, out and the caches

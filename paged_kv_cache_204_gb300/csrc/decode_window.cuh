@@ -308,6 +308,7 @@ struct MmaTile {
   static constexpr int KS = D / 16;  // k-steps of the scores, m-tiles of the output
   static constexpr int ROW = D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of ring per warp, three CTAs on an SM
+  static constexpr bool kTwoParts = true;  // weights in 16-bit parts
   static constexpr bool kScaled = std::is_same<T, __half>::value;
   static constexpr float kWeight = kScaled ? 32768.f : 1.f;  // factor of the weights in l and o until finish()
   using Ring = TileRing<TT, ROW, kStages>;
@@ -336,6 +337,8 @@ struct MmaTile {
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
 
+  // kExact: V in products with the 32-bit weights (see the kernel)
+  template <bool kExact>
   __device__ __forceinline__ void consume(const WindowParams& p, int s, int h0, const unsigned char* slot, int64_t t0,
                                           int L, int lane) {
     const uint32_t ks = smem_u32(slot);
@@ -386,29 +389,52 @@ struct MmaTile {
         }
       }
     }
-    uint32_t hi[2], lo[2];
+    if constexpr (kExact) {
+      const bool mine = kWide || t < 2;  // else the lane's columns are those of remainders
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint32_t h = pack2(pr[2 * v], pr[2 * v + 1], T());
-      const float2 f = unpack2(h, T());
-      const uint32_t rest = pack2(pr[2 * v] - f.x, pr[2 * v + 1] - f.y, T());
-      if constexpr (kWide) {
-        hi[v] = transpose8x8(h);
-        lo[v] = transpose8x8(rest);
-      } else {
-        hi[v] = transpose8x8(t < 2 ? h : rest);
+      for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+        for (int r8 = 0; r8 < 8; ++r8) {
+          const float p0 = __shfl_sync(kFullMask, pr[2 * half], 4 * r8 + t);
+          const float p1 = __shfl_sync(kFullMask, pr[2 * half + 1], 4 * r8 + t);
+          const unsigned char* row = slot + Ring::kTileBytes + (8 * half + r8) * ROW;
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // dims 16 i + g and 16 i + g + 8
+              const float v =
+                  static_cast<float>(reinterpret_cast<const T*>(row + (((2 * i + e) ^ r8) * 16))[g]);
+              if (mine) {
+                o[i][2 * e] = fmaf(p0, v, o[i][2 * e]);
+                o[i][2 * e + 1] = fmaf(p1, v, o[i][2 * e + 1]);
+              }
+            }
+        }
+    } else {
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t h = pack2(pr[2 * v], pr[2 * v + 1], T());
+        const float2 f = unpack2(h, T());
+        const uint32_t rest = pack2(pr[2 * v] - f.x, pr[2 * v + 1] - f.y, T());
+        if constexpr (kWide) {
+          hi[v] = transpose8x8(h);
+          lo[v] = transpose8x8(rest);
+        } else {
+          hi[v] = transpose8x8(t < 2 ? h : rest);
+        }
       }
-    }
-    // V^T fragments: matrices (dims 0-7, tokens 0-7), (dims 8-15, tokens 0-7), then
-    // tokens 8-15; lane i gives token row i % 8 + 8 (i / 16), chunk 2 m + (i / 8) % 2
-    const uint32_t vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
-    const uint32_t vs = ks + Ring::kTileBytes + vr * ROW;
+      // V^T fragments: matrices (dims 0-7, tokens 0-7), (dims 8-15, tokens 0-7), then
+      // tokens 8-15; lane i gives token row i % 8 + 8 (i / 16), chunk 2 m + (i / 8) % 2
+      const uint32_t vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+      const uint32_t vs = ks + Ring::kTileBytes + vr * ROW;
 #pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
-      uint32_t f[4];
-      ldsm_x4_trans(vs + ((2 * mt + vc) ^ (vr & 7)) * 16, f);
-      mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], hi[0], hi[1]);
-      if constexpr (kWide) mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], lo[0], lo[1]);
+      for (int mt = 0; mt < KS; ++mt) {
+        uint32_t f[4];
+        ldsm_x4_trans(vs + ((2 * mt + vc) ^ (vr & 7)) * 16, f);
+        mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], hi[0], hi[1]);
+        if constexpr (kWide) mma_16816<T>(o[mt], f[0], f[1], f[2], f[3], lo[0], lo[1]);
+      }
     }
   }
 
@@ -456,6 +482,7 @@ struct FmaTile {
   static constexpr int TT = D == 128 ? 8 : 16;  // 8 KB of K and V rows
   static constexpr int RPG = TT / 4;            // rows of a tile per group
   static constexpr int kHeads = kPart;
+  static constexpr bool kTwoParts = false;
   static constexpr int NC = D / 32;  // chunks of a row per lane
   static constexpr int ROW = D * 4;
   static constexpr int kStages = 2;
@@ -490,6 +517,7 @@ struct FmaTile {
     return *reinterpret_cast<const float4*>(rows + r * ROW + ((sub + 8 * c) ^ (r & 7)) * 16);
   }
 
+  template <bool>
   __device__ __forceinline__ void consume(const WindowParams& p, int s, int h0, const unsigned char* slot, int64_t t0,
                                           int L, int) {
     bool ok[RPG];
@@ -635,48 +663,66 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   const int begin = cut(piece) * kWinWarps, end = min(cut(piece + 1) * kWinWarps, r.n);
 
   unsigned char* mine = rings + warp * Ring::kBytes;
-  Ring ring;
   Tile tile;
-  ring.start(p, mine, s, kvh, L, r, begin, end, warp, kWinWarps, lane);
-  tile.init(p, s, h0, heads, lane);
-  for (int i = begin + warp, n = 0; i < end; i += kWinWarps, ++n) {
-    copies_wait<Tile::kStages - 2>();
-    __syncwarp();  // tile n has landed for all lanes, and all are done with the slot refilled now
-    ring.issue(p);
-    tile.consume(p, s, h0, mine + (n % Tile::kStages) * Ring::kSlotBytes, (int64_t)r.tile(i) * Tile::TT, L, lane);
-  }
-  __syncwarp();
-  tile.finish(reinterpret_cast<float*>(mine), sm_ml[warp]);
-  __syncthreads();
+  auto walk = [&](auto exact) {
+    Ring ring;
+    ring.start(p, mine, s, kvh, L, r, begin, end, warp, kWinWarps, lane);
+    tile.init(p, s, h0, heads, lane);
+    for (int i = begin + warp, n = 0; i < end; i += kWinWarps, ++n) {
+      copies_wait<Tile::kStages - 2>();
+      __syncwarp();  // tile n has landed for all lanes, and all are done with the slot refilled now
+      ring.issue(p);
+      tile.template consume<decltype(exact)::value>(p, s, h0, mine + (n % Tile::kStages) * Ring::kSlotBytes,
+                                                    (int64_t)r.tile(i) * Tile::TT, L, lane);
+    }
+    __syncwarp();
+    tile.finish(reinterpret_cast<float*>(mine), sm_ml[warp]);
+    __syncthreads();
+  };
 
-  // join the warps: a thread takes 4 dims of a head
+  // join the warps: a thread takes 4 dims of a head. True where an output is a NaN and its weights are not.
   T* out = static_cast<T*>(p.out) + ((size_t)s * p.num_heads + h0) * D;
   const size_t first = (size_t)seg * p.splits * p.part_heads;
   const size_t slot = first + (size_t)piece * p.part_heads;
-  for (int i = threadIdx.x; i < heads * (D / 4); i += kWinThreads) {
-    const int h = i / (D / 4), d = 4 * (i % (D / 4));
-    float M = -INFINITY;
+  auto join = [&]() {
+    bool nan = false;
+    for (int i = threadIdx.x; i < heads * (D / 4); i += kWinThreads) {
+      const int h = i / (D / 4), d = 4 * (i % (D / 4));
+      float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWinWarps; ++w) M = fmaxf(M, sm_ml[w][h].x);
-    Join t;
-    t.clear();
+      for (int w = 0; w < kWinWarps; ++w) M = fmaxf(M, sm_ml[w][h].x);
+      Join t;
+      t.clear();
 #pragma unroll
-    for (int w = 0; w < kWinWarps; ++w)
-      t.add(sm_ml[w][h], reinterpret_cast<const float4*>(rings + w * Ring::kBytes)[(h * D + d) / 4], M);
-    if (pieces == 1) {
-      // no token: zeros; a row whose every logit is -inf: 0 / 0, as the formula has it
-      const float inv = L > 0 ? 1.f / t.l : 0.f;
-      store4(out + h * D + d, t.a[0] * inv, t.a[1] * inv, t.a[2] * inv, t.a[3] * inv);
-      if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, t.l);
-    } else {
-      __stcg(reinterpret_cast<float4*>(p.piece_o + (slot + h) * D + d), make_float4(t.a[0], t.a[1], t.a[2], t.a[3]));
-      if (d == 0) __stcg(p.piece_ml + slot + h, make_float2(M, t.l));
+      for (int w = 0; w < kWinWarps; ++w)
+        t.add(sm_ml[w][h], reinterpret_cast<const float4*>(rings + w * Ring::kBytes)[(h * D + d) / 4], M);
+      const float all = (t.a[0] + t.a[1]) + (t.a[2] + t.a[3]);
+      nan |= all != all && t.l == t.l;
+      if (pieces == 1) {
+        // no token: zeros; a row whose every logit is -inf: 0 / 0, as the formula has it
+        const float inv = L > 0 ? 1.f / t.l : 0.f;
+        store4(out + h * D + d, t.a[0] * inv, t.a[1] * inv, t.a[2] * inv, t.a[3] * inv);
+        if (kLogits && d == 0) p.row_ml[(size_t)s * p.num_heads + h0 + h] = make_float2(M, t.l);
+      } else {
+        __stcg(reinterpret_cast<float4*>(p.piece_o + (slot + h) * D + d), make_float4(t.a[0], t.a[1], t.a[2], t.a[3]));
+        if (d == 0) __stcg(p.piece_ml + slot + h, make_float2(M, t.l));
+      }
     }
+    return nan;
+  };
+  walk(std::false_type());
+  const bool nan = join();
+  // (a barrier too: the partial's writes precede the release below)
+  if (Tile::kTwoParts ? __syncthreads_or(nan) : (__syncthreads(), 0)) {
+    // A remainder of 0, or below 0, times an infinity in V is a NaN where the weight itself gives
+    // infinity: the tiles once more with the weights as they are, slowly.
+    walk(std::true_type());
+    join();
+    __syncthreads();
   }
   if (pieces == 1) return;
 
   // the last piece of the segment joins them all
-  __syncthreads();  // the partial's writes precede the release below
   if (threadIdx.x == 0) {
     const int prev = atomic_add_acq_rel_gpu(p.counter + seg, 1);
     sm_last = prev == pieces - 1;

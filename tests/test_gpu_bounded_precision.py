@@ -89,3 +89,41 @@ def test_prefill_window_keeps_small_weights(pkv, dtype, D, Hkv, G, bits):
                 want, _, bound, _ = attend(q[0], c.rows_k[s], c.rows_v[s], seen_by(L, P, 2500, 1), c.scale,
                                            eps_p(c.dtype))
                 check(out[s * n + i], want, bound, f"{bits} bits L={L} P={P}")
+
+
+# ---- infinities among the values ----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,D,bs,Hkv,G", [("f16", 64, 8, 2, 1), ("f16", 128, 16, 1, 8), ("bf16", 128, 16, 2, 4),
+                                             ("bf16", 64, 32, 2, 12), ("f32", 128, 16, 1, 2)])
+@pytest.mark.parametrize("L,window", [(9, 5), (500, 300), (12011, 12000)])
+def test_decode_infinity_in_a_value(pkv, dtype, D, bs, Hkv, G, L, window):
+    """A visible value of infinity makes its head dim of the output infinite, two of either sign or a NaN
+    make it a NaN; all other dims, and the scores, are what they are without. Weights lie within 2^-40 of
+    each other, so that none is 0 in fp32."""
+    c = Cache((L, L - 2), Hkv, G, D, bs, dtype, seed=L)
+    c.q *= 0.5
+    inf = float("inf")
+    clean = [v.clone() for v in c.rows_v]
+    for s, n in enumerate(c.lens):
+        c.rows_v[s][:, n - 2, 5] = inf
+        c.rows_v[s][:, n - 1, 11] = -inf
+        c.rows_v[s][:, n - 3, 40] = inf
+        c.rows_v[s][:, n - 4, 40] = -inf
+        c.rows_v[s][:, n - 1, 50] = float("nan")
+        c.put(c.v, s, torch.arange(n), c.rows_v[s])
+    plain = torch.ones(D, dtype=torch.bool, device=DEV)
+    plain[[5, 11, 40, 50]] = False
+    new = torch.full((2, Hkv, L), float("nan"), device=DEV)
+    for what, out, w in (("window", run_window(pkv, c, window, 1), window), ("scores", run_scores(pkv, c, None, new), L)):
+        assert (out[..., 5] == inf).all() and (out[..., 11] == -inf).all(), what
+        assert torch.isnan(out[..., 40]).all() and torch.isnan(out[..., 50]).all(), what
+        for s, n in enumerate(c.lens):
+            want, _, bound, _ = attend(c.q[s], c.rows_k[s], clean[s], seen_by(n, n - 1, w, 1), c.scale, eps_p(c.dtype))
+            check(out[s][:, plain], want[:, plain], bound[:, plain], f"{what} L={n}")
+    again = torch.full_like(new, float("nan"))
+    c.rows_v = clean
+    for s, n in enumerate(c.lens):
+        c.put(c.v, s, torch.arange(n), clean[s])
+    run_scores(pkv, c, None, again)
+    assert torch.equal(torch.nan_to_num(new, -1.0), torch.nan_to_num(again, -1.0))
