@@ -3,7 +3,7 @@
 Argument marshalling only: every entry point forwards device pointers, sizes
 and the current CUDA stream to the compiled library, which does all the work
 in its own kernels. There is no fallback: importing this package without the
-built library (``python -m paged_kv_cache_204_gb300.build`` or
+built library (``python paged_kv_cache_204_gb300/build.py`` or
 ``__graft_entry__.build()``) raises ImportError.
 
 Functions mirror the C entry points:
@@ -37,18 +37,32 @@ from . import build as _build
 
 LIB_PATH = _build.LIB
 
+_BUILD_COMMAND = f"python {os.path.abspath(_build.__file__)}"
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"paged_kv_cache_204_gb300: compiled library missing at {LIB_PATH}; "
-                      "build it with `python -m paged_kv_cache_204_gb300.build`")
-
-if not os.path.exists(_build.BINDING):
-    raise ImportError(f"paged_kv_cache_204_gb300: compiled binding missing at {_build.BINDING}; "
-                      "build it with `python -m paged_kv_cache_204_gb300.build`")
+                      f"build it with `{_BUILD_COMMAND}`")
 
 lib = ctypes.CDLL(LIB_PATH)
-_binding_spec = importlib.util.spec_from_file_location("_pkv_torch", _build.BINDING)
-_binding = importlib.util.module_from_spec(_binding_spec)
-_binding_spec.loader.exec_module(_binding)
+_binding_module = None
+
+
+def _binding():
+    """The Python extension of the bounded-cache operators, loaded when one of them is first called: nothing
+    else needs it, and it is bound to the PyTorch that it was compiled against."""
+    global _binding_module
+    if _binding_module is None:
+        made_for = _build.binding_for()
+        if made_for != _build.binding_abi():
+            what = f"missing at {_build.BINDING}" if made_for is None else \
+                f"at {_build.BINDING} was built for {made_for}, this is {_build.binding_abi()}"
+            raise ImportError(f"paged_kv_cache_204_gb300: compiled binding {what}; build it with `{_BUILD_COMMAND}`")
+        spec = importlib.util.spec_from_file_location("_pkv_torch", _build.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding_module = module
+    return _binding_module
+
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA, PKV_ERR_OUT_OF_BLOCKS = range(6)
 DEV_ERR_BLOCK_ID, DEV_ERR_SLOT, DEV_ERR_CONTEXT_LEN, DEV_ERR_TIMEOUT, DEV_ERR_PAIR = 1, 2, 4, 8, 16
@@ -382,7 +396,7 @@ def paged_attention_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: t
     num_sinks tokens and its newest `window` (the query's own included).
     Block-table entries of blocks with no visible token are not read.
     workspace: new_window_workspace()."""
-    _check(_binding.decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, window, num_sinks,
+    _check(_binding().decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, window, num_sinks,
                                   max_context_len, workspace, dev_err, stream), "pkv_paged_attention_decode_window")
 
 
@@ -392,7 +406,7 @@ def paged_attention_prefill_window(out: torch.Tensor, q: torch.Tensor, k_cache: 
                                    max_query_len: int, dev_err: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention_prefill in which the query at position P sees the tokens
     t <= P with t < num_sinks or t > P - window."""
-    _check(_binding.prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, window,
+    _check(_binding().prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, window,
                                    num_sinks, max_query_len, dev_err, stream), "pkv_paged_attention_prefill_window")
 
 
@@ -406,7 +420,7 @@ def paged_attention_decode_scores(out: torch.Tensor, scores_out: torch.Tensor, q
     scores float32 [B, Hkv, n >= max_context_len]; scores None: zeros;
     scores_out may be scores (in place). The newest token starts from zero.
     workspace: new_scores_workspace()."""
-    _check(_binding.decode_scores(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scale,
+    _check(_binding().decode_scores(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scale,
                                   max_context_len, workspace, scores, dev_err, stream),
            "pkv_paged_attention_decode_scores")
 
@@ -425,6 +439,6 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Ten
     blocks are each the same as in block_tables or in no row of it
     (BlockManager.shrink_batch). Pools of any cache type; head_dim for uint8
     pools of q4_0 rows."""
-    _check(_binding.evict_tokens(k_cache, v_cache, scores, scores_out, block_tables, dst_block_tables, context_lens,
+    _check(_binding().evict_tokens(k_cache, v_cache, scores, scores_out, block_tables, dst_block_tables, context_lens,
                                  new_context_lens, kept, num_sinks, num_recent, max_context_len, head_dim, dev_err,
                                  stream), "pkv_evict_tokens")

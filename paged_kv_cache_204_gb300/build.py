@@ -3,7 +3,11 @@ sm_103a (and every .cpp, host-only code, by nvcc's host compiler) in
 parallel and linked into _build/libpkv.so (CUDA runtime linked statically,
 so the library loads beside any PyTorch build). csrc/torch_binding.cxx becomes
 the Python extension _build/_pkv_torch.so, compiled against this machine's
-PyTorch and linked to libpkv.so."""
+PyTorch and linked to libpkv.so; it is built again when either it or that
+PyTorch has changed.
+
+Run by its path, `python paged_kv_cache_204_gb300/build.py`: importing the package
+needs the library."""
 from __future__ import annotations
 
 import glob
@@ -20,6 +24,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cxx")
 BINDING = os.path.join(OUT_DIR, "_pkv_torch.so")
+BINDING_ABI = BINDING + ".abi"  # the PyTorch and the Python it was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -35,16 +40,40 @@ def _sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def _deps() -> list[str]:
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)])
+def _headers() -> list[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def _newer(made: str, sources: list[str]) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(d) <= os.path.getmtime(made) for d in sources)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+                  + _headers())
+
+
+def binding_abi() -> str:
+    """What the Python extension is bound to: this PyTorch and this Python."""
+    import sysconfig
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_for() -> str | None:
+    """The binding_abi() that the extension was built for; None if there is none."""
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_ABI):
+        return None
+    with open(BINDING_ABI) as f:
+        return f.read()
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SRC] + _headers()) and binding_for() == binding_abi()
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _binding_flags() -> tuple[list[str], list[str]]:
@@ -61,50 +90,59 @@ def _binding_flags() -> tuple[list[str], list[str]]:
              "-Wl,-rpath,$ORIGIN"])
 
 
+def _run(what: str, cmd: list[str]) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+    return r.stderr
+
+
+def _compile_binding(obj: str) -> list[str]:
+    """The extension's object file; returns the flags it is linked with."""
+    cflags, ldflags = _binding_flags()
+    _run(f"g++ on {BINDING_SRC}", ["g++", "-O2", "-std=c++17", "-fPIC", *cflags, "-c", BINDING_SRC, "-o", obj])
+    return ldflags
+
+
+def _link_binding(obj: str, ldflags: list[str]) -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run("link", ["g++", "-shared", "-o", tmp, obj, *ldflags])
+    if os.path.exists(BINDING_ABI):
+        os.remove(BINDING_ABI)
+    os.replace(tmp, BINDING)
+    with open(BINDING_ABI, "w") as f:
+        f.write(binding_abi())
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    if not force and up_to_date():
+    """Build what is not up to date: the library and the Python extension. The library is in
+    place even where the extension does not compile, which then raises."""
+    library, extension = force or not library_up_to_date(), force or not binding_up_to_date()
+    if not library and not extension:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
+    srcs = _sources() if library else []
+    binding_obj = os.path.join(OUT_DIR, "torch_binding.cxx.o")
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
 
     def compile_one(src: str) -> tuple[str, str]:
         obj = os.path.join(OUT_DIR, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
-        return obj, r.stderr
+        return obj, _run(f"nvcc on {src}", [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj])
 
-    binding_obj = os.path.join(OUT_DIR, "torch_binding.cxx.o")
-
-    def compile_binding() -> list[str]:
-        cflags, ldflags = _binding_flags()
-        r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", *cflags, "-c", BINDING_SRC, "-o", binding_obj],
-                           capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
-        return ldflags
-
-    srcs = _sources()
     with ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding)
+        binding = ex.submit(_compile_binding, binding_obj) if extension else None
         results = list(ex.map(compile_one, srcs))
-        ldflags = binding.result()
-    if verbose_ptxas:
-        for _, log in results:
-            sys.stderr.write(log)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpkv.so", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, binding_obj, *ldflags], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        if library:
+            if verbose_ptxas:
+                for _, log in results:
+                    sys.stderr.write(log)
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run("link", [nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpkv.so", "-o", tmp]
+                 + [o for o, _ in results])
+            os.replace(tmp, LIB)
+        if binding is not None:
+            _link_binding(binding_obj, binding.result())
     return LIB
 
 
