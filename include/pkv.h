@@ -513,8 +513,10 @@ pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const vo
  *     scores_out[s][g][t] = old + sum over the query heads h of g of softmax(x_h)_t,
  *     old = scores[s][g][t] for t < L - 1 when scores is not NULL, else 0
  * (the newest token has no past: whatever its place held is replaced). The sum
- * runs over the heads in order, in fp32; results do not depend on the work
- * split. Entries at and behind L are neither read nor written, and a sequence
+ * runs over the heads in order, in fp32. Equal arguments give equal bits; the
+ * batch's sizes and max_context_len choose how a row is split, so that in another
+ * batch or under another bound its outputs and scores may differ in their last
+ * bits (likewise for pkv_paged_attention_decode_window). Entries at and behind L are neither read nor written, and a sequence
  * with L == 0 (an idle row of a fixed batch) has none.
  *
  *   scores      float [num_seqs][num_kv_heads][score_stride], or NULL

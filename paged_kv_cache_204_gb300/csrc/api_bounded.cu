@@ -17,7 +17,7 @@ namespace {
 // are resident at a time). 64 sequences, window 4096 / 8 sequences of up to 32768
 // with scores: 171 / 141 us with 4 waves, 2 more or 1 less with 3, 4 and 2 more with 5, 11
 // and 5 more with 6.
-// At least kMinTiles: one sequence, window 1024: 7.5 us, 10.5 with 16. At most kMaxTiles,
+// At least kMinTiles on average: one sequence, window 1024: 7.5 us, 10.5 with 16. At most kMaxTiles,
 // for the one long sequence of a batch that is sized by its length (131072 tokens beside
 // 127 x 100: 227 us with 16 pieces, 1295 with the 2 that an equal share of tiles gives).
 constexpr int64_t kWaveCtas = 152 * 3, kWaves = 4;

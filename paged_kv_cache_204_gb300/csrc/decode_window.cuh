@@ -66,7 +66,7 @@ struct WindowParams {
   int part_heads;  // query heads of a part (the last part may have fewer)
   int block_size, block_bits, max_blocks_per_seq, num_blocks, max_context_len;  // block_size = 2^block_bits
   int splits;        // pieces a segment may be cut into
-  int min_tiles;     // tiles a piece has at least (where the segment has as many)
+  int min_tiles;     // tiles of a piece on average, at least (where the segment has as many)
   int32_t* counter;  // [segments], zero between calls (used where splits > 1)
   float2* piece_ml;  // [segments * splits][part_heads] (m, l)
   float* piece_o;    // [segments * splits][part_heads][D]
@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   const int heads = min(p.part_heads, p.group - part * p.part_heads);
   const int L = checked_len(p, s);
   const TileRange r = tiles_visible<Tile::TT>(L, p.window, p.sinks);
-  // pieces of this segment: none is shorter than min_tiles where that can be
+  // pieces of this segment: min_tiles or more on average (the last are shorter, and may have no
+  // tile at all: then m = -inf and nothing is added)
   const int pieces = max(1, min(p.splits, r.n / p.min_tiles));
   if (piece >= pieces) return;
   // in whole rounds of the warps
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
 
 using WindowLauncher = cudaError_t (*)(const WindowParams&, cudaStream_t);
 
-// 16-bit (is_bf16) and 32-bit caches; part_heads picks the variant (see WindowShape).
+// 16-bit (is_bf16) and 32-bit caches; part_heads picks the variant.
 WindowLauncher window_launcher_16(int is_bf16, int head_dim, int part_heads, bool logits);
 WindowLauncher window_launcher_f32(int head_dim, int part_heads, bool logits);
 cudaError_t launch_add_scores(const ScoreParams& p, int num_seqs, int max_context_len, cudaStream_t stream);

@@ -1,4 +1,5 @@
 """One workspace for window and score decodes of many sizes."""
+import numpy as np
 import pytest
 import torch
 
@@ -40,3 +41,21 @@ def test_a_small_calls_workspace_for_a_larger_call(pkv):
     ws[pkv.WINDOW_COUNTER_BYTES:].fill_(0xFF)
     for c in (many, few, many):
         check_window(c, run_window(pkv, c, 2400, 4, ws), 2400, 4, str(len(c.lens)))
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 4), ("f16", 64, 8), ("f32", 128, 2)])
+def test_split_by_batch_and_bound(pkv, dtype, D, G):
+    """The same sequence by itself, in a batch and under larger bounds, each of which splits it in its own
+    way: every one within the bound of the exact values, and the same bits on a second call."""
+    for lens, bounds in (((5000,), (5000, 40000, 1 << 20)), ((5000, 40, 0, 4999, 128, 700, 1, 2500), (5000, 40000))):
+        c = Cache(lens, 2, G, D, 16, dtype, seed=7)
+        c.bt = np.concatenate([c.bt, np.full((len(lens), 1 << 16), -1, np.int32)], 1)
+        c.tables = torch.from_numpy(c.bt).to(DEV)
+        for n in bounds:
+            out = run_window(pkv, c, 4500, 4, max_len=n)
+            check_window(c, out, 4500, 4, f"bound {n}")
+            assert torch.equal(out, run_window(pkv, c, 4500, 4, max_len=n))
+            got = [torch.full((len(lens), 2, n), float("nan"), device=DEV) for _ in range(2)]
+            outs = [run_scores(pkv, c, None, x, max_len=n) for x in got]
+            check_scores(c, outs[0], None, got[0], f"bound {n}")
+            assert torch.equal(*outs) and torch.equal(*(torch.nan_to_num(x, -1.0) for x in got))
