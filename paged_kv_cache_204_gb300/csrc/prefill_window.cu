@@ -1,6 +1,8 @@
 // Launch of the windowed prefill kernel (binary16 and bfloat16).
 #include "prefill_window.cuh"
 
+#include <limits>
+
 namespace pkv {
 
 namespace {
@@ -27,9 +29,10 @@ cudaError_t launch_prefill_window(const PrefillWindowParams& params, const void*
     if (dev >= 0 && dev < 64) __atomic_store_n(&sms_of_device[dev], sms, __ATOMIC_RELEASE);
   }
   // scores are taken raw, so the scale has to be positive: a negative one's sign goes
-  // into the queries, and 0 becomes a number that any score's product with is below rounding
+  // into the queries, and 0 becomes the smallest number: any finite score's product with it is
+  // 2^-21 at most
   p.flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-  p.scale_log2 = p.scale_log2 == 0.f ? 1e-37f : fabsf(p.scale_log2);
+  p.scale_log2 = p.scale_log2 == 0.f ? std::numeric_limits<float>::denorm_min() : fabsf(p.scale_log2);
   CUtensorMap kmap, vmap;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   e = encode_pool_rows_map(&kmap, k_cache, (uint64_t)pool_rows, D, p.block_size, bf16);

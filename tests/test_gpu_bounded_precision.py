@@ -127,3 +127,28 @@ def test_decode_infinity_in_a_value(pkv, dtype, D, bs, Hkv, G, L, window):
         c.put(c.v, s, torch.arange(n), clean[s])
     run_scores(pkv, c, None, again)
     assert torch.equal(torch.nan_to_num(new, -1.0), torch.nan_to_num(again, -1.0))
+
+
+# ---- a scale of zero ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("D,n", [(64, 3), (128, 400)])
+def test_scale_of_zero_with_large_scores(pkv, D, n):
+    """All logits are 0 however large q . k is (up to 10^37 here): every visible token has the same weight."""
+    c = Cache((400,), 20, 1, D, 16, "bf16", seed=D)
+    c.scale = 0.0
+    c.k *= 3e17
+    c.rows_k = [r * 3e17 for r in c.rows_k]
+    q = (torch.randn(n, c.H, D, device=DEV) * 3e17).to(c.dtype)
+    size = torch.einsum("nhd,hld->nhl", q.float().abs(), c.rows_k[0].float().abs())
+    assert size.max() < 1e38 and (torch.einsum("nhd,hld->nhl", q.float(), c.rows_k[0].float()).abs() > 1e36).any()
+    out = run_prefill(pkv, c, [n], 150, 4, q)
+    c.q = q[-1:]
+    dec = run_window(pkv, c, 150, 4)
+    for i in sorted({0, n // 2, n - 1}):
+        seen = seen_by(400, 400 - n + i, 150, 4).to(DEV)
+        v = c.rows_v[0][:, seen].double()
+        bound = (seen.sum() + 8) * 2.0 ** -23 * v.abs().mean(1) + (eps_p(c.dtype) + 2.0 ** -20) * v.abs().mean(1)
+        check(out[i], v.mean(1), bound, f"query {i}")
+        if i == n - 1:
+            check(dec[0], v.mean(1), bound, "decode")
