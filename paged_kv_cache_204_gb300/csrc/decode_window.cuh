@@ -713,17 +713,18 @@ __global__ void __launch_bounds__(kWinThreads) pa_window_kernel(const WindowPara
   };
   walk(std::false_type());
   const bool nan = join();
-  // (a barrier too: the partial's writes precede the release below)
-  if (Tile::kTwoParts ? __syncthreads_or(nan) : (__syncthreads(), 0)) {
-    // A remainder of 0, or below 0, times an infinity in V is a NaN where the weight itself gives
-    // infinity: the tiles once more with the weights as they are, slowly.
-    walk(std::true_type());
-    join();
-    __syncthreads();
+  if constexpr (Tile::kTwoParts) {
+    if (__syncthreads_or(nan)) {
+      // A remainder of 0, or below 0, times an infinity in V is a NaN where the weight itself gives
+      // infinity: the tiles once more with the weights as they are, slowly.
+      walk(std::true_type());
+      join();
+    }
   }
   if (pieces == 1) return;
 
   // the last piece of the segment joins them all
+  __syncthreads();  // the partial's writes precede the release below
   if (threadIdx.x == 0) {
     const int prev = atomic_add_acq_rel_gpu(p.counter + seg, 1);
     sm_last = prev == pieces - 1;
