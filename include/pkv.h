@@ -442,8 +442,10 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* k_c
  * fixed size are served here; both are this library's choice:
  *   by position  attention sees a sequence's first tokens ("sinks") and a
  *                sliding window of its newest ones; blocks that lie wholly
- *                outside both may be given back, and their block-table entries
- *                are not read;
+ *                outside both are not read, nor are their block-table entries,
+ *                so that a caller who allocates blocks may use them for other
+ *                things (pkv_bm_* has no call that gives them back: its tables
+ *                are whole);
  *   by use       every decode step adds each cached token's attention weight
  *                to a score, and from time to time the cache is cut to a
  *                budget: the first tokens, the newest ones and the highest-
@@ -499,7 +501,8 @@ size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_heads, int num_kv
  * Block-table entries of blocks that no query of the call sees need not be
  * valid. V rows of tokens that some query of the call sees must
  * be finite (an infinity or a NaN there may also reach queries that do not
- * see the token); rows that no query sees may hold anything. */
+ * see the token); rows that no query sees may hold anything. A probability enters
+ * the product with V as two 16-bit parts, in both types. */
 pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, const int32_t* context_lens,
                                               const int32_t* query_start, float scale, int window, int num_sinks,
@@ -517,7 +520,10 @@ pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const vo
  * batch's sizes and max_context_len choose how a row is split, so that in another
  * batch or under another bound its outputs and scores may differ in their last
  * bits (likewise for pkv_paged_attention_decode_window). Entries at and behind L are neither read nor written, and a sequence
- * with L == 0 (an idle row of a fixed batch) has none.
+ * with L == 0 (an idle row of a fixed batch) has none. Only the newest token's
+ * entry starts from 0: tokens that came into the cache in another way (a
+ * prefill's) start from what their entries hold, which the caller sets to 0
+ * first, behind an eviction too.
  *
  *   scores      float [num_seqs][num_kv_heads][score_stride], or NULL
  *   scores_out  the same shape; the same address as scores (in place), or a
@@ -554,7 +560,8 @@ size_t pkv_decode_scores_workspace_bytes(int num_seqs, int num_heads, int num_kv
  *     scores_out[s][g][i]                = scores[s][g][kept[s][g][i]]
  * where rows are read through block_tables and written through
  * dst_block_tables, and new_context_lens[s] = n. Bytes are moved as they are:
- * bit-exact. Nothing at and behind position n is written.
+ * bit-exact. Nothing at and behind position n is written: the scores there
+ * (in place: those of tokens that are gone) stay as they were.
  *
  *   scores        float [num_seqs][num_kv_heads][score_stride], score_stride >=
  *                 max_context_len; read
@@ -564,10 +571,11 @@ size_t pkv_decode_scores_workspace_bytes(int num_seqs, int num_heads, int num_kv
  *                 byte in common with it
  *   dst_block_tables  int32 [num_seqs][max_blocks_per_seq]: the blocks that hold
  *                 the result (the first ceil(n / block_size) entries of a row).
- *                 Each entry is the entry of block_tables at the same place, a
- *                 block that this sequence alone uses, or a block that is in no
- *                 row of block_tables (a fresh one; a block that other
- *                 sequences hold must be replaced by one); a block is the
+ *                 An entry is either that of block_tables at the same place,
+ *                 which no other sequence may hold then, or a block that is in no
+ *                 row of block_tables (a fresh one, as it has to be where other
+ *                 sequences hold the old one); another block of the same
+ *                 sequence is not allowed, and a block is the
  *                 destination of one entry only. The two tables may be the same
  *                 array. pkv_bm_shrink_batch hands out such tables.
  *   new_context_lens  int32 [num_seqs]; may be context_lens

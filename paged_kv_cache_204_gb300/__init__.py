@@ -418,7 +418,8 @@ def paged_attention_decode_scores(out: torch.Tensor, scores_out: torch.Tensor, q
     """paged_attention_decode that adds every cached token's attention weight,
     summed over the query heads of its kv head, to its score. scores_out,
     scores float32 [B, Hkv, n >= max_context_len]; scores None: zeros;
-    scores_out may be scores (in place). The newest token starts from zero.
+    scores_out may be scores (in place). The newest token starts from zero;
+    before tokens come in another way (a prefill) the caller zeroes their entries.
     workspace: new_scores_workspace()."""
     _check(_binding().decode_scores(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scale,
                                   max_context_len, workspace, scores, dev_err, stream),
@@ -436,8 +437,8 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Ten
     float32 [B, Hkv, n]; scores_out likewise (may be scores); kept int32
     [B, Hkv, budget]; new_context_lens may be context_lens. dst_block_tables:
     block_tables itself for sequences that share no block, or a table whose
-    blocks are each the same as in block_tables or in no row of it
-    (BlockManager.shrink_batch). Pools of any cache type; head_dim for uint8
+    blocks are each the same as in block_tables, at the same place, or in no row
+    of it (BlockManager.shrink_batch). Pools of any cache type; head_dim for uint8
     pools of q4_0 rows."""
     _check(_binding().evict_tokens(k_cache, v_cache, scores, scores_out, block_tables, dst_block_tables, context_lens,
                                  new_context_lens, kept, num_sinks, num_recent, max_context_len, head_dim, dev_err,

@@ -19,7 +19,7 @@
 // pieces in their order (log-sum-exp), all in one launch.
 //
 // Bound by memory: K and V of the visible tokens are read once, 4 to 32 operations to an
-// element. What keeps the reads coming (times of 128 sequences of up to 2048 tokens, 40
+// element. What keeps the reads coming (GPU times of 128 sequences of up to 2048 tokens, 40
 // heads, window 1000 / 64 sequences of up to 32768, 64 query and 8 kv heads, window
 // 4096; bfloat16, head_dim 128):
 //  - asynchronous copies into shared-memory rings, 16 KB a warp, two tiles deep, three CTAs
@@ -32,7 +32,9 @@
 //  - first pieces first and longest, so that the last ones to start are short: 173 -> 171,
 //    and 8 sequences of up to 32768 with scores 4 us less of 147.
 // 280 us are 7.1 TB/s and 171 us 6.4 (a plain copy runs at 6.8). One sequence of 7001
-// tokens, window 1024: 7.4 us, the latency of table, rows, join and launch.
+// tokens, window 1024: 7.4 us, the latency of table, rows, join and launch. 32-bit caches (16
+// sequences of up to 32768, window 4096): 40 heads 384 us, 7.1 TB/s; 32 query and 8 kv heads 114 us,
+// 4.8 TB/s, the queries and outputs of four heads in registers leaving two CTAs on an SM.
 #pragma once
 
 #include <type_traits>

@@ -19,16 +19,17 @@
 // P enters its product as a 16-bit high part and a 16-bit remainder, two MMAs for one: 16
 // significant bits or more. One part, 2^-8 (bfloat16) or 2^-11 of each weight, would put an error
 // of its own beside the output's rounding (each is that fraction of the output, rms, whatever
-// the values' signs): 1.4 times the rounding's alone; it would take 218 us instead of 273 for
+// the values' signs): 1.4 times the rounding's alone; it would take 214 us instead of 258 for
 // the 8192 queries below.
 // Bound by the MMAs for long walks: 8192 queries over a window of 2048 (32 query and 8 kv heads,
-// bfloat16, head_dim 128) take 273 us, 880 TFLOP/s over the visible tokens and 1320 with the
-// remainders' MMAs (1956 are the library product's). A step of 128 tokens for both A and B takes
-// about 3700 cycles, 3072 of them MMAs; what lies between is the way from S over the softmax and
+// bfloat16, head_dim 128) take 258 us of GPU time (as all times here), 930 TFLOP/s over the visible
+// tokens and 1400 with the remainders' MMAs (1956 are the library product's); the tensor pipe is
+// active for 71 %. A step of 128 tokens for both A and B takes
+// about 3500 cycles, 3072 of them MMAs; what lies between is the way from S over the softmax and
 // the waits to the next MMA. Tiles that a row sees in part take longer, the start and the end
 // of a pair some 8000 cycles: of short walks they are most (8 sequences of up to
-// 1500 tokens, window 500, head_dim 64, 40 heads: 115 us). One chunk of 100 queries, window
-// 1024: 20 us.
+// 1500 tokens, window 500, head_dim 64, 40 heads: 114 us). One chunk of 100 queries, window
+// 1024: 18 us.
 #pragma once
 
 #include <type_traits>
@@ -43,8 +44,8 @@ constexpr int kPwStages = 4;     // tiles in shared memory: two links of a V and
 constexpr int kPwSoft = 256;     // 2 softmax warpgroups
 constexpr int kPwThreads = kPwSoft + 128;  // + MMA warp of A, TMA warp, clearing warp, MMA warp of B
 constexpr uint32_t kPwTmemCols = 512;     // S of A and B (128 columns each), O of A and B
-// CTAs to a cluster at most. One chunk of 100 queries, window 1024: 26 us with 1, 21 with 2,
-// 16 with 4; of clusters of 8 no more than 15 are resident at a time, so that 16 items
+// CTAs to a cluster at most. One chunk of 100 queries, window 1024: 29 us with 1, 23 with 2,
+// 18 with 4; of clusters of 8 no more than 15 are resident at a time, so that 16 items
 // would take two rounds.
 constexpr int kPwMaxCluster = 4;
 
@@ -86,7 +87,7 @@ struct PrefillWindowParams {
 // moves by 8 (with 0: 9 % slower). Binary16 has a short range: its weights reach up to 2^15, so that
 // they keep 22 bits down to 2^-16 of the largest and have an error of 2^-38 of it below that (with
 // 2^8, 2^-32: 2^17 tokens that far below one other lose 2^-15 of the output). The base moves by 2; by 8, 4
-// or 1 the time is the same (116 to 117 us, 8 sequences of up to 1500 tokens, 40 heads of 64).
+// or 1 the time is the same (8 sequences of up to 1500 tokens, 40 heads of 64).
 template <typename T>
 struct PwPack;
 template <>
@@ -274,7 +275,8 @@ __device__ __forceinline__ float pw_max3(float a, float b, float c) {
 // A warp's walk over the items `item`, `item` + step, .. < items that have query rows.
 // The grid is laid out for the longest sequence, so that in a ragged batch most may have
 // none: 32 are looked at together, one by a lane (8192 queries beside 63 sequences of one
-// query each: 203 us, 273 with a look at one item after another, 150 for the 8192 alone).
+// query each, window 1024: 240 us, 169 for the 8192 alone; 70 us more with a look at one item
+// after another).
 struct PwScan {
   int base;       // item of lane 0
   uint32_t mask;  // lanes whose items are still to come
@@ -469,9 +471,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     // both fall into step and the tensor pipe idles under both softmaxes. The pipe holds no
     // more than an MMA or two ahead, so that what comes between one's MMAs and the other's
     // leaves it idle: each makes its waits, and works out its next step, under the other's
-    // MMAs (one warp for both: 224 us instead of 213 for 8192 queries, window 2048, 32 query
-    // and 8 kv heads). At head_dim 64 the MMAs are half as long as the exponentials, and both
-    // may go as they are ready (93 us, 96 with turns, for 8 sequences of 40 heads).
+    // MMAs (without turns 4 % slower for 8192 queries, window 2048, 32 query and 8 kv heads; one warp
+    // for both 5 %, when P had one part). At head_dim 64 the MMAs are shorter than the softmax, and both
+    // may go as they are ready (114 us, 119 with turns, for 8 sequences of 40 heads).
     // MMAs of one thread complete in order, so S may take the place of a P that the MMA
     // before it reads, and "S done" says that O holds every earlier tile.
     // The whole warp walks and waits, one elected lane issues; what a step needs to know is
