@@ -187,7 +187,9 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_pa
  *                  holds int32 counters that MUST be zero before the first call;
  *                  every call that ends with *dev_err == 0 leaves them zero
  *                  again. After a call that reports a device error, zero the
- *                  workspace again. Two calls that share a workspace must not
+ *                  workspace again; likewise before a call of other sizes than the
+ *                  one before (partial results follow the counters of that call's
+ *                  num_seqs * num_heads, in the place of others' counters). Two calls that share a workspace must not
  *                  overlap on the GPU.
  *
  * Work split: the (sequence, head group) pairs are laid end to end as one
