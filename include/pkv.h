@@ -189,8 +189,8 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_pa
  *                  again. After a call that reports a device error, zero the
  *                  workspace again; likewise before a call of other sizes than the
  *                  one before (partial results follow the counters of that call's
- *                  num_seqs * num_heads, in the place of others' counters). Two calls that share a workspace must not
- *                  overlap on the GPU.
+ *                  num_seqs * num_heads, in the place of others' counters). Two
+ *                  calls that share a workspace must not overlap on the GPU.
  *
  * Work split: the (sequence, head group) pairs are laid end to end as one
  * sequence of 16-token tiles and every warp of a device-sized, resident grid
@@ -504,7 +504,8 @@ size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_heads, int num_kv
  * valid. V rows of tokens that some query of the call sees must
  * be finite (an infinity or a NaN there may also reach queries that do not
  * see the token); rows that no query sees may hold anything. A probability enters
- * the product with V as two 16-bit parts, in both types. */
+ * the product with V as two 16-bit parts, in both types. A row whose largest
+ * logit scale * q . K_t is 2^27 or more in magnitude may come out as NaN. */
 pkv_status pkv_paged_attention_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, const int32_t* context_lens,
                                               const int32_t* query_start, float scale, int window, int num_sinks,

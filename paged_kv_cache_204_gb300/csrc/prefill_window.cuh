@@ -44,6 +44,7 @@ constexpr int kPwStages = 4;     // tiles in shared memory: two links of a V and
 constexpr int kPwSoft = 256;     // 2 softmax warpgroups
 constexpr int kPwThreads = kPwSoft + 128;  // + MMA warp of A, TMA warp, clearing warp, MMA warp of B
 constexpr uint32_t kPwTmemCols = 512;     // S of A and B (128 columns each), O of A and B
+constexpr float kPwFar = 8388608.f;       // 2^23
 // CTAs to a cluster at most. One chunk of 100 queries, window 1024: 29 us with 1, 23 with 2,
 // 18 with 4; of clusters of 8 no more than 15 are resident at a time, so that 16 items
 // would take two rounds.
@@ -720,11 +721,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           for (int e = 0; e < 4; ++e) m4[e] = pw_max3(m4[e], v[i + e], v[i + e + 4]);
         const float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // the base moves only when the maximum grows by more than kRescaleLog2: every
-        // P stays below 2^kTopLog2, and O and the row sum have the same base
-        const bool grow = mt > m_use + P16::kTopLog2;
+        // P stays below 2^kTopLog2, and O and the row sum have the same base. (Logits from kPwFar on
+        // are whole numbers, and a base may be off by half their distance: there it is the maximum
+        // and moves whenever that does.)
+        const bool grow = mt - m_use > (fabsf(m_use) < kPwFar ? P16::kTopLog2 : 0.f);  // (no for -inf - -inf)
         float alpha = 1.f;
         if (grow) {
-          const float base = mt - (P16::kTopLog2 - P16::kRescaleLog2);
+          const float base = mt - (fabsf(mt) < kPwFar ? P16::kTopLog2 - P16::kRescaleLog2 : 0.f);
           alpha = exp2f(m_use - base);  // 0 while nothing was visible
           m_use = base;
         }

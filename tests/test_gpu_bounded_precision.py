@@ -152,3 +152,34 @@ def test_scale_of_zero_with_large_scores(pkv, D, n):
         check(out[i], v.mean(1), bound, f"query {i}")
         if i == n - 1:
             check(dec[0], v.mean(1), bound, "decode")
+
+
+# ---- logits far from zero -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("D,Hkv,L,n", [(64, 2, 300, 3), (128, 20, 600, 500), (64, 1, 2000, 700)])
+@pytest.mark.parametrize("dtype,log2", [("f16", 9), ("f16", 10), ("f16", 11), ("f16", 12), ("bf16", 10), ("bf16", 11),
+                                        ("bf16", 12)])
+def test_logits_far_from_zero(pkv, dtype, log2, D, Hkv, L, n):
+    """Elements of +-2^log2: q . k is a whole multiple of 2^(2 log2 + 1), so that one logit is above all others or
+    exactly as large as some, and the output is the mean of those tokens' values. (Weights of 1/c are off by 2^-24, their
+    sum by c 2^-24.)"""
+    c = Cache((L,), Hkv, 1, D, 16, dtype, seed=log2)
+    sign = lambda x: torch.where(x < 0, -1.0, 1.0).to(c.dtype) * 2.0 ** log2
+    c.rows_k[0] = sign(c.rows_k[0])
+    c.put(c.k, 0, torch.arange(L), c.rows_k[0])
+    q = sign(torch.randn(n, c.H, D, device=DEV))
+    out = run_prefill(pkv, c, [n], 250, 4, q)
+    c.q = q[-1:]
+    dec = run_window(pkv, c, 250, 4)
+    x = torch.einsum("nhd,hld->hnl", q.double(), c.rows_k[0].double())
+    seen = torch.stack([seen_by(L, L - n + i, 250, 4) for i in range(n)]).to(DEV)
+    assert x.abs().max() * c.scale < 2.0 ** 27
+    x = x.masked_fill(~seen, float("-inf"))
+    p = (x == x.amax(2, keepdim=True)).double()
+    count = p.sum(2).T[..., None]
+    want = torch.einsum("hnl,hld->nhd", p, c.rows_v[0].double()) / count
+    size = torch.einsum("hnl,hld->nhd", p, c.rows_v[0].double().abs()) / count
+    bound = (eps_p(c.dtype) + (2 * count + 8) * 2.0 ** -23) * size
+    check(out, want, bound, "prefill")
+    check(dec, want[-1:], bound[-1:], "decode")
