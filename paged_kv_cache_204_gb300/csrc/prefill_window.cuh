@@ -19,13 +19,13 @@
 // P enters its product as a 16-bit high part and a 16-bit remainder, two MMAs for one: 16
 // significant bits or more. One part, 2^-8 (bfloat16) or 2^-11 of each weight, would put an error
 // of its own beside the output's rounding (each is that fraction of the output, rms, whatever
-// the values' signs): 1.4 times the rounding's alone; it would take 214 us instead of 258 for
+// the values' signs): 1.4 times the rounding's alone; it would take 214 us instead of 260 for
 // the 8192 queries below.
 // Bound by the MMAs for long walks: 8192 queries over a window of 2048 (32 query and 8 kv heads,
-// bfloat16, head_dim 128) take 258 us of GPU time (as all times here), 930 TFLOP/s over the visible
+// bfloat16, head_dim 128) take 260 us of GPU time (as all times here), 930 TFLOP/s over the visible
 // tokens and 1400 with the remainders' MMAs (1956 are the library product's); the tensor pipe is
 // active for 71 %. A step of 128 tokens for both A and B takes
-// about 3500 cycles, 3072 of them MMAs; what lies between is the way from S over the softmax and
+// about 3500 cycles, 87 % of them MMAs; what lies between is the way from S over the softmax and
 // the waits to the next MMA. Tiles that a row sees in part take longer, the start and the end
 // of a pair some 8000 cycles: of short walks they are most (8 sequences of up to
 // 1500 tokens, window 500, head_dim 64, 40 heads: 114 us). One chunk of 100 queries, window
