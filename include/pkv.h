@@ -91,6 +91,7 @@ typedef enum pkv_status {
 #define PKV_DEV_ERR_TIMEOUT 0x8     /* a bounded wait inside a kernel ran out */
 #define PKV_DEV_ERR_PAIR 0x10       /* copy_blocks pair entry outside [0, num_blocks) */
 #define PKV_DEV_ERR_GROUP 0x20      /* grouped decode: grouping not a partition, or shared blocks differ */
+#define PKV_DEV_ERR_POSITION 0x40   /* rotating cache write: a position outside the table */
 
 /* Human-readable name of a pkv_status value (static string, never NULL). */
 const char* pkv_status_string(int status);
@@ -601,6 +602,82 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores, i
                             int num_kv_heads, int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
                             int num_blocks, int max_context_len, pkv_dtype dtype, int32_t* dev_err,
                             pkv_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * Rotating cache writes
+ *
+ * Models with rotary positions turn every query and key by its position before
+ * attention sees it. These calls do that and [VM]'s write of the new rows in
+ * one pass: they take a step's queries, keys and values as the projection gives
+ * them, write the turned queries, and the turned keys and the values into the
+ * cache slots. The rotation and its conventions are this library's choice.
+ * ---------------------------------------------------------------------- */
+
+/* pkv_reshape_and_cache with rotary positions. The first R = rotary_dim values
+ * of a query or key row form R / 2 pairs: pair i is (x[i], x[i + R / 2]), or
+ * with interleaved != 0 (x[2 i], x[2 i + 1]). For token t, pair i becomes
+ *     (a, b) -> (a c - b s, b c + a s),
+ *     c = cos_sin[P][i], s = cos_sin[P][R / 2 + i], P = positions[axis(i)][t];
+ * the other head_dim - R values stay. axis(i) is 0 with one axis, and pair_axis[i]
+ * with several (time, height, width of a picture's patch). Each product and the
+ * sum are rounded to binary32, the result once to dtype: the same bytes as on
+ * any IEEE host. Then
+ *     q_out[t][h][:] = turned q[t][h][:]           for every query head
+ *     k_cache, v_cache at slot_mapping[t] = turned k[t], v[t] (unchanged)
+ * A slot < 0 stores no K and V (its q is turned all the same); a token with
+ * positions[0][t] < 0 is an idle row of a fixed batch: nothing of it is read or
+ * written, and its other positions and slot may hold anything.
+ *
+ *   q, q_out      [num_tokens][num_heads][head_dim] dtype; k, v
+ *                 [num_tokens][num_kv_heads][head_dim]: a token's rows lie
+ *                 together, and *_stride (elements, a multiple of 16 bytes, at
+ *                 least a token's rows) leads from token to token, so that parts
+ *                 of one projection's output serve as they are. q_out is q (same
+ *                 address and stride), or a range (first to last row) that has
+ *                 no byte in common with it; q_out must not meet k and v, nor
+ *                 the caches anything.
+ *   positions     int32 [num_axes][num_tokens]
+ *   cos_sin       float [max_position][rotary_dim]: R / 2 cosines, then R / 2
+ *                 sines of each position, 16-byte aligned
+ *   pair_axis     HOST array of rotary_dim / 2 axes, read before the call
+ *                 returns; may be NULL with one axis
+ *   num_axes      1 to 4
+ *   other arguments as in pkv_reshape_and_cache.
+ *
+ * Errors: host - INVALID_ARG as for pkv_reshape_and_cache, and for a stride, a
+ * pair_axis entry, or a q_out that does not obey the above; UNSUPPORTED for
+ * rotary_dim that is no multiple of 16 or above head_dim, num_axes > 4, more
+ * than 65535 heads of a kind. Device - a token with a position (of any axis) outside
+ * [0, max_position) that is not idle is left out and sets PKV_DEV_ERR_POSITION; a slot >= num_blocks
+ * * block_size sets PKV_DEV_ERR_SLOT and stores no K and V. One kernel. */
+pkv_status pkv_rope_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, void* k_cache, void* v_cache,
+                              const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+                              int max_position, int rotary_dim, const uint8_t* pair_axis, int num_axes,
+                              int interleaved, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                              int block_size, int num_blocks, pkv_dtype dtype, int32_t* dev_err,
+                              pkv_stream_t stream);
+
+/* pkv_rope_and_cache into fp8 caches, stored as in pkv_reshape_and_cache_fp8:
+ * the turned key is divided by k_scale in binary32 and rounded once, to e4m3
+ * (not to src_dtype before). q, k, v, q_out: src_dtype, PKV_F16 or PKV_BF16. */
+pkv_status pkv_rope_and_cache_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, void* k_cache, void* v_cache,
+                                  const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+                                  int max_position, int rotary_dim, const uint8_t* pair_axis, int num_axes,
+                                  int interleaved, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, pkv_dtype src_dtype, float k_scale, float v_scale,
+                                  int32_t* dev_err, pkv_stream_t stream);
+
+/* pkv_rope_and_cache into q4_0 caches: the rows of pkv_reshape_and_cache_q4_0,
+ * quantised from the turned key's binary32 values. */
+pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride, void* k_cache, void* v_cache,
+                                   const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+                                   int max_position, int rotary_dim, const uint8_t* pair_axis, int num_axes,
+                                   int interleaved, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int num_blocks, pkv_dtype src_dtype, int32_t* dev_err,
+                                   pkv_stream_t stream);
 
 /* Bytes of workspace pkv_paged_attention_decode needs for these sizes: the
  * segment counters (num_seqs * num_heads int32) plus a fixed area for the

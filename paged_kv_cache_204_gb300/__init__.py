@@ -21,6 +21,8 @@ Functions mirror the C entry points:
                           -> attention over the first tokens and a sliding window
   paged_attention_decode_scores, evict_tokens
                           -> decode that adds up attention weights, and the eviction that goes by them
+  rope_and_cache, rope_and_cache_fp8, rope_and_cache_q4_0
+                          -> cache writes with rotary positions (of one axis or several)
   set_wait_timeout_ns / get_wait_timeout_ns, status_string, version
 The host block manager (include/pkv_block_manager.h) is wrapped by
 ``paged_kv_cache_204_gb300.block_manager.BlockManager``.
@@ -48,8 +50,8 @@ _binding_module = None
 
 
 def _binding():
-    """The Python extension of the bounded-cache operators, loaded when one of them is first called: nothing
-    else needs it, and it is bound to the PyTorch that it was compiled against."""
+    """The Python extension of the later operators (bounded caches, rotating cache writes, prefill over
+    quantised caches), loaded when one of them is first called: nothing else needs it, and it is bound to the PyTorch that it was compiled against."""
     global _binding_module
     if _binding_module is None:
         made_for = _build.binding_for()
@@ -66,7 +68,7 @@ def _binding():
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA, PKV_ERR_OUT_OF_BLOCKS = range(6)
 DEV_ERR_BLOCK_ID, DEV_ERR_SLOT, DEV_ERR_CONTEXT_LEN, DEV_ERR_TIMEOUT, DEV_ERR_PAIR = 1, 2, 4, 8, 16
-DEV_ERR_GROUP = 32
+DEV_ERR_GROUP, DEV_ERR_POSITION = 32, 64
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.uint8: 3}  # uint8: e4m3 codes
 PKV_FP8_E4M3 = 3
 PKV_Q4_0 = 4
@@ -127,6 +129,14 @@ lib.pkv_paged_attention_decode_scores.restype = _I
 lib.pkv_evict_tokens.argtypes = [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                  _I, _I, _P, _P]
 lib.pkv_evict_tokens.restype = _I
+_ROPE = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, ctypes.c_char_p, _I, _I, _I, _I, _I, _I,
+         _I, _I, _I]
+lib.pkv_rope_and_cache.argtypes = [*_ROPE, _P, _P]
+lib.pkv_rope_and_cache.restype = _I
+lib.pkv_rope_and_cache_fp8.argtypes = [*_ROPE, _F, _F, _P, _P]
+lib.pkv_rope_and_cache_fp8.restype = _I
+lib.pkv_rope_and_cache_q4_0.argtypes = [*_ROPE, _P, _P]
+lib.pkv_rope_and_cache_q4_0.restype = _I
 WINDOW_COUNTER_BYTES = 524288  # PKV_WINDOW_COUNTER_BYTES
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PKV_NOALLOC_SCRATCH_BYTES
 
@@ -443,3 +453,50 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Ten
     _check(_binding().evict_tokens(k_cache, v_cache, scores, scores_out, block_tables, dst_block_tables, context_lens,
                                  new_context_lens, kept, num_sinks, num_recent, max_context_len, head_dim, dev_err,
                                  stream), "pkv_evict_tokens")
+
+
+def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The table of the rope_and_cache functions for the usual angles, position *
+    base ** (-2 i / rotary_dim) of pair i: float32 [max_position, rotary_dim],
+    cosines, then sines, from angles in 64 bits."""
+    pair = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * base ** (-pair / rotary_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def rope_sections(*pairs: int) -> bytes:
+    """pair_axis of sections: the first pairs[0] pairs turn by axis 0, the next pairs[1] by axis 1, and so on."""
+    return b"".join(bytes([axis]) * n for axis, n in enumerate(pairs))
+
+
+def rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                   pair_axis: bytes | None = None, interleaved: bool = False, dev_err: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """reshape_and_cache with rotary positions: q_out = q turned, and the turned k
+    and v into the cache slots. q, q_out [T, H, D], k, v [T, Hkv, D], each token's
+    rows together (slices of a packed projection serve as they are); q_out may be
+    q. slot_mapping int64 [T]: below 0 stores no K and V. positions int32 [T], or
+    [axes, T] with pair_axis, a byte of each pair (rope_sections); below 0 marks
+    an idle token. cos_sin float32 [max_position, rotary_dim] (rope_table);
+    interleaved pairs neighbours instead of the row's halves."""
+    _check(_binding().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, 0, 1.0, 1.0,
+                                     pair_axis, interleaved, dev_err, stream), "pkv_rope_and_cache")
+
+
+def rope_and_cache_fp8(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                       cos_sin: torch.Tensor, k_scale: float, v_scale: float, pair_axis: bytes | None = None,
+                       interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """rope_and_cache into uint8 pools of e4m3 codes (reshape_and_cache_fp8); q, k, v fp16/bf16."""
+    _check(_binding().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, 1, k_scale,
+                                     v_scale, pair_axis, interleaved, dev_err, stream), "pkv_rope_and_cache_fp8")
+
+
+def rope_and_cache_q4_0(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                        positions: torch.Tensor, cos_sin: torch.Tensor, pair_axis: bytes | None = None,
+                        interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """rope_and_cache into uint8 pools of q4_0 rows (reshape_and_cache_q4_0); q, k, v fp16/bf16."""
+    _check(_binding().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, 2, 1.0, 1.0,
+                                     pair_axis, interleaved, dev_err, stream), "pkv_rope_and_cache_q4_0")

@@ -1,5 +1,5 @@
-// Python extension: the bounded-cache entry points of pkv.h called with torch
-// tensors. Argument checks and marshalling only. A call from Python spends about
+// Python extension: the bounded-cache entry points of pkv.h, the rotating cache
+// writes and prefill over quantised caches, called with torch tensors. Argument checks and marshalling only. A call from Python spends about
 // as long on reading ten tensors' attributes, one by one, as the smallest of these
 // operators on the GPU (15 us against 7); here that is about 1 us.
 //
@@ -68,28 +68,53 @@ pkv_dtype code_of(at::ScalarType t, const char* name) {
   }
 }
 
-// The pools, block tables and lengths, which every operator takes.
-struct Cache {
-  const at::Tensor &k, &v, &tables;
+// The two pools, which every operator takes.
+struct Pools {
+  const at::Tensor &k, &v;
   at::Device dev;
-  int nb, Hkv, bs, D, B, MB;
-  const int32_t* lens;
+  int nb, Hkv, bs, D;
 
-  Cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo)
-      : k(tensor(ko, "k_cache")), v(tensor(vo, "v_cache")), tables(tensor(to, "block_tables")), dev(k.device()) {
+  Pools(PyObject* ko, PyObject* vo) : k(tensor(ko, "k_cache")), v(tensor(vo, "v_cache")), dev(k.device()) {
     if (!dev.is_cuda()) refuse("k_cache: need a CUDA tensor");
     if (k.dim() != 4 || !k.is_contiguous())
       refuse_tensor(k, "k_cache", "a contiguous [num_blocks, Hkv, block_size, D] tensor");
     want(v, "v_cache", k.scalar_type(), k.sizes(), dev, "a tensor like k_cache");
-    if (tables.dim() != 2) refuse_tensor(tables, "block_tables", "int32 [num_seqs, max_blocks_per_seq]");
     nb = size(k, 0), Hkv = size(k, 1), bs = size(k, 2), D = size(k, 3);
-    B = size(tables, 0), MB = size(tables, 1);
-    want(tables, "block_tables", at::kInt, tables.sizes(), dev, "contiguous int32 [num_seqs, max_blocks_per_seq]");
-    lens = static_cast<const int32_t*>(lengths(lo, "context_lens"));
   }
   static int size(const at::Tensor& t, int d) {
     if (t.size(d) > INT32_MAX) refuse("a dimension does not fit in 32 bits");
     return (int)t.size(d);
+  }
+  int32_t* error_word(PyObject* o) const {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, "dev_err");
+    if (t.scalar_type() != at::kInt || t.numel() < 1 || t.device() != dev)
+      refuse_tensor(t, "dev_err", "an int32 tensor on the pools' device");
+    return t.data_ptr<int32_t>();
+  }
+  // `o`: None (the device's current stream) or a torch stream
+  pkv_stream_t stream(PyObject* o) const {
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
+    if (a == nullptr) throw PyError();
+    void* s = PyLong_AsVoidPtr(a);
+    Py_DECREF(a);
+    if (s == nullptr && PyErr_Occurred()) throw PyError();
+    return static_cast<pkv_stream_t>(s);
+  }
+};
+
+// The pools, block tables and lengths of the attention operators.
+struct Cache : Pools {
+  const at::Tensor& tables;
+  int B, MB;
+  const int32_t* lens;
+
+  Cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) : Pools(ko, vo), tables(tensor(to, "block_tables")) {
+    if (tables.dim() != 2) refuse_tensor(tables, "block_tables", "int32 [num_seqs, max_blocks_per_seq]");
+    B = size(tables, 0), MB = size(tables, 1);
+    want(tables, "block_tables", at::kInt, tables.sizes(), dev, "contiguous int32 [num_seqs, max_blocks_per_seq]");
+    lens = static_cast<const int32_t*>(lengths(lo, "context_lens"));
   }
   void* lengths(PyObject* o, const char* name) const {
     return want(tensor(o, name), name, at::kInt, {B}, dev, "contiguous int32 [num_seqs] on the pools' device");
@@ -116,23 +141,6 @@ struct Cache {
     if (t.device() != dev || !t.is_contiguous()) refuse_tensor(t, "workspace", "a contiguous tensor on the pools' device");
     *bytes = t.nbytes();
     return t.data_ptr();
-  }
-  int32_t* error_word(PyObject* o) const {
-    if (o == Py_None) return nullptr;
-    const at::Tensor& t = tensor(o, "dev_err");
-    if (t.scalar_type() != at::kInt || t.numel() < 1 || t.device() != dev)
-      refuse_tensor(t, "dev_err", "an int32 tensor on the pools' device");
-    return t.data_ptr<int32_t>();
-  }
-  // `o`: None (the device's current stream) or a torch stream
-  pkv_stream_t stream(PyObject* o) const {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
-    if (a == nullptr) throw PyError();
-    void* s = PyLong_AsVoidPtr(a);
-    Py_DECREF(a);
-    if (s == nullptr && PyErr_Occurred()) throw PyError();
-    return static_cast<pkv_stream_t>(s);
   }
 };
 
@@ -255,10 +263,79 @@ PyObject* evict_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A step's rows [tokens, heads, head_dim], each token's together; *stride: from token to token.
+void* step_rows(const at::Tensor& t, const char* name, at::ScalarType type, int64_t tokens, int64_t D, at::Device dev,
+                int64_t* stride) {
+  if (t.dim() != 3 || t.scalar_type() != type || t.size(0) != tokens || t.size(2) != D || t.device() != dev ||
+      (t.numel() > 0 && (t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != D))))
+    refuse_tensor(t, name, "[tokens, heads, head_dim], a token's rows together, on the pools' device");
+  *stride = t.stride(0);
+  return t.data_ptr();
+}
+
+// q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, kind (0: caches of q's type,
+// 1: e4m3, 2: q4_0), k_scale, v_scale, pair_axis (None or bytes), interleaved, dev_err, stream
+PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&] {
+    const Pools c(a[4], a[5]);
+    const at::Tensor &qt = tensor(a[1], "q"), &kt = tensor(a[2], "k"), &vt = tensor(a[3], "v");
+    const at::Tensor &ot = tensor(a[0], "q_out"), &st = tensor(a[6], "slot_mapping"), &pt = tensor(a[7], "positions");
+    const at::Tensor& ct = tensor(a[8], "cos_sin");
+    const int kind = as_int(a[9], "kind");
+    if (qt.dim() != 3) refuse_tensor(qt, "q", "[tokens, num_heads, head_dim]");
+    const int T = Pools::size(qt, 0), H = Pools::size(qt, 1), D = Pools::size(qt, 2);
+    const at::ScalarType type = qt.scalar_type();
+    const pkv_dtype code = code_of(type, "q");
+    if (c.k.scalar_type() != (kind == 0 ? type : at::kByte) || c.D != (kind == 2 ? D / 16 * 9 : D))
+      refuse_tensor(c.k, "k_cache", kind == 0 ? "rows of q's type" : kind == 1 ? "e4m3 rows of head_dim bytes" : "q4_0 rows of 9 head_dim / 16 bytes");
+    int64_t so, sq, sk, sv;
+    void* out = step_rows(ot, "q_out", type, T, D, c.dev, &so);
+    if (ot.size(1) != H) refuse_tensor(ot, "q_out", "a tensor of q's shape");
+    const void* q = step_rows(qt, "q", type, T, D, c.dev, &sq);
+    const void* k = step_rows(kt, "k", type, T, D, c.dev, &sk);
+    const void* v = step_rows(vt, "v", type, T, D, c.dev, &sv);
+    if (kt.size(1) != c.Hkv || vt.size(1) != c.Hkv) refuse("k, v: need the pools' number of kv heads");
+    const void* slots = want(st, "slot_mapping", at::kLong, {T}, c.dev, "contiguous int64 [tokens] on the pools' device");
+    if (pt.dim() != 1 && pt.dim() != 2) refuse_tensor(pt, "positions", "int32 [tokens] or [axes, tokens]");
+    const int axes = pt.dim() == 2 ? Pools::size(pt, 0) : 1;
+    const char* need = "contiguous int32 [tokens] or [axes, tokens] on the pools' device";
+    const void* positions = pt.dim() == 2 ? want(pt, "positions", at::kInt, {axes, T}, c.dev, need)
+                                          : want(pt, "positions", at::kInt, {T}, c.dev, need);
+    if (ct.dim() != 2) refuse_tensor(ct, "cos_sin", "float32 [max_position, rotary_dim]");
+    const void* table = want(ct, "cos_sin", at::kFloat, ct.sizes(), c.dev,
+                             "contiguous float32 [max_position, rotary_dim] on the pools' device");
+    const int most = Pools::size(ct, 0), R = Pools::size(ct, 1);
+    const float k_scale = as_float(a[10]), v_scale = as_float(a[11]);
+    const uint8_t* axis = nullptr;
+    if (a[12] != Py_None) {
+      if (!PyBytes_Check(a[12]) || PyBytes_GET_SIZE(a[12]) != R / 2) refuse("pair_axis: need bytes, one of each pair");
+      axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[12]));
+    }
+    const int interleaved = PyObject_IsTrue(a[13]);
+    if (interleaved < 0) throw PyError();
+    int32_t* err = c.error_word(a[14]);
+    const c10::cuda::CUDAGuard guard(c.dev);
+    const pkv_stream_t stream = c.stream(a[15]);
+    const auto slot_ids = static_cast<const int64_t*>(slots);
+    const auto at_positions = static_cast<const int32_t*>(positions);
+    const auto cos_sin = static_cast<const float*>(table);
+    void *kc = c.k.data_ptr(), *vc = c.v.data_ptr();
+    if (kind == 1)
+      return pkv_rope_and_cache_fp8(out, so, q, sq, k, sk, v, sv, kc, vc, slot_ids, at_positions, cos_sin, most, R,
+                                    axis, axes, interleaved, T, H, c.Hkv, D, c.bs, c.nb, code, k_scale, v_scale, err,
+                                    stream);
+    return (kind == 2 ? pkv_rope_and_cache_q4_0 : pkv_rope_and_cache)(out, so, q, sq, k, sk, v, sv, kc, vc, slot_ids,
+                                                                      at_positions, cos_sin, most, R, axis, axes,
+                                                                      interleaved, T, H, c.Hkv, D, c.bs, c.nb, code,
+                                                                      err, stream);
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(decode_window), ENTRY(prefill_window), ENTRY(decode_scores), ENTRY(evict_tokens),
+                         ENTRY(rope_and_cache),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_torch", "Bounded-cache calls with torch tensors", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_torch", "Calls with torch tensors", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
