@@ -679,6 +679,56 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
                                    int block_size, int num_blocks, pkv_dtype src_dtype, int32_t* dev_err,
                                    pkv_stream_t stream);
 
+/* ----------------------------------------------------------------------
+ * Prefill over quantised caches
+ *
+ * [WL], [QKV]: a prompt, a chunk of one or a few drafted tokens attend over
+ * fp8 or q4_0 pools, as decode does with one token.
+ * ---------------------------------------------------------------------- */
+
+/* pkv_paged_attention_prefill over fp8 caches: K is k_scale * code, V v_scale *
+ * code, q and out of `dtype` (PKV_F16 or PKV_BF16). Arguments and errors as in
+ * pkv_paged_attention_prefill, and
+ *   k_scale, v_scale  finite and > 0 (with scale * k_scale finite)
+ *   max_query_len     a sequence with more new tokens sets
+ *                     PKV_DEV_ERR_CONTEXT_LEN and is skipped
+ *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whose
+ *                     first PKV_PREFILL_COUNTER_BYTES must be zero before the first
+ *                     call; every call that ends with *dev_err == 0 leaves them zero. One
+ *                     workspace serves calls of any sizes, of both operators.
+ *                     Two calls that share a workspace must not overlap on the GPU.
+ * Outputs are rounded once to dtype from 32-bit sums; on the way, probabilities
+ * are rounded to binary16 (relative 2^-11), and bfloat16 queries enter as
+ * binary16 numbers times a power of two of their row (exact but for values of
+ * less than 2^-28 of the row's largest). V rows that some query of the call sees
+ * must be finite (a NaN there may also reach queries that do not see the token);
+ * rows that no query sees may hold anything. A row whose largest logit is 2^27 or
+ * more in magnitude may come out as NaN. */
+pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                           const int32_t* block_tables, const int32_t* context_lens,
+                                           const int32_t* query_start, float scale, float k_scale, float v_scale,
+                                           int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                           int num_seqs, int max_blocks_per_seq, int num_blocks, int max_query_len,
+                                           pkv_dtype dtype, void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_err, pkv_stream_t stream);
+
+/* The same over q4_0 caches. K and V values d * (q - 8) are rounded to binary16
+ * on the way (relative 2^-11, below 2^-14 absolute 2^-25; values beyond 65504,
+ * which only rows of bfloat16 give, become infinite and count as such). */
+pkv_status pkv_paged_attention_prefill_q4_0(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                            const int32_t* block_tables, const int32_t* context_lens,
+                                            const int32_t* query_start, float scale, int num_heads, int num_kv_heads,
+                                            int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
+                                            int num_blocks, int max_query_len, pkv_dtype dtype, void* workspace,
+                                            size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream);
+
+/* The counters at the start of a workspace of prefill over quantised caches. */
+#define PKV_PREFILL_COUNTER_BYTES 4096
+
+/* Bytes of workspace the two calls need, whatever the sizes. Pure host function; 0
+ * for a head_dim that they do not take. */
+size_t pkv_prefill_workspace_bytes(int head_dim);
+
 /* Bytes of workspace pkv_paged_attention_decode needs for these sizes: the
  * segment counters (num_seqs * num_heads int32) plus a fixed area for the
  * partial results of the split segments (independent of the context lengths;

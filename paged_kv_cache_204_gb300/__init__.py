@@ -23,6 +23,8 @@ Functions mirror the C entry points:
                           -> decode that adds up attention weights, and the eviction that goes by them
   rope_and_cache, rope_and_cache_fp8, rope_and_cache_q4_0
                           -> cache writes with rotary positions (of one axis or several)
+  paged_attention_prefill_fp8, paged_attention_prefill_q4_0
+                          -> prefill over the fp8 and the 4-bit caches
   set_wait_timeout_ns / get_wait_timeout_ns, status_string, version
 The host block manager (include/pkv_block_manager.h) is wrapped by
 ``paged_kv_cache_204_gb300.block_manager.BlockManager``.
@@ -137,6 +139,15 @@ lib.pkv_rope_and_cache_fp8.argtypes = [*_ROPE, _F, _F, _P, _P]
 lib.pkv_rope_and_cache_fp8.restype = _I
 lib.pkv_rope_and_cache_q4_0.argtypes = [*_ROPE, _P, _P]
 lib.pkv_rope_and_cache_q4_0.restype = _I
+lib.pkv_prefill_workspace_bytes.argtypes = [_I]
+lib.pkv_prefill_workspace_bytes.restype = _SZ
+lib.pkv_paged_attention_prefill_fp8.argtypes = [_P, _P, _P, _P, _P, _P, _P, _F, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I,
+                                                _I, _P, _SZ, _P, _P]
+lib.pkv_paged_attention_prefill_fp8.restype = _I
+lib.pkv_paged_attention_prefill_q4_0.argtypes = [_P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                                                 _P, _SZ, _P, _P]
+lib.pkv_paged_attention_prefill_q4_0.restype = _I
+PREFILL_COUNTER_BYTES = 4096  # PKV_PREFILL_COUNTER_BYTES
 WINDOW_COUNTER_BYTES = 524288  # PKV_WINDOW_COUNTER_BYTES
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PKV_NOALLOC_SCRATCH_BYTES
 
@@ -500,3 +511,38 @@ def rope_and_cache_q4_0(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     """rope_and_cache into uint8 pools of q4_0 rows (reshape_and_cache_q4_0); q, k, v fp16/bf16."""
     _check(_binding().rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, 2, 1.0, 1.0,
                                      pair_axis, interleaved, dev_err, stream), "pkv_rope_and_cache_q4_0")
+
+
+def prefill_workspace_bytes(head_dim: int) -> int:
+    return lib.pkv_prefill_workspace_bytes(head_dim)
+
+
+def new_prefill_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    """A workspace of paged_attention_prefill_fp8 and paged_attention_prefill_q4_0: its counters zeroed,
+    the room for partial results as it comes. It serves calls of any sizes of that head_dim or a smaller one."""
+    ws = torch.empty(prefill_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
+    ws[:PREFILL_COUNTER_BYTES].zero_()
+    return ws
+
+
+def paged_attention_prefill_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                                scale: float, k_scale: float, v_scale: float, max_query_len: int,
+                                workspace: torch.Tensor, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """paged_attention_prefill over uint8 pools of e4m3 codes: K values are
+    k_scale * code, V values v_scale * code; q, out fp16/bf16. workspace:
+    new_prefill_workspace()."""
+    _check(_binding().prefill_quant(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, k_scale,
+                                    v_scale, max_query_len, workspace, dev_err, stream),
+           "pkv_paged_attention_prefill_fp8")
+
+
+def paged_attention_prefill_q4_0(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                                 scale: float, max_query_len: int, workspace: torch.Tensor,
+                                 dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """paged_attention_prefill over uint8 pools of q4_0 rows; q, out fp16/bf16.
+    workspace: new_prefill_workspace()."""
+    _check(_binding().prefill_quant(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, None,
+                                    None, max_query_len, workspace, dev_err, stream),
+           "pkv_paged_attention_prefill_q4_0")

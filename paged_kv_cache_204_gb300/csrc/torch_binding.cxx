@@ -331,9 +331,45 @@ PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, k_scale and
+// v_scale (both None: q4_0 pools), max_query_len, workspace, dev_err, stream
+PyObject* prefill_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&] {
+    const Cache c(a[2], a[3], a[4], a[5]);
+    const bool q4 = a[8] == Py_None;
+    const at::Tensor &qt = tensor(a[1], "q"), &ot = tensor(a[0], "out");
+    if (qt.dim() != 3) refuse_tensor(qt, "q", "[rows, num_heads, head_dim]");
+    if (c.k.scalar_type() != at::kByte) refuse_tensor(c.k, "k_cache", "a uint8 pool");
+    const char* need = "a contiguous [rows, num_heads, head_dim] tensor on the pools' device, out of q's type";
+    const void* q = want(qt, "q", qt.scalar_type(), qt.sizes(), c.dev, need);
+    void* out = want(ot, "out", qt.scalar_type(), qt.sizes(), c.dev, need);
+    const int H = Pools::size(qt, 1), D = Pools::size(qt, 2);
+    if (c.D != (q4 ? D / 16 * 9 : D))
+      refuse_tensor(c.k, "k_cache", q4 ? "q4_0 rows of 9 head_dim / 16 bytes" : "e4m3 rows of head_dim bytes");
+    const auto start = static_cast<const int32_t*>(want(tensor(a[6], "query_start"), "query_start", at::kInt, {c.B + 1},
+                                                        c.dev, "contiguous int32 [num_seqs + 1] on the pools' device"));
+    const float scale = as_float(a[7]);
+    const int longest = as_int(a[10], "max_query_len");
+    size_t bytes;
+    void* ws = c.workspace(a[11], &bytes);
+    int32_t* err = c.error_word(a[12]);
+    const pkv_dtype code = code_of(qt.scalar_type(), "q");
+    const float k_scale = q4 ? 1.f : as_float(a[8]), v_scale = q4 ? 1.f : as_float(a[9]);
+    const c10::cuda::CUDAGuard guard(c.dev);
+    const pkv_stream_t stream = c.stream(a[13]);
+    if (q4)
+      return pkv_paged_attention_prefill_q4_0(out, q, c.k.data_ptr(), c.v.data_ptr(), c.table(), c.lens, start, scale,
+                                              H, c.Hkv, D, c.bs, c.B, c.MB, c.nb, longest, code, ws, bytes, err,
+                                              stream);
+    return pkv_paged_attention_prefill_fp8(out, q, c.k.data_ptr(), c.v.data_ptr(), c.table(), c.lens, start, scale,
+                                           k_scale, v_scale, H, c.Hkv, D, c.bs, c.B, c.MB, c.nb, longest, code, ws,
+                                           bytes, err, stream);
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(decode_window), ENTRY(prefill_window), ENTRY(decode_scores), ENTRY(evict_tokens),
-                         ENTRY(rope_and_cache),
+                         ENTRY(rope_and_cache), ENTRY(prefill_quant),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_torch", "Calls with torch tensors", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -52,6 +52,6 @@ def q4_values(rows):
     """The float64 values that q4_0 rows stand for."""
     n = rows.shape[-1] // 9
     d = np.ascontiguousarray(rows[..., :n]).view(np.float16).astype(np.float64)
-    code = rows[..., n:].reshape(*rows.shape[:-1], -1, 16)
+    code = rows[..., n:].reshape(*rows.shape[:-1], n // 2, 16)
     code = np.concatenate([code & 15, code >> 4], -1).astype(np.float64) - 8
-    return (code * d[..., None]).reshape(*rows.shape[:-1], -1)
+    return (code * d[..., None]).reshape(*rows.shape[:-1], 16 * n)
