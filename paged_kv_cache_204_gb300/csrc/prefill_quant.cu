@@ -1,87 +1,92 @@
-// Prefill over quantised caches: a warp to a query row, lanes over the head dims.
-#include "common.cuh"
-#include "prefill_quant.h"
+// Launch of prefill over quantised caches (binary16 and bfloat16 queries; q4_0 and e4m3 pools).
+#include "prefill_quant.cuh"
+
+#include <limits>
 
 namespace pkv {
 
 namespace {
 
-// Values 4 l .. 4 l + 3 (head_dim 128) or 2 l, 2 l + 1 (64) of a cache row.
-template <bool Q4, int D>
-__device__ __forceinline__ void row_values(const unsigned char* row, int lane, float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int d = lane * (D / 32) + i;
-    if constexpr (Q4) {
-      const float s = __half2float(__ushort_as_half(reinterpret_cast<const unsigned short*>(row)[d / 32]));
-      const int byte = row[D / 16 + d / 32 * 16 + d % 16];
-      x[i] = s * (float)((d % 32 < 16 ? byte & 15 : byte >> 4) - 8);
-    } else {
-      __nv_fp8_e4m3 v;
-      v.__x = row[d];
-      x[i] = (float)v;
-    }
-  }
-}
+size_t counters_end() { return PKV_PREFILL_COUNTER_BYTES; }
+size_t ml_bytes() { return sizeof(float2) * 2 * kPqMaxCtas * 256; }
 
-template <typename T, bool Q4, int D>
-__global__ void __launch_bounds__(128) prefill_quant_kernel(const __grid_constant__ PrefillQuantParams p) {
-  constexpr int N = D / 32, kRow = Q4 ? D / 16 * 9 : D;
-  const int lane = threadIdx.x & 31, s = blockIdx.z, h = blockIdx.y;
-  const int L = p.context_lens[s], q0 = p.query_start[s], n = p.query_start[s + 1] - q0;
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (L < 0 || L > p.max_blocks_per_seq * p.block_size || n < 0 || n > L || n > p.max_query_len) {
-    if (i == 0 && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
-    return;
+template <typename T, PqFormat F, int D>
+cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
+  using S = PqShape<F, D>;
+  auto kernel = pa_prefill_quant_kernel<T, F, D>;
+  static int sms_of_device[64] = {0};  // SMs per device ordinal (0 = not yet known)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = (dev >= 0 && dev < 64) ? __atomic_load_n(&sms_of_device[dev], __ATOMIC_ACQUIRE) : 0;
+  if (sms == 0) {
+    // the warpgroups' shares of registers are taken from what the launch has: a kernel that was
+    // given fewer would wait for them without end
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != 128) return cudaErrorNotSupported;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&sms_of_device[dev], sms, __ATOMIC_RELEASE);
   }
-  if (i >= n) return;
-  const int g = h / p.group;
-  const size_t at = ((size_t)(q0 + i) * p.num_heads + h) * D + lane * N;
-  float q[N], o[N] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < N; ++e) q[e] = to_float(static_cast<const T*>(p.q)[at + e]);
-  for (int t = 0; t <= L - n + i; ++t) {
-    const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + t / p.block_size];
-    float k[N] = {}, v[N] = {}, x = 0.f;
-    if (b >= 0 && b < p.num_blocks) {
-      const size_t row = (((size_t)b * p.num_kv_heads + g) * p.block_size + t % p.block_size) * kRow;
-      row_values<Q4, D>(static_cast<const unsigned char*>(p.k_cache) + row, lane, k);
-      row_values<Q4, D>(static_cast<const unsigned char*>(p.v_cache) + row, lane, v);
-    } else if (lane == 0) {
-      set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
-    }
-    for (int e = 0; e < N; ++e) x += q[e] * k[e];
-    for (int e = 16; e > 0; e >>= 1) x += __shfl_xor_sync(kFullMask, x, e);
-    x *= p.scale * p.k_scale;
-    const float top = fmaxf(m, x), keep = expf(m - top), w = expf(x - top);
-    l = l * keep + w;
-    for (int e = 0; e < N; ++e) o[e] = o[e] * keep + w * v[e];
-    m = top;
-  }
-  for (int e = 0; e < N; ++e) store_elem(static_cast<T*>(p.out) + at + e, o[e] * p.v_scale / l);
-}
-
-template <typename T, bool Q4, int D>
-cudaError_t launch(const PrefillQuantParams& p, cudaStream_t stream) {
-  if (p.num_heads > 65535) return cudaErrorNotSupported;
-  const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
-  const int64_t queries = p.max_query_len < longest ? p.max_query_len : longest;
-  prefill_quant_kernel<T, Q4, D><<<dim3((unsigned)((queries + 3) / 4), p.num_heads, p.num_seqs), 128, 0, stream>>>(p);
+  PqParams p{};
+  p.out = a.out;
+  p.q = a.q;
+  p.k_cache = static_cast<const unsigned char*>(a.k_cache);
+  p.v_cache = static_cast<const unsigned char*>(a.v_cache);
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.query_start = a.query_start;
+  // scores are taken raw, so the factor has to be positive: a negative one's sign goes into the
+  // queries, and 0 becomes the smallest number: any finite score's product with it is next to nothing
+  const float factor = a.scale * a.k_scale * 1.4426950408889634f;
+  p.flip = factor < 0.f ? 0x80008000u : 0u;
+  p.zero_scale = factor == 0.f;
+  p.scale_log2 = factor == 0.f ? std::numeric_limits<float>::denorm_min() : fabsf(factor);
+  p.v_scale = a.v_scale;
+  p.num_seqs = a.num_seqs;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = a.group;
+  p.block_size = a.block_size;
+  p.block_bits = a.block_size == 8 ? 3 : (a.block_size == 16 ? 4 : 5);
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.num_blocks = a.num_blocks;
+  // rows of a kv head's queries are counted in 32 bits
+  const int64_t longest = (int64_t)a.max_blocks_per_seq * a.block_size;
+  const int64_t queries = a.max_query_len < longest ? a.max_query_len : longest;
+  if (queries * a.group > 0x7fffffffLL - 256) return cudaErrorNotSupported;
+  p.max_query_len = a.max_query_len;
+  p.by_group.set((uint32_t)a.group);
+  char* ws = static_cast<char*>(a.workspace);
+  p.counter = reinterpret_cast<int32_t*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + counters_end());
+  p.part_o = reinterpret_cast<float4*>(ws + counters_end() + ml_bytes());
+  p.dev_err = a.dev_err;
+  p.wait_limit_ns = a.wait_limit_ns;
+  kernel<<<sms < kPqMaxCtas ? sms : kPqMaxCtas, kPqThreads, S::kSmemBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <bool Q4>
+template <PqFormat F>
 PrefillQuantLauncher of(bool bf16, int head_dim) {
-  if (head_dim == 64) return bf16 ? launch<__nv_bfloat16, Q4, 64> : launch<__half, Q4, 64>;
-  if (head_dim == 128) return bf16 ? launch<__nv_bfloat16, Q4, 128> : launch<__half, Q4, 128>;
+  if (head_dim == 64) return bf16 ? launch<__nv_bfloat16, F, 64> : launch<__half, F, 64>;
+  if (head_dim == 128) return bf16 ? launch<__nv_bfloat16, F, 128> : launch<__half, F, 128>;
   return nullptr;
 }
 
 }  // namespace
 
-size_t prefill_quant_workspace_bytes(int head_dim) { return head_dim == 64 || head_dim == 128 ? 4096 : 0; }
+size_t prefill_quant_workspace_bytes(int head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return counters_end() + ml_bytes() + sizeof(float) * 2 * kPqMaxCtas * 256 * (size_t)head_dim;
+}
 
 PrefillQuantLauncher prefill_quant_launcher(bool q4, bool bf16, int head_dim) {
-  return q4 ? of<true>(bf16, head_dim) : of<false>(bf16, head_dim);
+  return q4 ? of<PqFormat::kQ4>(bf16, head_dim) : of<PqFormat::kFp8>(bf16, head_dim);
 }
 
 }  // namespace pkv
