@@ -25,7 +25,7 @@ cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs != 128) return cudaErrorNotSupported;
+    if (attr.numRegs < kPqLaunchRegs) return cudaErrorNotSupported;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

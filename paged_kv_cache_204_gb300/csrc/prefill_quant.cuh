@@ -28,13 +28,17 @@
 
 namespace pkv {
 
-constexpr int kPqThreads = 512;   // 2 softmax warpgroups; MMA warps of A and B, copying warp; 4 converting warps
+// 4 softmax warpgroups; MMA warps of A and B, copying warp, walking warp; a converting warpgroup
+constexpr int kPqThreads = 768;
+constexpr int kPqSoft = 16;       // softmax warps: A's first and second halves of the columns, B's
+constexpr int kPqConvert = 4;     // converting warps
 constexpr int kPqMaxCtas = 152;
-// Registers of a thread after the split, which the launch's 128 add up to: softmax, MMA and copy, conversion.
-constexpr int kPqSoftRegs = 176, kPqIssueRegs = 64, kPqConvertRegs = 96;
-static_assert(2 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs == 4 * 128, "no more than the launch has");
+// Registers of a thread after the split, which the launch's 96 add up to: softmax, MMA and copy, conversion.
+constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 96, kPqIssueRegs = 48, kPqConvertRegs = 48;
+static_assert(4 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs <= kPqThreads / 128 * kPqLaunchRegs, "no more than the launch has");
 constexpr int kPqStart = 256;     // a pair's start and end, as tokens of its walk
 constexpr int kPqMinTokens = 512; // a CTA's stretch is no shorter
+constexpr int kPqRing = 4;        // parts that the walking warp may be ahead
 
 // Cost of what a CTA does, in tokens x group.
 using PqCost = long long;
@@ -52,7 +56,7 @@ struct PqParams {
   int zero_scale;    // scale 0: rows have equal weights, their exponents left alone
   int num_seqs, num_heads, num_kv_heads, group, block_size, block_bits, max_blocks_per_seq, num_blocks, max_query_len;
   PwDivisor by_group;
-  int32_t* counter;  // [kPqMaxCtas]
+  int32_t* counter;  // [kPqMaxCtas], of the pairs that start in a CTA and do not end there
   float2* part_ml;   // [2 kPqMaxCtas][256]
   float4* part_o;    // [2 kPqMaxCtas][D / 4][256]
   int32_t* dev_err;
@@ -69,11 +73,15 @@ struct PqShape {
   static constexpr int kRow = F == PqFormat::kQ4 ? D / 16 * 9 : D;   // bytes of a cache row
   static constexpr int kRaw = 128 * kRow;
   static constexpr int kRawStages = D == 64 ? 6 : (F == PqFormat::kQ4 ? 3 : 2);
-  static constexpr int kStageOff = 2 * kTile;                        // links: K, V, K, V
+  static constexpr int kStageOff = 2 * kTile;                        // K, V, K, V
   static constexpr int kRawOff = kStageOff + 4 * kTile;
   static constexpr int kBarOff = kRawOff + kRawStages * kRaw;
-  static constexpr int kMiscOff = kBarOff + 32 * 8;
-  static constexpr int kUsed = kMiscOff + 256 + 512 + 1024;          // + alignment slack
+  static constexpr int kBars = 2 * kRawStages + 18 + 2 * kPqRing + 16 + 4;
+  static constexpr int kRingOff = (kBarOff + 8 * kBars + 15) / 16 * 16;
+  static constexpr int kSwapOff = kRingOff + 64 * kPqRing;
+  static constexpr int kExpOff = kSwapOff + 2 * 2 * 128 * 4;
+  static constexpr int kMiscOff = kExpOff + 2 * 128;
+  static constexpr int kUsed = kMiscOff + 64;
   // more than half of an SM's, so that one CTA has its tensor memory to itself
   static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -111,71 +119,80 @@ struct PqShare {
   }
 };
 
-// A CTA's walk over the pairs (or parts of them) in its stretch; every role makes it for itself.
-struct PqItem {
-  PqSeq seq;
-  int s, kvh, pair, np;
-  PqCost at, cost, lo, hi;  // of the pair: its place and length; the CTA's stretch
-  int row0, rows;           // first row; rows of the kv head's queries
-  int active;               // of the pair
-  int end_a, end_b;         // tokens that the last queries of A and B see
-  int j0, j1;               // K/V tiles of this part
-  bool dual;                // one tile of rows: A and B take K/V tiles in turn
-
-  __device__ __forceinline__ bool done() const { return at >= hi; }
-  __device__ __forceinline__ bool whole() const { return lo <= at && at + cost <= hi; }
-  __device__ __forceinline__ int end() const { return dual ? end_a : end_b; }
-  __device__ __forceinline__ int active_of(int x) const {
-    return dual ? active : max(min(active - 128 * x, 128), 0);
-  }
+// A pair of query tiles, or the part of one that lies in the CTA's stretch.
+struct alignas(16) PqPart {
+  int s, kvh, q0, base;      // sequence; kv head; its first query; tokens before it
+  int row0, active;          // first row; rows of the pair
+  int end_a, end_b;          // tokens that the last queries of A and B see
+  int j0, j1;                // K/V tiles of this part
+  int c0, c1;                // CTAs that the pair's parts lie in
+  int kind;                  // bits below
+  int pad[3];
+  static constexpr int kStop = 1;   // no part: the walk is over
+  static constexpr int kDual = 2;   // one tile of rows: A and B take K/V tiles in turn
+  static constexpr int kHead = 4;   // the pair starts here
+  __device__ __forceinline__ bool stop() const { return kind & kStop; }
+  __device__ __forceinline__ bool dual() const { return kind & kDual; }
+  __device__ __forceinline__ bool whole() const { return c0 == c1; }
+  __device__ __forceinline__ int end() const { return dual() ? end_a : end_b; }
+  __device__ __forceinline__ int active_of(int x) const { return dual() ? active : max(min(active - 128 * x, 128), 0); }
   // Queries of tile x (A: 0, B: 1) take part in K/V tile j.
   __device__ __forceinline__ bool sees(int x, int j) const {
-    if (dual) return ((j - j0) & 1) == x;
-    return x ? j * 128 < end_b : j * 128 < end_a;
+    return dual() ? ((j - j0) & 1) == x : j * 128 < (x ? end_b : end_a);
   }
-  __device__ __forceinline__ void shape(const PqParams& p) {
-    const PqCost c0 = seq.before(pair, p.group);
-    cost = seq.before(pair + 1, p.group) - c0;
-    rows = seq.n * p.group;
-    row0 = pair * 256;
-    active = min(rows - row0, 256);
-    dual = active <= 128;
-    const int base = seq.L - seq.n + 1;
-    end_a = base + p.by_group.of(row0 + min(active, 128) - 1);
-    end_b = dual ? 0 : base + p.by_group.of(row0 + active - 1);
-    const int tiles = (end() + 127) / 128;
+};
+static_assert(sizeof(PqPart) == 64, "a slot of the ring");
+
+// A CTA's walk over the pairs in its stretch.
+struct PqWalk {
+  PqShare share;
+  PqSeq seq;
+  int s, kvh, pair, np;
+  PqCost at, cost, lo, hi;  // the pair's place and length; the CTA's stretch
+
+  __device__ __forceinline__ bool done() const { return at >= hi; }
+  __device__ __forceinline__ PqPart part(const PqParams& p) {
+    PqPart t;
+    cost = seq.before(pair + 1, p.group) - seq.before(pair, p.group);
+    t.s = s, t.kvh = kvh, t.q0 = seq.q0, t.base = seq.L - seq.n;
+    t.row0 = pair * 256;
+    t.active = min(seq.n * p.group - t.row0, 256);
+    const bool dual = t.active <= 128, head = lo <= at;
+    t.end_a = t.base + 1 + p.by_group.of(t.row0 + min(t.active, 128) - 1);
+    t.end_b = dual ? 0 : t.base + 1 + p.by_group.of(t.row0 + t.active - 1);
+    t.kind = (dual ? PqPart::kDual : 0) | (head ? PqPart::kHead : 0);
+    const int tiles = (t.end() + 127) / 128;
     const PqCost a = max(lo - at, (PqCost)0), b = min(hi - at, cost);
-    j0 = a == 0 ? 0 : (int)(tiles * a / cost);
-    j1 = b == cost ? tiles : (int)(tiles * b / cost);
+    t.j0 = a == 0 ? 0 : (int)(tiles * a / cost);
+    t.j1 = b == cost ? tiles : (int)(tiles * b / cost);
+    t.c0 = head ? (int)blockIdx.x : share.of(at);
+    t.c1 = at + cost <= hi ? (int)blockIdx.x : share.of(at + cost - 1);
+    return t;
   }
   __device__ __forceinline__ void next(const PqParams& p) {
     at += cost;
-    if (at >= hi) return;
-    if (++pair == np) {
-      pair = 0;
-      if (++kvh == p.num_kv_heads) {
-        kvh = 0;
-        // the next sequence with queries: there is one, the stretch not being at its end
-        for (++s; s < p.num_seqs; s += 32) {
-          PqSeq q;
-          q.live = false;
-          const int mine = s + (int)(threadIdx.x & 31);
-          if (mine < p.num_seqs) q.load(p, mine);
-          const uint32_t some = __ballot_sync(kFullMask, q.live);
-          if (some != 0u) {
-            s += __ffs(some) - 1;
-            break;
-          }
-        }
-        if (s >= p.num_seqs) {
-          at = hi;
-          return;
-        }
-        seq.load(p, s);
-        np = seq.pairs(p.group);
+    if (at >= hi || ++pair < np) return;
+    pair = 0;
+    if (++kvh < p.num_kv_heads) return;
+    kvh = 0;
+    // the next sequence with queries: there is one, the stretch not being at its end
+    for (++s; s < p.num_seqs; s += 32) {
+      PqSeq q;
+      q.live = false;
+      const int mine = s + (int)(threadIdx.x & 31);
+      if (mine < p.num_seqs) q.load(p, mine);
+      const uint32_t some = __ballot_sync(kFullMask, q.live);
+      if (some != 0u) {
+        s += __ffs(some) - 1;
+        break;
       }
     }
-    shape(p);
+    if (s >= p.num_seqs) {
+      at = hi;
+      return;
+    }
+    seq.load(p, s);
+    np = seq.pairs(p.group);
   }
 };
 
@@ -222,82 +239,66 @@ __device__ __forceinline__ uint32_t pq_from_e4m3x2(uint32_t two) {
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 
-// Row r of a tile: its bytes at `row` become the operand's values (zeros where !held) in the
-// swizzled tile at `tile`.
+// One half (h) of row r of a tile: its bytes at `row` become the operand's values (zeros where
+// !held) in the swizzled tile at `tile`.
 template <PqFormat F, int D>
-__device__ __forceinline__ void pq_convert_row(const unsigned char* row, unsigned char* tile, int r, bool held) {
+__device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, int h, bool held) {
   unsigned char* at = tile + r * 128;
   const uint32_t swz = (r & 7) << 4;
   // values 8 c .. 8 c + 7 of the row
   auto put = [&](int c, uint4 v) {
     *reinterpret_cast<uint4*>(at + (c >> 3) * (128 * 128) + ((((uint32_t)c & 7) << 4) ^ swz)) = v;
   };
+  const int c0 = h * (D / 16);
   if (!held) {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) put(c, make_uint4(0u, 0u, 0u, 0u));
+    for (int c = 0; c < D / 16; ++c) put(c0 + c, make_uint4(0u, 0u, 0u, 0u));
     return;
   }
+  // all is read before anything is written, so that the reads need not wait for one another
   if constexpr (F == PqFormat::kQ4) {
-    // (rows start on 8 bytes at head_dim 128, on 4 at 64)
+    constexpr int kBlocks = D / 64;  // of this half
+    uint32_t w[4 * kBlocks], scales;
+    const unsigned char* codes = row + D / 16 + 16 * kBlocks * h;
+    if constexpr (D == 128) {  // (rows start on 8 bytes at head_dim 128, on 4 at 64)
+      scales = reinterpret_cast<const uint32_t*>(row)[h];
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-      const __half2 d = __half2half2(*reinterpret_cast<const __half*>(row + 2 * b));
-      uint32_t w[4];
-      const unsigned char* codes = row + D / 16 + 16 * b;
-      if constexpr (D == 128) {
-        const uint2 x = *reinterpret_cast<const uint2*>(codes), y = *reinterpret_cast<const uint2*>(codes + 8);
-        w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(codes)[i];
+      for (int i = 0; i < 2 * kBlocks; ++i) {
+        const uint2 x = reinterpret_cast<const uint2*>(codes)[i];
+        w[2 * i] = x.x, w[2 * i + 1] = x.y;
       }
+    } else {
+      scales = reinterpret_cast<const unsigned short*>(row)[h];
+#pragma unroll
+      for (int i = 0; i < 4 * kBlocks; ++i) w[i] = reinterpret_cast<const uint32_t*>(codes)[i];
+    }
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      const __half2 d = __half2half2(__ushort_as_half((unsigned short)(scales >> (16 * b))));
       uint4 lo, hi;
-      pq_from_q4(w[0], w[1], d, lo, hi);
-      put(4 * b, lo);
-      put(4 * b + 2, hi);
-      pq_from_q4(w[2], w[3], d, lo, hi);
-      put(4 * b + 1, lo);
-      put(4 * b + 3, hi);
+      pq_from_q4(w[4 * b], w[4 * b + 1], d, lo, hi);
+      put(c0 + 4 * b, lo);
+      put(c0 + 4 * b + 2, hi);
+      pq_from_q4(w[4 * b + 2], w[4 * b + 3], d, lo, hi);
+      put(c0 + 4 * b + 1, lo);
+      put(c0 + 4 * b + 3, hi);
     }
   } else {
     // lanes take a row's 16-byte chunks in orders of their own, so that eight lanes' chunks fall
     // into different banks
     const int turn = D == 128 ? r & 7 : (r >> 1) & 3;
+    uint4 x[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const int c = i ^ turn;
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * c);
-      put(2 * c, make_uint4(pq_from_e4m3x2(x.x & 0xffffu), pq_from_e4m3x2(x.x >> 16), pq_from_e4m3x2(x.y & 0xffffu),
-                            pq_from_e4m3x2(x.y >> 16)));
-      put(2 * c + 1, make_uint4(pq_from_e4m3x2(x.z & 0xffffu), pq_from_e4m3x2(x.z >> 16),
-                                pq_from_e4m3x2(x.w & 0xffffu), pq_from_e4m3x2(x.w >> 16)));
+    for (int i = 0; i < D / 32; ++i) x[i] = *reinterpret_cast<const uint4*>(row + 16 * ((h * (D / 32) + i) ^ turn));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int c = (h * (D / 32) + i) ^ turn;
+      put(2 * c, make_uint4(pq_from_e4m3x2(x[i].x & 0xffffu), pq_from_e4m3x2(x[i].x >> 16),
+                            pq_from_e4m3x2(x[i].y & 0xffffu), pq_from_e4m3x2(x[i].y >> 16)));
+      put(2 * c + 1, make_uint4(pq_from_e4m3x2(x[i].z & 0xffffu), pq_from_e4m3x2(x[i].z >> 16),
+                                pq_from_e4m3x2(x[i].w & 0xffffu), pq_from_e4m3x2(x[i].w >> 16)));
     }
   }
-}
-
-__device__ __forceinline__ void pq_barrier(int id, int threads) {
-  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Four lanes hand round 16-byte pieces: v[i] of lane l becomes v[l % 4] of lane (l & ~3) + i.
-__device__ __forceinline__ void pq_transpose(uint4 (&v)[4]) {
-  const int lane = threadIdx.x & 31;
-  auto swap = [&](uint4& a, uint4& b, int bit) {  // a: index bit clear, b: set
-    const bool up = lane & bit;
-    uint4 send = up ? a : b;
-    send.x = __shfl_xor_sync(kFullMask, send.x, bit);
-    send.y = __shfl_xor_sync(kFullMask, send.y, bit);
-    send.z = __shfl_xor_sync(kFullMask, send.z, bit);
-    send.w = __shfl_xor_sync(kFullMask, send.w, bit);
-    if (up)
-      a = send;
-    else
-      b = send;
-  };
-  swap(v[0], v[1], 1);
-  swap(v[2], v[3], 1);
-  swap(v[0], v[2], 2);
-  swap(v[1], v[3], 2);
 }
 
 template <typename T, PqFormat F, int D>
@@ -307,36 +308,53 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   using P16 = PwPack<__half>;
   constexpr int CB = S::kCB, NR = S::kRawStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // 16-bit parts of P. One part, 2^-12 of a weight and rms half of that, is far below a bfloat16
+  // output's rounding. Beside a binary16 output's it is as much again, and so are together the roundings of
+  // q4_0's K and V: there P has a high part and a remainder (error against 64 bits 1.65 times the
+  // rounding's alone with one part, 1.3 with two; 1.4 over e4m3 pools, whose values are exact).
+  constexpr int kParts = !kBf16 && F == PqFormat::kQ4 ? 2 : 1;
+  extern __shared__ __align__(1024) unsigned char sm[];
   // Every barrier's phases follow one another in the order of the work, and nobody who waits for
-  // a phase can fall two behind.
+  // a phase can fall two behind. K and V tiles are counted through all parts of the CTA: tile m is in
+  // buffers m % 2.
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
-  uint64_t* raw_full = bars;                // [NR] a tile's bytes landed
-  uint64_t* raw_empty = bars + NR;          // [NR] and were converted (an arrival per converting warp)
-  uint64_t* ready = bars + 2 * NR;          // [2] a link's operands are in place (likewise)
-  uint64_t* empty = ready + 2;              // [2] the MMAs are done with it (A's and B's: two arrivals)
-  uint64_t* s_full = ready + 4;             // [A, B] S computed
-  uint64_t* p_full = ready + 6;             // [A, B] P written (one arrival per softmax warp)
-  uint64_t* q_full = ready + 8;             // [A, B] query rows in place (likewise)
-  uint64_t* o_full = ready + 10;            // [A, B] the part's last O computed
-  uint64_t* turn = ready + 12;              // [A, B] the other's MMAs of a link are issued
-  uint64_t* shared_q = ready + 14;          // A's query rows in place for B too (an arrival per warp of A)
-  uint64_t* drained = ready + 15;           // every MMA of the CTA done (two arrivals)
+  uint64_t* raw_full = bars;             // [NR] a tile's bytes landed
+  uint64_t* raw_empty = raw_full + NR;   // [NR] and were converted (an arrival per converting warp)
+  uint64_t* k_ready = raw_empty + NR;    // [2] a K tile is in place (likewise)
+  uint64_t* v_ready = k_ready + 2;       // [2] a V tile is
+  uint64_t* k_empty = k_ready + 4;       // [2] the MMAs are done with it (A's and B's: two arrivals)
+  uint64_t* v_empty = k_ready + 6;       // [2] likewise
+  uint64_t* s_full = k_ready + 8;        // [A, B] S computed
+  uint64_t* p_full = k_ready + 10;       // [A, B] P written (one arrival per softmax warp)
+  uint64_t* q_full = k_ready + 12;       // [A, B] query rows in place (likewise)
+  uint64_t* o_full = k_ready + 14;       // [A, B] the part's last O computed
+  uint64_t* turn = k_ready + 16;         // [A, B] the other's MMAs of a step are issued
+  uint64_t* part_full = k_ready + 18;    // [kPqRing] the walk's next part is there
+  uint64_t* part_empty = part_full + kPqRing;  // [kPqRing] and was read (by every warp but the walking one)
+  uint64_t* box_full = part_empty + kPqRing;   // [8] B's partial results for A's warp are there
+  uint64_t* box_empty = box_full + 8;    // [8] and were read
+  uint64_t* left = box_empty + 8;        // a cut pair's part is in the workspace (one arrival per softmax warp)
+  uint64_t* counted = left + 1;          // and counted
+  uint64_t* shared_q = left + 2;         // A's query rows in place for B too (an arrival per warp of A)
+  uint64_t* drained = left + 3;          // every MMA of the CTA done (two arrivals)
+  PqPart* ring = reinterpret_cast<PqPart*>(sm + S::kRingOff);     // [kPqRing]
+  float* swap = reinterpret_cast<float*>(sm + S::kSwapOff);       // [half][A, B][128] from one half's warp to the other's
+  unsigned char* exps = sm + S::kExpOff;                          // [A, B][128] exponents taken out of the query rows
   unsigned char* misc = sm + S::kMiscOff;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(misc);           // tensor-memory address
-  volatile int* last_flag = reinterpret_cast<int*>(misc + 4);
-  uint32_t* held_blocks = reinterpret_cast<uint32_t*>(misc + 8);  // [NR] blocks of a raw tile that were copied
-  PqBegin* begin = reinterpret_cast<PqBegin*>(misc + 64);
-  float* shared_sc = reinterpret_cast<float*>(misc + 256);        // [128] factors of A's rows for B
-  static_assert(sizeof(PqBegin) <= 128 && 8 + 4 * NR <= 64 && (2 * NR + 16) * 8 <= 32 * 8, "room");
+  uint32_t* slot = reinterpret_cast<uint32_t*>(misc);             // tensor-memory address
+  volatile int* last = reinterpret_cast<int*>(misc + 4);          // the counted part was the last of its pair
+  volatile int* lost = reinterpret_cast<int*>(misc + 8);          // a softmax warp ran out of a wait
+  uint32_t* held_blocks = reinterpret_cast<uint32_t*>(misc + 16); // [NR] blocks of a raw tile that were copied
+  PqBegin* begin = reinterpret_cast<PqBegin*>(swap);              // (read before the first part is there)
+  static_assert(sizeof(PqBegin) <= 128 && 16 + 4 * NR <= 64, "room");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group;
 
   // ---- the CTA's stretch of the whole -----------------------------------------
   {
-    PqCost* sums = reinterpret_cast<PqCost*>(sm);  // [16], before anything else is there
+    constexpr int kWarps = kPqThreads / 32;
+    PqCost* sums = reinterpret_cast<PqCost*>(sm);  // [kWarps], before anything else is there
     auto cost_of = [&](int s) {
       if (s >= p.num_seqs) return (PqCost)0;
       PqSeq q;
@@ -351,8 +369,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     __syncthreads();
     PqShare share;
     share.whole = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) share.whole += sums[i];
+    for (int i = 0; i < kWarps; ++i) share.whole += sums[i];
     const PqCost most = share.whole / ((PqCost)G * kPqMinTokens);
     share.ctas = (int)max(min(most, (PqCost)gridDim.x), (PqCost)1);
     if (share.whole == 0 || (int)blockIdx.x >= share.ctas) return;
@@ -365,8 +382,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       if (lane == 31) sums[warp] = upto;
       __syncthreads();
       PqCost before = base;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kWarps; ++i) {
         if (i < warp) before += sums[i];
         base += sums[i];
       }
@@ -401,104 +417,143 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], kPqConvert);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ready[i], 4);
-      mbar_init(&empty[i], 2);
+      mbar_init(&k_ready[i], kPqConvert);
+      mbar_init(&v_ready[i], kPqConvert);
+      mbar_init(&k_empty[i], 2);
+      mbar_init(&v_empty[i], 2);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&q_full[i], 4);
+      mbar_init(&p_full[i], 8);
+      mbar_init(&q_full[i], 8);
       mbar_init(&o_full[i], 1);
       mbar_init(&turn[i], 1);
     }
-    mbar_init(shared_q, 4);
+    for (int i = 0; i < kPqRing; ++i) {
+      mbar_init(&part_full[i], 1);
+      mbar_init(&part_empty[i], kPqSoft + 3 + kPqConvert);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&box_full[i], 1);
+      mbar_init(&box_empty[i], 1);
+    }
+    mbar_init(left, kPqSoft);
+    mbar_init(counted, 1);
+    mbar_init(shared_q, 8);
     mbar_init(drained, 2);
     mbar_init_fence();
+    *lost = 0;
   }
-  if (warp == 8) tmem_alloc(slot, kPwTmemCols);
+  if (warp == 16) tmem_alloc(slot, kPwTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *slot;
   bool bad = false;  // a wait ran out
-  PqItem it;
-  it.s = begin->s, it.kvh = begin->kvh, it.pair = begin->pair;
-  it.at = begin->at, it.lo = begin->lo, it.hi = begin->hi;
-  it.seq.load(p, it.s);
-  it.np = it.seq.pairs(G);
-  it.shape(p);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // the same answer in the whole warp
+    return __all_sync(kFullMask, pw_wait(bar, parity, p.wait_limit_ns));
+  };
+  // The n-th part of the walk; false where there is none.
+  auto take = [&](uint32_t n, PqPart& part) {
+    if (!bad && !wait(&part_full[n % kPqRing], (n / kPqRing) & 1)) bad = true;
+    if (bad) return false;
+    part = ring[n % kPqRing];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&part_empty[n % kPqRing]);
+    return !part.stop();
+  };
 
   // (the registers of a warpgroup change hands for all its warps at once)
-  if (warp >= 12) {
-    // ---- conversion: V of one tile, K of the next, into the link's operands -----------------
+  if (warp >= 20) {
+    // ---- conversion: K of one tile, V of the one before, into the operands' buffers; a thread to
+    // half a row
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqConvertRegs));
     const int r = tid & 127, block = r >> p.block_bits;
-    uint32_t link = 0, raw = 0;  // links and tiles so far
+    uint32_t tiles = 0;  // of earlier parts
     int stage = 0;
     uint32_t phase = 0;
-    for (; !bad && !it.done(); it.next(p)) {
-      const int end = it.end();
-      for (int j = it.j0; j <= it.j1 && it.j0 < it.j1 && !bad; ++j, ++link) {
-        const uint32_t c = link & 1;
-        if (link >= 2 && !__all_sync(kFullMask, pw_wait(&empty[c], ((link >> 1) + 1) & 1, p.wait_limit_ns))) {
+    PqPart part;
+    for (uint32_t n = 0; take(n, part); ++n) {
+      const int end = part.end(), j0 = part.j0, j1 = part.j1;
+      for (int i = 0; i < 2 * (j1 - j0) && !bad; ++i) {
+        // K0, K1, V0, K2, V1, ...
+        const bool is_v = i == 2 * (j1 - j0) - 1 || (i > 0 && (i & 1) == 0);
+        const int j = j0 + (is_v ? (i - 1) / 2 : (i + 1) / 2);
+        const uint32_t m = tiles + (j - j0), c = m & 1;
+        if (m >= 2 && !wait((is_v ? v_empty : k_empty) + c, ((m >> 1) + 1) & 1)) {
           bad = true;
           break;
         }
-#pragma unroll 1
-        for (int which = 1; which >= 0; --which) {  // V of tile j - 1, K of tile j
-          const int t = j - which;
-          if (t < it.j0 || t >= it.j1) continue;
-          if (!__all_sync(kFullMask, pw_wait(&raw_full[stage], phase, p.wait_limit_ns))) {
-            bad = true;
-            break;
-          }
-          const bool held = t * 128 + r < end && ((held_blocks[stage] >> block) & 1u);
-          pq_convert_row<F, D>(sm + S::kRawOff + stage * S::kRaw + r * S::kRow,
-                               sm + S::kStageOff + (2 * c + which) * S::kTile, r, held);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[stage]);
-          ++raw;
-          if (++stage == NR) stage = 0, phase ^= 1;
+        if (!wait(&raw_full[stage], phase)) {
+          bad = true;
+          break;
         }
+        const bool held = j * 128 + r < end && ((held_blocks[stage] >> block) & 1u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pq_convert<F, D>(sm + S::kRawOff + stage * S::kRaw + r * S::kRow,
+                           sm + S::kStageOff + (2 * c + is_v) * S::kTile, r, h, held);
         fence_async_smem();
         __syncwarp();
-        if (!bad && lane == 0) mbar_arrive(&ready[c]);
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[stage]);
+          mbar_arrive((is_v ? v_ready : k_ready) + c);
+        }
+        if (++stage == NR) stage = 0, phase ^= 1;
       }
+      tiles += j1 - j0;
     }
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqIssueRegs));
-    if (warp == 9) {
-    // ---- copies: a tile's cache blocks, one to a lane -----------------------------------------
-    const int per_tile = 128 >> p.block_bits;  // <= 16 blocks
-    const uint32_t bytes = (uint32_t)p.block_size * S::kRow;
-    uint32_t raw = 0;
-    int stage = 0;
-    uint32_t phase = 1;  // of raw_empty, from the second round on
-    for (; !bad && !it.done(); it.next(p)) {
-      const int32_t* bt = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
-      const int blocks = (it.end() + p.block_size - 1) >> p.block_bits;
-      auto fetch = [&](int j) {
-        const int b = j * per_tile + lane;
-        return j < it.j1 && lane < per_tile && b < blocks ? __ldg(bt + b) : -2;  // -2: none there
-      };
-      int id = fetch(it.j0), id_v = -2;
-      for (int j = it.j0; j <= it.j1 && it.j0 < it.j1 && !bad; ++j) {
-        if (id != -2 && (id < 0 || id >= p.num_blocks)) {
-          set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
-          id = -2;
+    if (warp == 18) {
+      // ---- the walk
+      PqWalk walk;
+      walk.share = begin->share;
+      walk.s = begin->s, walk.kvh = begin->kvh, walk.pair = begin->pair;
+      walk.at = begin->at, walk.lo = begin->lo, walk.hi = begin->hi;
+      walk.seq.load(p, walk.s);
+      walk.np = walk.seq.pairs(G);
+      for (uint32_t n = 0;; ++n) {
+        if (n >= kPqRing && !wait(&part_empty[n % kPqRing], (n / kPqRing + 1) & 1)) {
+          bad = true;
+          break;
         }
-        const int id_next = fetch(j + 1);
-#pragma unroll
-        for (int which = 1; which >= 0; --which) {  // V of tile j - 1, K of tile j
-          const int t = j - which;
-          if (t < it.j0 || t >= it.j1 || bad) continue;
-          if (raw >= NR && !__all_sync(kFullMask, pw_wait(&raw_empty[stage], phase, p.wait_limit_ns))) {
+        const bool stop = walk.done();
+        PqPart part;
+        if (!stop) part = walk.part(p);
+        if (lane == 0) {
+          if (stop)
+            ring[n % kPqRing].kind = PqPart::kStop;
+          else
+            ring[n % kPqRing] = part;
+          mbar_arrive(&part_full[n % kPqRing]);
+        }
+        __syncwarp();
+        if (stop) break;
+        walk.next(p);
+      }
+    } else if (warp == 17) {
+      // ---- copies: a tile's cache blocks, one to a lane
+      const int per_tile = 128 >> p.block_bits;  // <= 16 blocks
+      const uint32_t bytes = (uint32_t)p.block_size * S::kRow;
+      uint32_t raw = 0;  // tiles so far
+      int stage = 0;
+      uint32_t phase = 1;  // of raw_empty, from the second round on
+      PqPart part;
+      for (uint32_t n = 0; take(n, part); ++n) {
+        const int32_t* bt = p.block_tables + (size_t)part.s * p.max_blocks_per_seq;
+        const int blocks = (part.end() + p.block_size - 1) >> p.block_bits, j0 = part.j0, j1 = part.j1;
+        auto fetch = [&](int j) {
+          const int b = j * per_tile + lane;
+          return j < j1 && lane < per_tile && b < blocks ? __ldg(bt + b) : -2;  // -2: none there
+        };
+        auto copy = [&](int b, const unsigned char* pool) {
+          if (raw >= NR && !wait(&raw_empty[stage], phase)) {
             bad = true;
-            break;
+            return;
           }
-          const int b = which ? id_v : id;
           const uint32_t some = __ballot_sync(kFullMask, b != -2);
           if (lane == 0) {
             held_blocks[stage] = some;
@@ -507,397 +562,444 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           __syncwarp();
           if (b != -2)
             bulk_copy_g2s(sm + S::kRawOff + stage * S::kRaw + lane * bytes,
-                          (which ? p.v_cache : p.k_cache) + ((size_t)b * p.num_kv_heads + it.kvh) * bytes, bytes,
-                          &raw_full[stage]);
+                          pool + ((size_t)b * p.num_kv_heads + part.kvh) * bytes, bytes, &raw_full[stage]);
           ++raw;
           if (++stage == NR) stage = 0, phase ^= 1;
-        }
-        id_v = id;
-        id = id_next;
-      }
-    }
-    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-    // the last copies must land before the CTA can leave
-    if (lane == 0)
-      for (uint32_t c = raw >= NR ? raw - NR : 0; c < raw; ++c)
-        mbar_wait_bounded(&raw_full[c % NR], (c / NR) & 1, kDrainLimitNs);
-    __syncwarp();
-    } else if (warp != 10) {
-    // ---- MMA issue, a warp for each of A and B ------------------------------------------
-    // Per link: O += P V of one tile, S of the next. With two tiles of rows at head_dim 128 A and B
-    // take turns, so that one's softmax runs under the other's MMAs. MMAs of one thread complete
-    // in order, so S may take the place of a P that the MMA before it reads, and "S done" says
-    // that O holds every earlier tile.
-    const int x = warp == 8 ? 0 : 1;
-    constexpr uint32_t id_s = mma_idesc_f16(128, 128, 0, 0);
-    constexpr uint32_t id_o = mma_idesc_f16(128, D, 0, 1);
-    const uint32_t tb = __shfl_sync(kFullMask, tbase, 0);
-    const uint32_t sb = __shfl_sync(kFullMask, smem_u32(sm), 0);
-    // of a descriptor only the start address in its low word moves
-    const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
-    const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
-    const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
-    uint32_t link = 0, nth = 0, done = 0, turns = 0;  // links, parts, P's and links in turn so far
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool ok = __all_sync(kFullMask, pw_wait(bar, parity, p.wait_limit_ns));
-      tc_fence_after();
-      return ok;
-    };
-    for (; !bad && !it.done(); it.next(p)) {
-      const int tiles = it.j1 - it.j0;
-      const bool in_turn = D == 128 && !it.dual;
-      const uint32_t qd = (uint32_t)smem_desc_sw128(sb + (it.dual ? 0 : x) * S::kTile, 16, 1024);
-      bool seen = false, opened = false;  // the tile at hand is seen, O holds something
-      bad = !wait(&q_full[x], nth & 1);
-      for (int i = tiles > 0 ? 0 : 1; i <= tiles && !bad; ++i, ++link) {  // O of tile i - 1, S of tile i
-        const uint32_t c = link & 1;
-        const bool next = i < tiles && it.sees(x, it.j0 + i);
-        bad = !wait(&ready[c], (link >> 1) & 1);
-        if (in_turn && !bad && (x == 1 || turns > 0)) bad = !wait(&turn[x], (turns + (x ^ 1)) & 1);
-        // (a part's first P comes from warps that have read the O of the part before)
-        if (!bad && seen) bad = !wait(&p_full[x], done++ & 1);
-        if (!bad && elect_one()) {
-          if (seen) {
-            const uint32_t vb = vd + (c * (2 * S::kTile) >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 8 * ks, vb + (ks * 2048 >> 4), hi, id_o,
-                        (ks > 0 || opened) ? 1u : 0u);
+        };
+        int id = fetch(j0), id_v = -2;
+        for (int j = j0; j <= j1 && j0 < j1 && !bad; ++j) {  // K of tile j, V of the one before
+          if (id != -2 && (id < 0 || id >= p.num_blocks)) {
+            set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+            id = -2;
           }
-          if (next) {
-            const uint32_t kb = kd + (c * (2 * S::kTile) >> 4);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
-              pw_mma_ss(tb + 128 * x, qd + off, kb + off, hi, id_s, ks > 0);
-            }
-            mma_commit(&s_full[x]);
-          } else {
-            mma_commit(&empty[c]);  // (with an S the softmax sees to that)
-          }
-          if (in_turn) mbar_arrive(&turn[x ^ 1]);
+          const int id_next = fetch(j + 1);
+          if (j < j1) copy(id, p.k_cache);
+          if (j > j0 && !bad) copy(id_v, p.v_cache);
+          id_v = id;
+          id = id_next;
         }
-        __syncwarp();
-        turns += in_turn;
-        opened |= seen;
-        seen = next;
       }
-      if (!bad && elect_one()) mma_commit(&o_full[x]);
+      // the last copies must land before the CTA can leave
+      if (lane == 0)
+        for (uint32_t c = raw >= NR ? raw - NR : 0; c < raw; ++c)
+          mbar_wait_bounded(&raw_full[c % NR], (c / NR) & 1, kDrainLimitNs);
       __syncwarp();
-      ++nth;
-    }
-    // nothing may be torn down before the last MMA, after a timeout neither
-    if (elect_one()) mma_commit(drained);
-    __syncwarp();
-    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-    mbar_wait_bounded(drained, 0, kDrainLimitNs);
-    __syncwarp();
-    }
-  } else {
-    // ---- softmax: warpgroup x serves query tile x, a row to a thread --------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPqSoftRegs));
-    const int x = warp >> 2, w4 = warp & 3, r = tid & 127;
-    const uint32_t ts = tbase + ((uint32_t)(32 * w4) << 16) + 128 * x;  // S of this warp's lanes
-    const uint32_t to = ts + 256;                                      // and O
-    uint32_t done = 0, nth = 0, link = 0, duals = 0;  // tiles, parts, links and parts of one tile so far
-    constexpr int kLoads = 8 * CB;         // 16-byte loads of a lane for its warp's query rows
-    uint4 qv[kLoads];
-    float sc = 0.f;                        // this row's factor from S to logits in powers of two
-
-    // The part's query rows: 8 lanes to a row, 4 rows at a time (a row of 256 bytes in two).
-    auto load_q = [&]() {
-      const T* q = static_cast<const T*>(p.q);
-      const int active = it.active_of(x);
+    } else {
+      // ---- MMA issue, a warp for each of A and B ------------------------------------------
+      // A step: O += P V of one tile, S of the next. With two tiles of rows at head_dim 128 A and B
+      // take turns, so that one's softmax runs under the other's MMAs. MMAs of one thread complete
+      // in order, so S may take the place of a P that the MMA before it reads, and "S done" says
+      // that O holds every earlier tile.
+      const int x = warp == 16 ? 0 : 1;
+      constexpr uint32_t id_s = mma_idesc_f16(128, 128, 0, 0);
+      constexpr uint32_t id_o = mma_idesc_f16(128, D, 0, 1);
+      // One thread does it all: votes and hand-overs within the warp would lie in every step's way.
+      if (elect_one()) {
+        const uint32_t tb = tbase, sb = smem_u32(sm);
+        // of a descriptor only the start address in its low word moves
+        const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
+        const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
+        const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
+        uint32_t tiles = 0, done = 0, turns = 0;  // tiles of earlier parts; P's and steps in turn so far
+        auto met = [&](uint64_t* bar, uint32_t parity) {
+          const bool ok = pw_wait(bar, parity, p.wait_limit_ns);
+          bad |= !ok;
+          return ok;
+        };
+        for (uint32_t n = 0; met(&part_full[n % kPqRing], (n / kPqRing) & 1); ++n) {
+          const PqPart part = ring[n % kPqRing];
+          mbar_arrive(&part_empty[n % kPqRing]);
+          if (part.stop()) break;
+          const int count = part.j1 - part.j0;
+          const bool in_turn = D == 128 && !part.dual();
+          const uint32_t qd = (uint32_t)smem_desc_sw128(sb + (part.dual() ? 0 : x) * S::kTile, 16, 1024);
+          bool seen = false, opened = false;  // the tile before is seen, O holds something
+          if (!met(&q_full[x], n & 1)) break;
+          for (int i = 0; i <= count && count > 0; ++i) {  // O of tile i - 1, S of tile i
+            const uint32_t mk = tiles + i, mv = mk - 1;
+            const bool next = i < count && part.sees(x, part.j0 + i);
+            if (in_turn && (x == 1 || turns > 0) && !met(&turn[x], (turns + (x ^ 1)) & 1)) break;
+            if (seen) {
+              // (a part's first P comes from warps that have read the O of the part before)
+              if (!met(&v_ready[mv & 1], (mv >> 1) & 1) || !met(&p_full[x], done++ & 1)) break;
+              tc_fence_after();
+              const uint32_t vb = vd + ((mv & 1) * (2 * S::kTile) >> 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = 32 * w4 + 4 * i + (lane >> 3);
-        const bool in = rr < active;
-        const int g = it.row0 + (it.dual ? 0 : x * 128) + rr, t = in ? p.by_group.of(g) : 0, j = in ? g - t * G : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            q + ((size_t)(it.seq.q0 + t) * p.num_heads + it.kvh * G + j) * D) + (lane & 7);
+              for (int part16 = 0; part16 < kParts; ++part16)  // the high parts of P, then the remainders
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) qv[i * CB + cb] = in ? __ldg(src + 8 * cb) : make_uint4(0u, 0u, 0u, 0u);
+                for (int ks = 0; ks < 8; ++ks)
+                  pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 32 * (ks >> 1) + 16 * part16 + 8 * (ks & 1),
+                            vb + (ks * 2048 >> 4), hi, id_o,
+                            (part16 > 0 || ks > 0 || opened) ? 1u : 0u);
+              mma_commit(&v_empty[mv & 1]);
+            }
+            if (i < count && !met(&k_ready[mk & 1], (mk >> 1) & 1)) break;
+            if (next) {
+              tc_fence_after();
+              const uint32_t kb = kd + ((mk & 1) * (2 * S::kTile) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
+                pw_mma_ss(tb + 128 * x, qd + off, kb + off, hi, id_s, ks > 0);
+              }
+              mma_commit(&s_full[x]);  // (the softmax gives K back)
+            } else if (i < count) {
+              mbar_arrive(&k_empty[mk & 1]);
+            }
+            if (in_turn) mbar_arrive(&turn[x ^ 1]);
+            // (a tile that is not seen is given back when it is there, not before: an arrival ahead of
+            // its time would stand for the other query tile's)
+            if (i > 0 && !seen) {
+              if (!met(&v_ready[mv & 1], (mv >> 1) & 1)) break;
+              mbar_arrive(&v_empty[mv & 1]);
+            }
+            turns += in_turn;
+            opened |= seen;
+            seen = next;
+          }
+          if (bad) break;
+          mma_commit(&o_full[x]);
+          tiles += count;
+        }
+        // nothing may be torn down before the last MMA, after a timeout neither
+        mma_commit(drained);
+        if (bad) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+        bad = false;
       }
+      __syncwarp();
+      mbar_wait_bounded(drained, 0, kDrainLimitNs);
+    }
+    if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    __syncwarp();
+  } else {
+    // ---- softmax: two warpgroups to a query tile, half the columns of a row (64 of S, D / 2 of O) to a
+    // thread. The two warps of a row's halves have a named barrier, which both pass whatever happens to
+    // either, and agree there whether a wait ran out.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPqSoftRegs));
+    const int x = warp >> 3, h = (warp >> 2) & 1, w4 = warp & 3, r = tid & 127;
+    const int pair_id = 1 + 4 * x + w4;
+    const uint32_t ts = tbase + ((uint32_t)(32 * w4) << 16) + 128 * x;  // S of this warp's lanes
+    const uint32_t to = ts + 256 + h * (D / 2);                        // and its half of O
+    float* const mine_at = swap + 256 * h + 128 * x + r;
+    const float* const other_at = swap + 256 * (h ^ 1) + 128 * x + r;
+    uint32_t done = 0, tiles = 0;             // P's, tiles of earlier parts
+    uint32_t duals = 0, boxes = 0, cuts = 0;  // parts of one tile, boxes between A and B, parts of cut pairs
+
+    // A part's place in the ring is read from there whenever it is needed (no registers to spare) and
+    // given back at the part's end.
+    auto look = [&](uint32_t n) {
+      if (!bad && !wait(&part_full[n % kPqRing], (n / kPqRing) & 1)) bad = true;
+      return !bad && !ring[n % kPqRing].stop();
     };
-    // The next part's query rows on their way to L2 while this one's last MMAs run (a hint only).
-    auto prefetch_q = [&]() {
-      if (it.dual && x == 1) return;
-      const int rr = 32 * w4 + lane;
-      if (rr >= it.active_of(x)) return;
-      const int g = it.row0 + (it.dual ? 0 : x * 128) + rr, t = p.by_group.of(g);
-      const T* src = static_cast<const T*>(p.q) +
-                     ((size_t)(it.seq.q0 + t) * p.num_heads + it.kvh * G + g - t * G) * D;
+    auto first_row = [&](const PqPart& part) { return part.row0 + (part.dual() ? 0 : x * 128); };
+    // The part's query rows into shared memory as binary16: 16 rows to a warp, 8 lanes to a row, 4 rows at a
+    // time. A bfloat16 row is divided by 2^e so that its largest value lies in [2^14, 2^15): what exceeds
+    // 2^-28 of that keeps its 8 bits.
+    auto place_q = [&](const PqPart& part) {
+      if (part.dual() && x == 1) return;  // A's rows serve both
+      const T* q = static_cast<const T*>(p.q);
+      const int active = part.active_of(x);
+      uint4 all[4][CB];
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * cb));
-    };
-    // Into shared memory as binary16. A bfloat16 row is divided by 2^e so that its largest value lies in
-    // [2^14, 2^15): what exceeds 2^-28 of that keeps its 8 bits.
-    auto store_q = [&]() {
-      float mine = p.scale_log2;
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 32 * w4 + 16 * h + 4 * i + (lane >> 3);
+        const bool in = rr < active;
+        const int g = first_row(part) + rr, t = in ? p.by_group.of(g) : 0, j = in ? g - t * G : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            q + ((size_t)(part.q0 + t) * p.num_heads + part.kvh * G + j) * D) + (lane & 7);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = 32 * w4 + 4 * i + (lane >> 3);
+        for (int cb = 0; cb < CB; ++cb) all[i][cb] = in ? __ldg(src + 8 * cb) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 32 * w4 + 16 * h + 4 * i + (lane >> 3);
+        uint4(&v)[CB] = all[i];
         if constexpr (kBf16) {
           uint32_t top = 0u;  // largest exponent bits of the row
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
-            const uint4 v = qv[i * CB + cb];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {v[cb].x, v[cb].y, v[cb].z, v[cb].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7f80u, (w[k] >> 16) & 0x7f80u));
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
-          // 2^(14 - k) for an exponent of k, at most 2^126
-          const int k = max((int)(top >> 7) - 127, -112);
-          const float by = top == 0u ? 1.f : __uint_as_float((uint32_t)(14 - k + 127) << 23);
-          const float back = top == 0u ? 1.f : __uint_as_float((uint32_t)(k - 14 + 127) << 23);
+          // times 2^(14 - k) for an exponent of k, at most 2^126
+          const int k = top == 0u ? 14 : max((int)(top >> 7) - 127, -112);
+          const float by = __uint_as_float((uint32_t)(14 - k + 127) << 23);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
             float f[8];
-            Chunk<__nv_bfloat16>::widen(qv[i * CB + cb], f);
+            Chunk<__nv_bfloat16>::widen(v[cb], f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] *= by;
-            qv[i * CB + cb] = Chunk<__half>::narrow(f);
+            v[cb] = Chunk<__half>::narrow(f);
           }
-          const float theirs = __shfl_sync(kFullMask, back, (lane & 3) * 8);
-          if (!p.zero_scale && i == lane >> 2) mine = fmaxf(p.scale_log2 * theirs, 1.401298464e-45f);
+          if ((lane & 7) == 0) exps[128 * x + rr] = (unsigned char)(k + 112);
         }
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const uint4 v = qv[i * CB + cb];
+        for (int cb = 0; cb < CB; ++cb)
           *reinterpret_cast<uint4*>(sm + x * S::kTile + cb * S::kColBlock + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(v.x ^ p.flip, v.y ^ p.flip, v.z ^ p.flip, v.w ^ p.flip);
-        }
+              make_uint4(v[cb].x ^ p.flip, v[cb].y ^ p.flip, v[cb].z ^ p.flip, v[cb].w ^ p.flip);
       }
-      sc = mine;
-    };
-    auto place_q = [&]() {
-      if (it.dual && x == 1) return;  // A's rows serve both
-      load_q();
-      store_q();
-      if (it.dual) shared_sc[r] = sc;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&q_full[x]);
-        if (it.dual) mbar_arrive(shared_q);
+        if (part.dual()) mbar_arrive(shared_q);
       }
     };
-    place_q();
-    while (!it.done()) {
-      const bool dual = it.dual, whole = it.whole();
+    // The part's query rows on their way to L2 while earlier MMAs run (a hint only).
+    auto prefetch_q = [&](const PqPart& part) {
+      const int rr = 32 * w4 + lane;
+      if ((part.dual() && x == 1) || rr >= part.active_of(x)) return;
+      const int g = first_row(part) + rr, t = p.by_group.of(g);
+      const T* src = static_cast<const T*>(p.q) +
+                     ((size_t)(part.q0 + t) * p.num_heads + part.kvh * G + g - t * G) * D;
+      if (D == 128 || h == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * h));
+    };
+    bool more = look(0);
+    if (more) place_q(ring[0]);
+    for (uint32_t n = 0;; ++n) {
+      // (also: the other half's warp has put its query rows' exponents in place, and done with `swap`)
+      if (barrier_or(pair_id, 64, bad)) bad = true;
+      if (bad || !more) break;
+      const PqPart& part = ring[n % kPqRing];
+      const bool dual = part.dual();
       if (dual && x == 1) {
-        // (A's warps put the next rows in place behind this part's join only, so that the phase
-        // waited for is never more than one away)
-        if (!bad && !__all_sync(kFullMask, pw_wait(shared_q, duals & 1, p.wait_limit_ns))) bad = true;
-        sc = shared_sc[r];
-        __syncwarp();
+        // (A's warps put the next rows in place when they have B's results of this part only, so
+        // that the phase waited for is never more than one away)
+        if (!wait(shared_q, duals & 1)) bad = true;
         if (lane == 0) mbar_arrive(&q_full[1]);
         ++duals;
       }
-      const int active = it.active_of(x);
+      const int active = part.active_of(x);
       const bool idle = 32 * w4 >= active;  // no row of this warp is a query's
-      const int g = it.row0 + (dual ? 0 : x * 128) + min(r, max(active - 1, 0));
-      const int tok = p.by_group.of(g);
-      const int pos = it.seq.L - it.seq.n + tok;
-      const int j0 = it.j0, j1 = it.j1;
+      float sc = p.scale_log2;              // this row's factor from S to logits in powers of two
+      if (kBf16 && !p.zero_scale)
+        sc = fmaxf(sc * __uint_as_float((uint32_t)(exps[(dual ? 0 : 128 * x) + r] + 1) << 23), 1.401298464e-45f);
       float m_use = -INFINITY, l = 0.f;
       bool first = true;
-      for (int j = j0; j < j1 && !bad; ++j) {
-        if (!it.sees(x, j)) continue;
-        const int vis = pos - j * 128 + 1;  // tokens of the tile up to the row's own
-        if (!__all_sync(kFullMask, pw_wait(&s_full[x], done & 1, p.wait_limit_ns))) {
-          bad = true;
-          break;
-        }
-        tc_fence_after();
-        // S is the query tile's last MMA that reads its link
-        if (w4 == 0 && lane == 0) mbar_arrive(&empty[(link + (j - j0)) & 1]);
-        ++done;
-        if (idle) {  // (its rows of P, and so of O, may hold anything)
-          if (lane == 0) mbar_arrive(&p_full[x]);
-          continue;
-        }
-        uint32_t u[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, u[c]);
-        tmem_wait_ld();
-        float* v = reinterpret_cast<float*>(&u[0][0]);
-        if (__any_sync(kFullMask, vis < 128)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+      {
+        const int g = first_row(part) + min(r, max(active - 1, 0));  // past the last row: any result
+        const int pos = part.base + p.by_group.of(g) - 64 * h;
+        const int j0 = part.j0, step = dual ? 2 : 1;
+        const int j1 = dual ? part.j1 : min(part.j1, ((x ? part.end_b : part.end_a) + 127) / 128);  // that x sees
+#pragma unroll 1
+        for (int j = j0 + (dual ? x : 0); j < j1; j += step) {
+          if (!bad && !wait(&s_full[x], done & 1)) bad = true;
+          tc_fence_after();
+          if ((warp & 7) == 0 && lane == 0) mbar_arrive(&k_empty[(tiles + (j - j0)) & 1]);
+          ++done;
+          if (idle) {  // (its rows of P, and so of O, may hold anything)
+            if (bad) break;
+            if (lane == 0) mbar_arrive(&p_full[x]);
+            continue;
+          }
+          const int vis = pos - j * 128 + 1;  // columns of this half up to the row's own
+          const bool cut = __any_sync(kFullMask, vis < 64);
+          auto hide = [&](int c, uint32_t (&w)[32]) {  // of columns 32 c .. those that the row does not see
             const uint32_t see = low_bits(vis - 32 * c);
-            if (__any_sync(kFullMask, see != 0xffffffffu)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[32 * c + i] = (see >> i) & 1u ? v[32 * c + i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) w[i] = (see >> i) & 1u ? w[i] : 0xff800000u;
+          };
+          uint32_t u[32];  // (the first 32 columns are read again for the weights: no registers for all 64)
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(ts + 64 * h + 32 * c, u);
+            tmem_wait_ld();
+            if (cut) hide(c, u);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              m4[i / 2 & 3] = pw_max3(m4[i / 2 & 3], __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+          }
+          float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // the base moves only when the maximum grows by more than kTopLog2: every P stays below 2^kTopLog2,
+          // and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
+          // a base may be off by half their distance: there it is the maximum and moves whenever that does.)
+          const float most = fabsf(m_use) < kPwFar ? P16::kTopLog2 : 0.f;
+          // (the difference is not a number, and no growth, for -inf - -inf)
+          float alpha = 1.f;
+          if (barrier_or(pair_id, 64, bad || mt - m_use > most)) {
+            *mine_at = bad ? __uint_as_float(0x7fffffffu) : mt;
+            if (barrier_or(pair_id, 64, bad)) {
+              bad = true;
+              break;
+            }
+            mt = fmaxf(mt, *other_at);
+            const bool grow = mt - m_use > most;
+            if (grow) {
+              const float base = mt - (fabsf(mt) < kPwFar ? P16::kTopLog2 - P16::kRescaleLog2 : 0.f);
+              alpha = exp2f(m_use - base);  // 0 while nothing was visible
+              m_use = base;
+            }
+            if (!first && __any_sync(kFullMask, grow)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t w[16];
+                tmem_ld16(to + 16 * c, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+                tmem_st16(to + 16 * c, w);
+              }
             }
           }
-        }
-        float m4[4];
+          first = false;
+          const float nbase = m_use == -INFINITY ? 0.f : -m_use;
+          const uint64_t sc2 = pw_pair(sc, sc), nb2 = pw_pair(nbase, nbase);
+          uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(v[i], v[i + 4]);
+          for (int c = 1; c >= 0; --c) {
+            if (c == 0) {
+              tmem_ld32(ts + 64 * h, u);
+              tmem_wait_ld();
+              if (cut) hide(0, u);
+            }
+            uint32_t w[16], rest[16];
 #pragma unroll
-        for (int i = 8; i < 128; i += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = pw_max3(m4[e], v[i + e], v[i + e + 4]);
-        const float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        // the base moves only when the maximum grows by more than kTopLog2: every P stays below 2^kTopLog2,
-        // and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
-        // a base may be off by half their distance: there it is the maximum and moves whenever that does.)
-        const bool grow = mt - m_use > (fabsf(m_use) < kPwFar ? P16::kTopLog2 : 0.f);  // (no for -inf - -inf)
-        float alpha = 1.f;
-        if (grow) {
-          const float base = mt - (fabsf(mt) < kPwFar ? P16::kTopLog2 - P16::kRescaleLog2 : 0.f);
-          alpha = exp2f(m_use - base);  // 0 while nothing was visible
-          m_use = base;
-        }
-        if (!first && __any_sync(kFullMask, grow)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t w[16];
-            tmem_ld16(to + 16 * c, w);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-            tmem_st16(to + 16 * c, w);
+            for (int i = 0; i < 16; ++i) {
+              float2 e = pw_unpair(
+                  pw_fma2(pw_pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2, nb2));
+              e.x = pw_exp2(e.x);
+              e.y = pw_exp2(e.y);
+              sum[i & 1] = pw_add2(sum[i & 1], pw_pair(e.x, e.y));
+              if constexpr (kParts == 2) {
+                float2 hp;
+                w[i] = P16::high(e, hp);
+                hp = pw_unpair(pw_fma2(pw_pair(hp.x, hp.y), pw_pair(-1.f, -1.f), pw_pair(e.x, e.y)));
+                rest[i] = P16::pack(hp.x, hp.y);
+              } else {
+                w[i] = P16::pack(e.x, e.y);
+              }
+            }
+            // the weights of 32 tokens take the first half of their scores' place, remainders the second
+            tmem_st16(ts + 64 * h + 32 * c, w);
+            if constexpr (kParts == 2) tmem_st16(ts + 64 * h + 32 * c + 16, rest);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
+          const float2 total = pw_unpair(pw_add2(sum[0], sum[1]));
+          l = l * alpha + (total.x + total.y);
         }
-        first = false;
-        const float nbase = m_use == -INFINITY ? 0.f : -m_use;
-        const uint64_t sc2 = pw_pair(sc, sc), nb2 = pw_pair(nbase, nbase);
-        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = pw_unpair(pw_fma2(pw_pair(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nb2));
-            e.x = pw_exp2(e.x);
-            e.y = pw_exp2(e.y);
-            sum[i & 1] = pw_add2(sum[i & 1], pw_pair(e.x, e.y));
-            w[i] = P16::pack(e.x, e.y);
-          }
-          tmem_st16(ts + 16 * c, w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
-        const float2 total = pw_unpair(pw_add2(sum[0], sum[1]));
-        l = l * alpha + (total.x + total.y);
       }
-      // what the output needs of this part, then the next one's place and loads, then the wait
-      link += j0 < j1 ? j1 - j0 + 1 : 0;
-      T* og = static_cast<T*>(p.out) +
-              ((size_t)(it.seq.q0 + tok) * p.num_heads + it.kvh * G + (g - tok * G)) * D;
-      const PqCost part_at = it.at, part_end = it.at + it.cost;
-      const bool head = it.lo <= it.at;
-      it.next(p);
-      const bool more = !it.done();
-      if (more) prefetch_q();
-      if (!bad && !__all_sync(kFullMask, pw_wait(&o_full[x], nth & 1, p.wait_limit_ns))) bad = true;
+      // what the output needs of this part, then the next one's place, then the wait
+      tiles += part.j1 - part.j0;
+      const bool whole = part.whole();
+      const int c0 = part.c0, c1 = part.c1, row0 = first_row(part), pair_rows = part.active;
+      const int my_slot = 2 * blockIdx.x + ((part.kind & PqPart::kHead) ? 1 : 0);
+      T* const rows_out = static_cast<T*>(p.out) + ((size_t)part.q0 * p.num_heads + part.kvh * G) * D;
+      auto row_out = [&](int g) {  // row g of the kv head
+        const int t = p.by_group.of(g);
+        return rows_out + ((size_t)t * p.num_heads + (g - t * G)) * D;
+      };
+      more = look(n + 1);
+      const PqPart& after = ring[(n + 1) % kPqRing];
+      if (more) prefetch_q(after);
+      // the row's sum over both halves
+      barrier_or(pair_id, 64, false);
+      *mine_at = l;
+      barrier_or(pair_id, 64, false);
+      l += *other_at;
+      if (!bad && !wait(&o_full[x], n & 1)) bad = true;
       tc_fence_after();
-      ++nth;
-      if (more && !bad && !dual) place_q();
+      if (more && !bad && !dual) place_q(after);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_empty[n % kPqRing]);
 
-      // 32 dims of this row at a time: O as it is
-      auto load_o = [&](int c, uint32_t (&w)[32]) {
+      // 16 dims (chunk c of this half) of this row's O as it is
+      auto load_o = [&](int c, uint32_t (&w)[16]) {
         if (first || idle) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = 0u;
+          for (int i = 0; i < 16; ++i) w[i] = 0u;
         } else {
-          tmem_ld32(to + 32 * c, w);
+          tmem_ld16(to + 16 * c, w);
           tmem_wait_ld();
         }
       };
-      // Output of 32 dims (chunk c) of the warp's rows: w holds fp32 values of this row, `inv` its factor.
-      uint64_t row_at[4];
-      auto rows_of = [&]() {
-        const uint64_t mine = reinterpret_cast<uint64_t>(og);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) row_at[k] = __shfl_sync(kFullMask, mine, (lane & ~3) + k);
-      };
-      auto put = [&](int c, const uint32_t (&w)[32], float inv) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = make_uint4(Out::pack(__uint_as_float(w[8 * i]) * inv, __uint_as_float(w[8 * i + 1]) * inv),
-                            Out::pack(__uint_as_float(w[8 * i + 2]) * inv, __uint_as_float(w[8 * i + 3]) * inv),
-                            Out::pack(__uint_as_float(w[8 * i + 4]) * inv, __uint_as_float(w[8 * i + 5]) * inv),
-                            Out::pack(__uint_as_float(w[8 * i + 6]) * inv, __uint_as_float(w[8 * i + 7]) * inv));
-        pq_transpose(v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (32 * w4 + (lane & ~3) + k < active) reinterpret_cast<uint4*>(row_at[k])[4 * c + (lane & 3)] = v[k];
-      };
-      // a part of a pair: into the workspace, 16 bytes of 32 rows side by side
-      const int my_slot = 2 * blockIdx.x + (head ? 1 : 0);
-      auto leave = [&](int c, const uint32_t (&w)[32]) {
-        float4* dst = p.part_o + (size_t)my_slot * (D / 4) * 256 + (dual ? 0 : 128 * x) + r;
+      // Output: w holds 16 dims of this thread's row, `inv` their factor
+      T* const to_row = row_out(row0 + min(r, max(active - 1, 0))) + h * (D / 2);
+      auto put = [&](int c, const uint32_t (&w)[16], float inv) {
+        uint32_t v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dst[(size_t)(8 * c + i) * 256] = make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
-                                                       __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
+          v[i] = Out::pack(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv);
+        if (r < active) {
+          reinterpret_cast<uint4*>(to_row)[2 * c] = make_uint4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<uint4*>(to_row)[2 * c + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+      };
+      // a part of a pair: into the workspace, 16 bytes of 32 rows side by side
+      auto leave = [&](int c, const uint32_t (&w)[16]) {
+        float4* dst = p.part_o + ((size_t)my_slot * (D / 4) + h * (D / 8) + 4 * c) * 256 + (dual ? 0 : 128 * x) + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[(size_t)i * 256] = make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
+                                             __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
       };
       auto leave_ml = [&](float m, float sum) {
-        p.part_ml[(size_t)my_slot * 256 + (dual ? 0 : 128 * x) + r] = make_float2(m, sum);
+        if (h == 0) p.part_ml[(size_t)my_slot * 256 + (dual ? 0 : 128 * x) + r] = make_float2(m, sum);
       };
-      rows_of();
       if (dual) {
-        // B's part of the rows goes to A's warps through the place of B's query rows, 32 dims at a
-        // time (16-byte chunk k of row r at k ^ (r & 7)), warp by warp: 4 KB each
-        float4* box = reinterpret_cast<float4*>(sm + S::kTile + w4 * 4096) + lane * 8;
-        const int bar = 2 + w4;
-        if (x == 1) {
-          box[0] = make_float4(m_use, l, 0.f, 0.f);
-          pq_barrier(bar, 64);
-          pq_barrier(bar, 64);
+        // B's part of the rows goes to A's warps through the place of B's query rows, warp by warp (2 KB
+        // each, where that warp's own query rows come next): maxima and sums, then 16 dims at a time (16-byte chunk k of row r at k ^ (r / 2 & 3))
+        float4* box = reinterpret_cast<float4*>(sm + S::kTile + (2 * w4 + h) * 2048) + lane * 4;
+        uint64_t *full = &box_full[4 * h + w4], *empty = &box_empty[4 * h + w4];
+        const int most = idle ? 0 : D / 32;
+        float fa = 0.f, fb = 0.f, M = 0.f, total = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t w[32];
-            load_o(c, w);
+        for (int c = -1; c < most; ++c, ++boxes) {
+          uint32_t w[16];
+          if (c >= 0) load_o(c, w);
+          if (x == 1) {
+            if (boxes > 0 && !bad && !wait(empty, (boxes + 1) & 1)) bad = true;
+            if (c < 0) {
+              box[0] = make_float4(m_use, l, 0.f, 0.f);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(box + (k ^ (lane & 7))) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            pq_barrier(bar, 64);
-            pq_barrier(bar, 64);
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(box + (k ^ (lane >> 1 & 3))) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            continue;
           }
-        } else {
-          pq_barrier(bar, 64);
-          const float4 b = box[0];
-          pq_barrier(bar, 64);
-          const float M = fmaxf(m_use, b.x), nb = M == -INFINITY ? 0.f : M;
-          const float fa = exp2f(m_use - nb), fb = exp2f(b.x - nb);
-          const float sum = l * fa + b.y * fb;
-          const float inv = p.v_scale / sum;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t w[32];
-            load_o(c, w);
-            pq_barrier(bar, 64);
+          if (!bad && !wait(full, boxes & 1)) bad = true;
+          if (c < 0) {
+            const float4 b = box[0];
+            M = fmaxf(m_use, b.x);
+            const float nb = M == -INFINITY ? 0.f : M;
+            fa = exp2f(m_use - nb), fb = exp2f(b.x - nb);
+            total = l * fa + b.y * fb;
+          } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 o = box[k ^ (lane & 7)];
+            for (int k = 0; k < 4; ++k) {
+              const float4 o = box[k ^ (lane >> 1 & 3)];
               w[4 * k] = __float_as_uint(fmaf(o.x, fb, __uint_as_float(w[4 * k]) * fa));
               w[4 * k + 1] = __float_as_uint(fmaf(o.y, fb, __uint_as_float(w[4 * k + 1]) * fa));
               w[4 * k + 2] = __float_as_uint(fmaf(o.z, fb, __uint_as_float(w[4 * k + 2]) * fa));
               w[4 * k + 3] = __float_as_uint(fmaf(o.w, fb, __uint_as_float(w[4 * k + 3]) * fa));
             }
-            pq_barrier(bar, 64);
-            if (bad || idle) continue;
-            if (whole)
-              put(c, w, inv);
-            else
-              leave(c, w);
           }
-          if (!whole && !bad && !idle) leave_ml(M, sum);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty);
+          if (c < 0 || bad) continue;
+          if (whole)
+            put(c, w, p.v_scale / total);
+          else
+            leave(c, w);
         }
+        if (x == 1 && !bad && !wait(empty, (boxes + 1) & 1)) bad = true;  // the place is B's again
+        if (x == 0 && !whole && !bad && !idle) leave_ml(M, total);
       } else if (!idle && !bad) {
         const float inv = p.v_scale / l;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t w[32];
+          uint32_t w[16];
           load_o(c, w);
           if (whole)
             put(c, w, inv);
@@ -910,61 +1012,71 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       if (!whole) {
         // the last of the pair's CTAs joins the parts
         __threadfence();
-        const bool lost = barrier_or(1, 256, bad);  // (every warp comes by here, also after a timeout)
-        const PqShare share = begin->share;
-        const int c0 = share.of(part_at), c1 = share.of(part_end - 1);
-        if (tid == 0) {
-          int last = 0;
-          if (!lost && atomic_add_acq_rel_gpu(p.counter + c0, 1) == c1 - c0) {
-            p.counter[c0] = 0;
-            last = 1;
+        if (bad) *lost = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(left);
+        if (warp == 0) {
+          if (!bad && !wait(left, cuts & 1)) bad = true;
+          if (lane == 0) {
+            int is_last = 0;
+            if (!bad && *lost == 0 && atomic_add_acq_rel_gpu(p.counter + c0, 1) == c1 - c0) {
+              p.counter[c0] = 0;
+              is_last = 1;
+            }
+            *last = is_last;
+            mbar_arrive(counted);
           }
-          *last_flag = last;
+          __syncwarp();
         }
-        pq_barrier(1, 256);
-        const bool last = *last_flag != 0;
-        pq_barrier(1, 256);  // (the flag's next value may come at once)
-        if (last && !idle) {
+        if (!bad && !wait(counted, cuts & 1)) bad = true;
+        ++cuts;
+        if (!bad && *last != 0) {
           __threadfence();
-          const int row = (dual ? 0 : 128 * x) + r;
-          const size_t slot0 = 2 * (size_t)c0 + 1;
-          auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * (size_t)c; };
-          float M = -INFINITY;
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) * 256 + row).x);
-          const float nb = M == -INFINITY ? 0.f : M;
-          float sum = 0.f;
+          auto slot_of = [&](int c) { return c == c0 ? 2 * (size_t)c0 + 1 : 2 * (size_t)c; };
+          // 32 rows to some of the warps, 16 dims at a time to each of these
+          const int pair0 = row0 - (dual ? 0 : 128 * x), blocks = (pair_rows + 31) / 32;
+          const int row = warp % blocks * 32 + lane, each = kPqSoft / blocks;
+          float M = -INFINITY, total = 0.f;
+#pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
             const float2 ml = __ldcg(p.part_ml + slot_of(c) * 256 + row);
-            sum += ml.y * exp2f(ml.x - nb);
+            const float top = fmaxf(M, ml.x), nb = top == -INFINITY ? 0.f : top;
+            total = total * exp2f(M - nb) + ml.y * exp2f(ml.x - nb);
+            M = top;
           }
-          const float inv = p.v_scale / sum;
-          // (of a single tile's rows A's warps take one half of the dims, B's the other)
-          const int from = dual ? x * (D / 64) : 0, upto = dual ? (x + 1) * (D / 64) : D / 32;
+          const float nb = M == -INFINITY ? 0.f : M, inv = p.v_scale / total;
+          T* dst = row_out(pair0 + min(row, pair_rows - 1));
 #pragma unroll 1
-          for (int k = from; k < upto; ++k) {
-            float o[32];
+          for (int k0 = warp / blocks * 4; k0 < D / 4 && warp / blocks < each; k0 += 4 * each) {
+            float o[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
               const float2 ml = __ldcg(p.part_ml + slot_of(c) * 256 + row);
+              const float4* src = p.part_o + (slot_of(c) * (D / 4) + k0) * 256 + row;
+              float4 a[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = __ldcg(src + (size_t)i * 256);
               if (ml.y == 0.f) continue;  // nothing of the part is visible to the row
               const float f = exp2f(ml.x - nb);
-              const float4* src = p.part_o + (slot_of(c) * (D / 4) + 8 * k) * 256 + row;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 a = __ldcg(src + (size_t)i * 256);
-                o[4 * i] = fmaf(a.x, f, o[4 * i]), o[4 * i + 1] = fmaf(a.y, f, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(a.z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(a.w, f, o[4 * i + 3]);
+              for (int i = 0; i < 4; ++i) {
+                o[4 * i] = fmaf(a[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(a[i].y, f, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(a[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(a[i].w, f, o[4 * i + 3]);
               }
             }
-            uint32_t w[32];
+            if (row < pair_rows) {
+              uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
-            put(k, w, inv);
+              for (int i = 0; i < 8; ++i) w[i] = Out::pack(o[2 * i] * inv, o[2 * i + 1] * inv);
+              reinterpret_cast<uint4*>(dst)[k0 / 2] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst)[k0 / 2 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
-      if (more && !bad && dual) place_q();
+      if (more && !bad && dual) place_q(after);
     }
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
     __syncwarp();
@@ -973,7 +1085,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   // ---- tear-down: copies have landed, MMAs have completed (bounded drains above) ------------
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tbase, kPwTmemCols);
   }
