@@ -593,50 +593,45 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       const int x = warp == 16 ? 0 : 1;
       constexpr uint32_t id_s = mma_idesc_f16(128, 128, 0, 0);
       constexpr uint32_t id_o = mma_idesc_f16(128, D, 0, 1);
-      // One thread does it all: votes and hand-overs within the warp would lie in every step's way.
-      if (elect_one()) {
-        const uint32_t tb = tbase, sb = smem_u32(sm);
-        // of a descriptor only the start address in its low word moves
-        const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
-        const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
-        const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
-        uint32_t tiles = 0, done = 0, turns = 0;  // tiles of earlier parts; P's and steps in turn so far
-        auto met = [&](uint64_t* bar, uint32_t parity) {
-          const bool ok = pw_wait(bar, parity, p.wait_limit_ns);
-          bad |= !ok;
-          return ok;
-        };
-        for (uint32_t n = 0; met(&part_full[n % kPqRing], (n / kPqRing) & 1); ++n) {
-          const PqPart part = ring[n % kPqRing];
-          mbar_arrive(&part_empty[n % kPqRing]);
-          if (part.stop()) break;
-          const int count = part.j1 - part.j0;
-          const bool in_turn = D == 128 && !part.dual();
-          const uint32_t qd = (uint32_t)smem_desc_sw128(sb + (part.dual() ? 0 : x) * S::kTile, 16, 1024);
-          bool seen = false, opened = false;  // the tile before is seen, O holds something
-          if (!met(&q_full[x], n & 1)) break;
-          for (int i = 0; i <= count && count > 0; ++i) {  // O of tile i - 1, S of tile i
-            const uint32_t mk = tiles + i, mv = mk - 1;
-            const bool next = i < count && part.sees(x, part.j0 + i);
-            if (in_turn && (x == 1 || turns > 0) && !met(&turn[x], (turns + (x ^ 1)) & 1)) break;
+      // The whole warp waits, one elected lane issues; operands handed round from one lane are known to the
+      // compiler to be the same in all, and stay where the MMAs take them from.
+      const uint32_t tb = __shfl_sync(kFullMask, tbase, 0);
+      const uint32_t sb = __shfl_sync(kFullMask, smem_u32(sm), 0);
+      // of a descriptor only the start address in its low word moves
+      const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
+      const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
+      const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
+      uint32_t tiles = 0, done = 0, turns = 0;  // tiles of earlier parts; P's and steps in turn so far
+      PqPart part;
+      for (uint32_t n = 0; take(n, part); ++n) {
+        const int count = part.j1 - part.j0;
+        const bool in_turn = D == 128 && !part.dual();
+        const uint32_t qd =
+            __shfl_sync(kFullMask, (uint32_t)smem_desc_sw128(sb + (part.dual() ? 0 : x) * S::kTile, 16, 1024), 0);
+        bool seen = false, opened = false;  // the tile before is seen, O holds something
+        bad = !wait(&q_full[x], n & 1);
+        for (int i = 0; i <= count && count > 0 && !bad; ++i) {  // O of tile i - 1, S of tile i
+          const uint32_t mk = tiles + i, mv = mk - 1;
+          const bool next = i < count && part.sees(x, part.j0 + i);
+          const uint32_t kb = __shfl_sync(kFullMask, kd + ((mk & 1) * (2 * S::kTile) >> 4), 0);
+          const uint32_t vb = __shfl_sync(kFullMask, vd + ((mv & 1) * (2 * S::kTile) >> 4), 0);
+          // (the turn comes last, so that nothing but the issue lies between it and the other's)
+          if (i < count) bad = !wait(&k_ready[mk & 1], (mk >> 1) & 1);
+          // (a part's first P comes from warps that have read the O of the part before)
+          if (!bad && seen) bad = !wait(&v_ready[mv & 1], (mv >> 1) & 1) || !wait(&p_full[x], done++ & 1);
+          if (!bad && in_turn && (x == 1 || turns > 0)) bad = !wait(&turn[x], (turns + (x ^ 1)) & 1);
+          tc_fence_after();
+          if (!bad && elect_one()) {
             if (seen) {
-              // (a part's first P comes from warps that have read the O of the part before)
-              if (!met(&v_ready[mv & 1], (mv >> 1) & 1) || !met(&p_full[x], done++ & 1)) break;
-              tc_fence_after();
-              const uint32_t vb = vd + ((mv & 1) * (2 * S::kTile) >> 4);
 #pragma unroll
               for (int part16 = 0; part16 < kParts; ++part16)  // the high parts of P, then the remainders
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                   pw_mma_ts(tb + 256 + 128 * x, tb + 128 * x + 32 * (ks >> 1) + 16 * part16 + 8 * (ks & 1),
-                            vb + (ks * 2048 >> 4), hi, id_o,
-                            (part16 > 0 || ks > 0 || opened) ? 1u : 0u);
+                            vb + (ks * 2048 >> 4), hi, id_o, (part16 > 0 || ks > 0 || opened) ? 1u : 0u);
               mma_commit(&v_empty[mv & 1]);
             }
-            if (i < count && !met(&k_ready[mk & 1], (mk >> 1) & 1)) break;
             if (next) {
-              tc_fence_after();
-              const uint32_t kb = kd + ((mk & 1) * (2 * S::kTile) >> 4);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
@@ -647,25 +642,24 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
               mbar_arrive(&k_empty[mk & 1]);
             }
             if (in_turn) mbar_arrive(&turn[x ^ 1]);
-            // (a tile that is not seen is given back when it is there, not before: an arrival ahead of
-            // its time would stand for the other query tile's)
-            if (i > 0 && !seen) {
-              if (!met(&v_ready[mv & 1], (mv >> 1) & 1)) break;
-              mbar_arrive(&v_empty[mv & 1]);
-            }
-            turns += in_turn;
-            opened |= seen;
-            seen = next;
           }
-          if (bad) break;
-          mma_commit(&o_full[x]);
-          tiles += count;
+          __syncwarp();
+          // (a tile that is not seen is given back when it is there, not before: an arrival ahead of its
+          // time would stand for the other query tile's)
+          if (!bad && i > 0 && !seen) {
+            bad = !wait(&v_ready[mv & 1], (mv >> 1) & 1);
+            if (!bad && lane == 0) mbar_arrive(&v_empty[mv & 1]);
+          }
+          turns += in_turn;
+          opened |= seen;
+          seen = next;
         }
-        // nothing may be torn down before the last MMA, after a timeout neither
-        mma_commit(drained);
-        if (bad) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-        bad = false;
+        if (!bad && elect_one()) mma_commit(&o_full[x]);
+        __syncwarp();
+        tiles += count;
       }
+      // nothing may be torn down before the last MMA, after a timeout neither
+      if (elect_one()) mma_commit(drained);
       __syncwarp();
       mbar_wait_bounded(drained, 0, kDrainLimitNs);
     }
