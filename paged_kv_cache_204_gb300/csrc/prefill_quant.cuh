@@ -40,6 +40,38 @@ constexpr int kPqStart = 256;     // a pair's start and end, as tokens of its wa
 constexpr int kPqMinTokens = 512; // a CTA's stretch is no shorter
 constexpr int kPqRing = 4;        // parts that the walking warp may be ahead
 
+// pw_wait for a kernel of many warps that wait much of their time: sixty-four attempts between two looks at the
+// clock. (Polls take issue slots from the warps that work; a look at the clock is four times a poll.)
+__device__ __forceinline__ bool pq_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_test_wait(bar, parity)) return true;
+  if (limit_ns == 0) return false;
+  const uint32_t at = smem_u32(bar);
+  auto attempts = [&]() {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 64;\n\t"
+        "AGAIN_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra OUT_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra AGAIN_%=;\n\t"
+        "OUT_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    return done != 0;
+  };
+  if (attempts()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (attempts()) return true;
+  } while (globaltimer_ns() - t0 < limit_ns);
+  return false;
+}
+
 // Cost of what a CTA does, in tokens x group.
 using PqCost = long long;
 
@@ -306,6 +338,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   using S = PqShape<F, D>;
   using Out = PwPack<T>;
   using P16 = PwPack<__half>;
+  constexpr float kTopLog2 = 15.f, kRescaleLog2 = 8.f;
   constexpr int CB = S::kCB, NR = S::kRawStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   // 16-bit parts of P. One part, 2^-12 of a weight and rms half of that, is far below a bfloat16
@@ -452,7 +485,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   const uint32_t tbase = *slot;
   bool bad = false;  // a wait ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // the same answer in the whole warp
-    return __all_sync(kFullMask, pw_wait(bar, parity, p.wait_limit_ns));
+    return __all_sync(kFullMask, pq_wait(bar, parity, p.wait_limit_ns));
   };
   // The n-th part of the walk; false where there is none.
   auto take = [&](uint32_t n, PqPart& part) {
@@ -812,7 +845,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           // the base moves only when the maximum grows by more than kTopLog2: every P stays below 2^kTopLog2,
           // and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
           // a base may be off by half their distance: there it is the maximum and moves whenever that does.)
-          const float most = fabsf(m_use) < kPwFar ? P16::kTopLog2 : 0.f;
+          const float most = fabsf(m_use) < kPwFar ? kTopLog2 : 0.f;
           // (the difference is not a number, and no growth, for -inf - -inf)
           float alpha = 1.f;
           if (barrier_or(pair_id, 64, bad || mt - m_use > most)) {
@@ -824,7 +857,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
             mt = fmaxf(mt, *other_at);
             const bool grow = mt - m_use > most;
             if (grow) {
-              const float base = mt - (fabsf(mt) < kPwFar ? P16::kTopLog2 - P16::kRescaleLog2 : 0.f);
+              const float base = mt - (fabsf(mt) < kPwFar ? kTopLog2 - kRescaleLog2 : 0.f);
               alpha = exp2f(m_use - base);  // 0 while nothing was visible
               m_use = base;
             }
