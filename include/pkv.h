@@ -692,12 +692,11 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
  *   k_scale, v_scale  finite and > 0 (with scale * k_scale finite)
  *   max_query_len     a sequence with more new tokens sets
  *                     PKV_DEV_ERR_CONTEXT_LEN and is skipped
- *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whose
- *                     first PKV_PREFILL_COUNTER_BYTES must be zero before the first
- *                     call; every call that ends with *dev_err == 0 leaves them zero. One
- *                     workspace serves calls of any sizes, of both operators.
- *                     Two calls that share a workspace must not overlap on the GPU.
- * Outputs are rounded once to dtype from 32-bit sums; on the way, probabilities
+ *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whatever
+ *                     they hold. One workspace serves calls of any sizes, of both
+ *                     operators. Two calls that share a workspace must not
+ *                     overlap on the GPU.
+ * Two kernels. Outputs are rounded once to dtype from 32-bit sums; on the way, probabilities
  * are rounded to binary16 (relative 2^-11), and bfloat16 queries enter as
  * binary16 numbers times a power of two of their row (exact but for values of
  * less than 2^-28 of the row's largest). V rows that some query of the call sees
@@ -721,9 +720,6 @@ pkv_status pkv_paged_attention_prefill_q4_0(void* out, const void* q, const void
                                             int head_dim, int block_size, int num_seqs, int max_blocks_per_seq,
                                             int num_blocks, int max_query_len, pkv_dtype dtype, void* workspace,
                                             size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream);
-
-/* The counters at the start of a workspace of prefill over quantised caches. */
-#define PKV_PREFILL_COUNTER_BYTES 4096
 
 /* Bytes of workspace the two calls need, whatever the sizes. Pure host function; 0
  * for a head_dim that they do not take. */

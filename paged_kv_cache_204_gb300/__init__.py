@@ -147,7 +147,6 @@ lib.pkv_paged_attention_prefill_fp8.restype = _I
 lib.pkv_paged_attention_prefill_q4_0.argtypes = [_P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                                  _P, _SZ, _P, _P]
 lib.pkv_paged_attention_prefill_q4_0.restype = _I
-PREFILL_COUNTER_BYTES = 4096  # PKV_PREFILL_COUNTER_BYTES
 WINDOW_COUNTER_BYTES = 524288  # PKV_WINDOW_COUNTER_BYTES
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PKV_NOALLOC_SCRATCH_BYTES
 
@@ -518,11 +517,9 @@ def prefill_workspace_bytes(head_dim: int) -> int:
 
 
 def new_prefill_workspace(head_dim: int, device="cuda") -> torch.Tensor:
-    """A workspace of paged_attention_prefill_fp8 and paged_attention_prefill_q4_0: its counters zeroed,
-    the room for partial results as it comes. It serves calls of any sizes of that head_dim or a smaller one."""
-    ws = torch.empty(prefill_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
-    ws[:PREFILL_COUNTER_BYTES].zero_()
-    return ws
+    """A workspace of paged_attention_prefill_fp8 and paged_attention_prefill_q4_0, as it comes. It serves
+    calls of any sizes of that head_dim or a smaller one."""
+    return torch.empty(prefill_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
 
 
 def paged_attention_prefill_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -7,7 +7,7 @@ namespace pkv {
 
 namespace {
 
-size_t counters_end() { return PKV_PREFILL_COUNTER_BYTES; }
+size_t cut_bytes() { return sizeof(PqCut) * 2 * kPqMaxCtas; }
 size_t ml_bytes() { return sizeof(float2) * 2 * kPqMaxCtas * 256; }
 
 template <typename T, PqFormat F, int D>
@@ -62,13 +62,27 @@ cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
   p.max_query_len = a.max_query_len;
   p.by_group.set((uint32_t)a.group);
   char* ws = static_cast<char*>(a.workspace);
-  p.counter = reinterpret_cast<int32_t*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + counters_end());
-  p.part_o = reinterpret_cast<float4*>(ws + counters_end() + ml_bytes());
+  p.cuts = reinterpret_cast<PqCut*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + cut_bytes());
+  p.part_o = reinterpret_cast<float4*>(ws + cut_bytes() + ml_bytes());
   p.dev_err = a.dev_err;
   p.wait_limit_ns = a.wait_limit_ns;
-  kernel<<<sms < kPqMaxCtas ? sms : kPqMaxCtas, kPqThreads, S::kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  const unsigned ctas = sms < kPqMaxCtas ? sms : kPqMaxCtas;
+  kernel<<<ctas, kPqThreads, S::kSmemBytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join, launched under the first kernel's end (8 blocks of 32 rows to a pair)
+  cudaLaunchConfig_t cfg{};
+  const int64_t rows = queries * a.group < 256 ? queries * a.group : 256;
+  cfg.gridDim = dim3(ctas, (unsigned)((rows + 31) / 32));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pa_prefill_quant_join_kernel<T, D>, p);
 }
 
 template <PqFormat F>
@@ -82,7 +96,7 @@ PrefillQuantLauncher of(bool bf16, int head_dim) {
 
 size_t prefill_quant_workspace_bytes(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
-  return counters_end() + ml_bytes() + sizeof(float) * 2 * kPqMaxCtas * 256 * (size_t)head_dim;
+  return cut_bytes() + ml_bytes() + sizeof(float) * 2 * kPqMaxCtas * 256 * (size_t)head_dim;
 }
 
 PrefillQuantLauncher prefill_quant_launcher(bool q4, bool bf16, int head_dim) {

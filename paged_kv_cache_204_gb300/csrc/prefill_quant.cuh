@@ -17,8 +17,8 @@
 //
 // Split: the pairs of all sequences and kv heads are laid end to end, each as long as its walk and
 // a start, and every CTA takes an equal stretch (the grid has one to an SM, fewer where the whole
-// is short). A pair that a border cuts leaves partial results in the workspace, and the last of its
-// CTAs to get there joins them (log-sum-exp).
+// is short). A pair that a border cuts leaves partial results in the workspace, which a second kernel
+// joins (log-sum-exp), 32 rows to a CTA.
 #pragma once
 
 #include <type_traits>
@@ -72,8 +72,15 @@ __device__ __forceinline__ bool pq_wait(uint64_t* bar, uint32_t parity, uint64_t
   return false;
 }
 
-// Cost of what a CTA does, in tokens x group.
-using PqCost = long long;
+// What a stretch is measured in: tokens x group, halved until the whole fits in 30 bits.
+using PqCost = int;
+
+// A pair that lies in more than one CTA, as the one that it starts in tells the joining kernel.
+struct PqCut {
+  int last;  // CTA of its last part; below 0: no such pair
+  int q0, kvh, row0, active;
+  int pad[3];
+};
 
 struct PqParams {
   void* out;
@@ -88,7 +95,7 @@ struct PqParams {
   int zero_scale;    // scale 0: rows have equal weights, their exponents left alone
   int num_seqs, num_heads, num_kv_heads, group, block_size, block_bits, max_blocks_per_seq, num_blocks, max_query_len;
   PwDivisor by_group;
-  int32_t* counter;  // [kPqMaxCtas], of the pairs that start in a CTA and do not end there
+  PqCut* cuts;       // [kPqMaxCtas]
   float2* part_ml;   // [2 kPqMaxCtas][256]
   float4* part_o;    // [2 kPqMaxCtas][D / 4][256]
   int32_t* dev_err;
@@ -108,7 +115,7 @@ struct PqShape {
   static constexpr int kStageOff = 2 * kTile;                        // K, V, K, V
   static constexpr int kRawOff = kStageOff + 4 * kTile;
   static constexpr int kBarOff = kRawOff + kRawStages * kRaw;
-  static constexpr int kBars = 2 * kRawStages + 18 + 2 * kPqRing + 16 + 4;
+  static constexpr int kBars = 2 * kRawStages + 18 + 2 * kPqRing + 16 + 2;
   static constexpr int kRingOff = (kBarOff + 8 * kBars + 15) / 16 * 16;
   static constexpr int kSwapOff = kRingOff + 64 * kPqRing;
   static constexpr int kExpOff = kSwapOff + 2 * 2 * 128 * 4;
@@ -132,20 +139,24 @@ struct PqSeq {
     live = valid && n > 0;
   }
   __device__ __forceinline__ int pairs(int group) const { return (int)(((int64_t)n * group + 255) / 256); }
-  // cost of the first k of its pairs (per kv head)
-  __device__ __forceinline__ PqCost before(int k, int group) const {
-    const PqCost each = (PqCost)group * (kPqStart + L - n), rows = (PqCost)n * group;
-    return k * each + (256 * (PqCost)k < rows ? 128 * (PqCost)k * (k + 1) : 128 * (PqCost)k * (k - 1) + rows);
+  // tokens x group of the first k of its pairs (per kv head) ...
+  __device__ __forceinline__ long long tokens(int k, int group) const {
+    const long long each = (long long)group * (kPqStart + L - n), rows = (long long)n * group;
+    return k * each + (256LL * k < rows ? 128LL * k * (k + 1) : 128LL * k * (k - 1) + rows);
+  }
+  // ... and their cost: no pair without any
+  __device__ __forceinline__ PqCost before(int k, int group, int shift) const {
+    return (PqCost)(tokens(k, group) >> shift) + k;
   }
 };
 
 // The whole batch's cost and how CTAs share it.
 struct PqShare {
   PqCost whole;
-  int ctas;
+  int ctas, shift;
   __device__ __forceinline__ PqCost begin(int c) const { return whole / ctas * c + whole % ctas * c / ctas; }
   __device__ __forceinline__ int of(PqCost y) const {
-    int c = min(ctas - 1, (int)(y / (whole / ctas + 1)));
+    int c = min(ctas - 1, y / (whole / ctas + 1));
     while (begin(c + 1) <= y) ++c;
     return c;
   }
@@ -185,7 +196,7 @@ struct PqWalk {
   __device__ __forceinline__ bool done() const { return at >= hi; }
   __device__ __forceinline__ PqPart part(const PqParams& p) {
     PqPart t;
-    cost = seq.before(pair + 1, p.group) - seq.before(pair, p.group);
+    cost = seq.before(pair + 1, p.group, share.shift) - seq.before(pair, p.group, share.shift);
     t.s = s, t.kvh = kvh, t.q0 = seq.q0, t.base = seq.L - seq.n;
     t.row0 = pair * 256;
     t.active = min(seq.n * p.group - t.row0, 256);
@@ -194,9 +205,11 @@ struct PqWalk {
     t.end_b = dual ? 0 : t.base + 1 + p.by_group.of(t.row0 + t.active - 1);
     t.kind = (dual ? PqPart::kDual : 0) | (head ? PqPart::kHead : 0);
     const int tiles = (t.end() + 127) / 128;
-    const PqCost a = max(lo - at, (PqCost)0), b = min(hi - at, cost);
-    t.j0 = a == 0 ? 0 : (int)(tiles * a / cost);
-    t.j1 = b == cost ? tiles : (int)(tiles * b / cost);
+    // (the same place gives the same tile to the CTA before it and to the one behind)
+    const float scale = (float)tiles / (float)cost;
+    auto tile_at = [&](PqCost y) { return y <= 0 ? 0 : (y >= cost ? tiles : min((int)((float)y * scale), tiles)); };
+    t.j0 = tile_at(lo - at);
+    t.j1 = tile_at(hi - at);
     t.c0 = head ? (int)blockIdx.x : share.of(at);
     t.c1 = at + cost <= hi ? (int)blockIdx.x : share.of(at + cost - 1);
     return t;
@@ -235,14 +248,27 @@ struct PqBegin {
   int s, kvh, pair;
 };
 
-__device__ __forceinline__ PqCost pq_warp_scan(PqCost v) {  // inclusive
+template <typename I>
+__device__ __forceinline__ I pq_warp_scan(I v) {  // inclusive
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const PqCost u = __shfl_up_sync(kFullMask, v, o);
+    const I u = __shfl_up_sync(kFullMask, v, o);
     if (lane >= o) v += u;
   }
   return v;
+}
+// Sum over the CTA of every warp's `own` (that of its last lane): the sum, and of the warps before this one.
+template <typename I>
+__device__ __forceinline__ I pq_block_sum(I own, I* sums, I& before) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();  // (the last use of sums is over)
+  if (lane == 31) sums[warp] = own;
+  __syncthreads();
+  const I upto = pq_warp_scan(lane < kPqThreads / 32 ? sums[lane] : (I)0);
+  before = __shfl_sync(kFullMask, upto, max(warp - 1, 0));
+  if (warp == 0) before = 0;
+  return __shfl_sync(kFullMask, upto, 31);
 }
 
 // 8 bytes of codes as 16 values d (q - 8): low halves to lo, high halves to hi. A code placed
@@ -366,17 +392,13 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   uint64_t* part_empty = part_full + kPqRing;  // [kPqRing] and was read (by every warp but the walking one)
   uint64_t* box_full = part_empty + kPqRing;   // [8] B's partial results for A's warp are there
   uint64_t* box_empty = box_full + 8;    // [8] and were read
-  uint64_t* left = box_empty + 8;        // a cut pair's part is in the workspace (one arrival per softmax warp)
-  uint64_t* counted = left + 1;          // and counted
-  uint64_t* shared_q = left + 2;         // A's query rows in place for B too (an arrival per warp of A)
-  uint64_t* drained = left + 3;          // every MMA of the CTA done (two arrivals)
+  uint64_t* shared_q = box_empty + 8;    // A's query rows in place for B too (an arrival per warp of A)
+  uint64_t* drained = shared_q + 1;      // every MMA of the CTA done (two arrivals)
   PqPart* ring = reinterpret_cast<PqPart*>(sm + S::kRingOff);     // [kPqRing]
   float* swap = reinterpret_cast<float*>(sm + S::kSwapOff);       // [half][A, B][128] from one half's warp to the other's
   unsigned char* exps = sm + S::kExpOff;                          // [A, B][128] exponents taken out of the query rows
   unsigned char* misc = sm + S::kMiscOff;
   uint32_t* slot = reinterpret_cast<uint32_t*>(misc);             // tensor-memory address
-  volatile int* last = reinterpret_cast<int*>(misc + 4);          // the counted part was the last of its pair
-  volatile int* lost = reinterpret_cast<int*>(misc + 8);          // a softmax warp ran out of a wait
   uint32_t* held_blocks = reinterpret_cast<uint32_t*>(misc + 16); // [NR] blocks of a raw tile that were copied
   PqBegin* begin = reinterpret_cast<PqBegin*>(swap);              // (read before the first part is there)
   static_assert(sizeof(PqBegin) <= 128 && 16 + 4 * NR <= 64, "room");
@@ -385,64 +407,76 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   const int G = p.group;
 
   // ---- the CTA's stretch of the whole -----------------------------------------
+  grid_launch_dependents();  // (the joining kernel waits for all of this one's memory all the same)
+  if (tid == 0) p.cuts[blockIdx.x].last = -1;
   {
-    constexpr int kWarps = kPqThreads / 32;
-    PqCost* sums = reinterpret_cast<PqCost*>(sm);  // [kWarps], before anything else is there
-    auto cost_of = [&](int s) {
-      if (s >= p.num_seqs) return (PqCost)0;
-      PqSeq q;
-      q.load(p, s);
-      if (!q.valid && blockIdx.x == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
-      return q.live ? q.before(q.pairs(G), G) * p.num_kv_heads : (PqCost)0;
+    long long* sums64 = reinterpret_cast<long long*>(sm);  // [warps], before anything else is there
+    PqCost* sums = reinterpret_cast<PqCost*>(sm + 512);
+    auto load = [&](int s, PqSeq& q) {
+      q.live = false;
+      if (s < p.num_seqs) q.load(p, s);
+      return q.live;
     };
-    PqCost mine = 0;
-    for (int s = tid; s < p.num_seqs; s += kPqThreads) mine += cost_of(s);
-    const PqCost w = pq_warp_scan(mine);
-    if (lane == 31) sums[warp] = w;
-    __syncthreads();
+    PqSeq first;
+    long long tokens = 0;
+    for (int s = tid; s < p.num_seqs; s += kPqThreads) {
+      PqSeq q;
+      if (load(s, q)) tokens += q.tokens(q.pairs(G), G) * p.num_kv_heads;
+      if (!q.valid && blockIdx.x == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
+      if (s == tid) first = q;
+    }
+    if (tid >= p.num_seqs) first.live = false;
+    long long unused;
+    tokens = pq_block_sum(pq_warp_scan(tokens), sums64, unused);
+    const float most = (float)tokens / (float)(G * kPqMinTokens);
     PqShare share;
-    share.whole = 0;
-    for (int i = 0; i < kWarps; ++i) share.whole += sums[i];
-    const PqCost most = share.whole / ((PqCost)G * kPqMinTokens);
-    share.ctas = (int)max(min(most, (PqCost)gridDim.x), (PqCost)1);
-    if (share.whole == 0 || (int)blockIdx.x >= share.ctas) return;
+    share.ctas = min(max((int)fminf(most, 1e6f), 1), (int)gridDim.x);
+    if (tokens == 0 || (int)blockIdx.x >= share.ctas) return;
+    share.shift = max(34 - __clzll(tokens), 0);  // tokens >> shift < 2^30
+    auto cost_of = [&](bool live, const PqSeq& q) {
+      return live ? q.before(q.pairs(G), G, share.shift) * p.num_kv_heads : 0;
+    };
+    PqCost mine = 0, dummy;
+    if (p.num_seqs <= kPqThreads) {
+      mine = cost_of(first.live, first);
+    } else {
+      for (int s = tid; s < p.num_seqs; s += kPqThreads) {
+        PqSeq q;
+        const bool live = load(s, q);
+        mine += cost_of(live, q);
+      }
+    }
+    share.whole = pq_block_sum(pq_warp_scan(mine), sums, dummy);
     const PqCost lo = share.begin(blockIdx.x);
     PqCost base = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += kPqThreads) {
-      __syncthreads();
-      const PqCost own = p.num_seqs <= kPqThreads ? mine : cost_of(s0 + tid);
-      const PqCost upto = pq_warp_scan(own);
-      if (lane == 31) sums[warp] = upto;
-      __syncthreads();
-      PqCost before = base;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += sums[i];
-        base += sums[i];
-      }
-      before += upto - own;
+    for (int s0 = 0; s0 < p.num_seqs && base <= lo; s0 += kPqThreads) {
+      PqSeq q = first;
+      const bool live = p.num_seqs <= kPqThreads ? first.live : load(s0 + tid, q);
+      const PqCost own = cost_of(live, q), upto = pq_warp_scan(own);
+      PqCost before;
+      const PqCost all = pq_block_sum(upto, sums, before);
+      before += base + upto - own;
       if (own > 0 && before <= lo && lo < before + own) {
-        PqSeq q;
-        q.load(p, s0 + tid);
         const int np = q.pairs(G);
-        const PqCost head = q.before(np, G);
+        const PqCost head = q.before(np, G, share.shift);
         begin->s = s0 + tid;
-        begin->kvh = (int)((lo - before) / head);
+        begin->kvh = (lo - before) / head;
         const PqCost y = (lo - before) % head;
         int a = 0, b = np;  // the pair that holds y: before(a) <= y < before(b)
         while (b - a > 1) {
           const int mid = (a + b) / 2;
-          if (q.before(mid, G) <= y)
+          if (q.before(mid, G, share.shift) <= y)
             a = mid;
           else
             b = mid;
         }
         begin->pair = a;
-        begin->at = lo - y + q.before(a, G);
+        begin->at = lo - y + q.before(a, G, share.shift);
         begin->lo = lo;
         begin->hi = share.begin(blockIdx.x + 1);
         begin->share = share;
       }
-      if (base > lo) break;  // (uniform)
+      base += all;
     }
   }
 
@@ -471,12 +505,9 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       mbar_init(&box_full[i], 1);
       mbar_init(&box_empty[i], 1);
     }
-    mbar_init(left, kPqSoft);
-    mbar_init(counted, 1);
     mbar_init(shared_q, 8);
     mbar_init(drained, 2);
     mbar_init_fence();
-    *lost = 0;
   }
   if (warp == 16) tmem_alloc(slot, kPwTmemCols);
   tc_fence_before();
@@ -557,6 +588,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
         PqPart part;
         if (!stop) part = walk.part(p);
         if (lane == 0) {
+          if (!stop && (part.kind & PqPart::kHead) && !part.whole()) {
+            PqCut& told = p.cuts[blockIdx.x];
+            told.last = part.c1;
+            told.q0 = part.q0, told.kvh = part.kvh, told.row0 = part.row0, told.active = part.active;
+          }
           if (stop)
             ring[n % kPqRing].kind = PqPart::kStop;
           else
@@ -710,7 +746,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     float* const mine_at = swap + 256 * h + 128 * x + r;
     const float* const other_at = swap + 256 * (h ^ 1) + 128 * x + r;
     uint32_t done = 0, tiles = 0;             // P's, tiles of earlier parts
-    uint32_t duals = 0, boxes = 0, cuts = 0;  // parts of one tile, boxes between A and B, parts of cut pairs
+    uint32_t duals = 0, boxes = 0;            // parts of one tile, boxes between A and B
 
     // A part's place in the ring is read from there whenever it is needed (no registers to spare) and
     // given back at the part's end.
@@ -916,7 +952,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       // what the output needs of this part, then the next one's place, then the wait
       tiles += part.j1 - part.j0;
       const bool whole = part.whole();
-      const int c0 = part.c0, c1 = part.c1, row0 = first_row(part), pair_rows = part.active;
+      const int row0 = first_row(part);
       const int my_slot = 2 * blockIdx.x + ((part.kind & PqPart::kHead) ? 1 : 0);
       T* const rows_out = static_cast<T*>(p.out) + ((size_t)part.q0 * p.num_heads + part.kvh * G) * D;
       auto row_out = [&](int g) {  // row g of the kv head
@@ -1036,73 +1072,6 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
         if (!whole) leave_ml(m_use, l);
       }
       tc_fence_before();
-      if (!whole) {
-        // the last of the pair's CTAs joins the parts
-        __threadfence();
-        if (bad) *lost = 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(left);
-        if (warp == 0) {
-          if (!bad && !wait(left, cuts & 1)) bad = true;
-          if (lane == 0) {
-            int is_last = 0;
-            if (!bad && *lost == 0 && atomic_add_acq_rel_gpu(p.counter + c0, 1) == c1 - c0) {
-              p.counter[c0] = 0;
-              is_last = 1;
-            }
-            *last = is_last;
-            mbar_arrive(counted);
-          }
-          __syncwarp();
-        }
-        if (!bad && !wait(counted, cuts & 1)) bad = true;
-        ++cuts;
-        if (!bad && *last != 0) {
-          __threadfence();
-          auto slot_of = [&](int c) { return c == c0 ? 2 * (size_t)c0 + 1 : 2 * (size_t)c; };
-          // 32 rows to some of the warps, 16 dims at a time to each of these
-          const int pair0 = row0 - (dual ? 0 : 128 * x), blocks = (pair_rows + 31) / 32;
-          const int row = warp % blocks * 32 + lane, each = kPqSoft / blocks;
-          float M = -INFINITY, total = 0.f;
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(p.part_ml + slot_of(c) * 256 + row);
-            const float top = fmaxf(M, ml.x), nb = top == -INFINITY ? 0.f : top;
-            total = total * exp2f(M - nb) + ml.y * exp2f(ml.x - nb);
-            M = top;
-          }
-          const float nb = M == -INFINITY ? 0.f : M, inv = p.v_scale / total;
-          T* dst = row_out(pair0 + min(row, pair_rows - 1));
-#pragma unroll 1
-          for (int k0 = warp / blocks * 4; k0 < D / 4 && warp / blocks < each; k0 += 4 * each) {
-            float o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 2
-            for (int c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(p.part_ml + slot_of(c) * 256 + row);
-              const float4* src = p.part_o + (slot_of(c) * (D / 4) + k0) * 256 + row;
-              float4 a[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) a[i] = __ldcg(src + (size_t)i * 256);
-              if (ml.y == 0.f) continue;  // nothing of the part is visible to the row
-              const float f = exp2f(ml.x - nb);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                o[4 * i] = fmaf(a[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(a[i].y, f, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(a[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(a[i].w, f, o[4 * i + 3]);
-              }
-            }
-            if (row < pair_rows) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = Out::pack(o[2 * i] * inv, o[2 * i + 1] * inv);
-              reinterpret_cast<uint4*>(dst)[k0 / 2] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(dst)[k0 / 2 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-          }
-        }
-      }
       if (more && !bad && dual) place_q(after);
     }
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
@@ -1116,6 +1085,53 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     tc_fence_after();
     tmem_dealloc(tbase, kPwTmemCols);
   }
+}
+
+// The cut pairs' parts joined: grid = (CTA that a pair starts in, 32 rows of it), a warp to a quarter of the
+// head dims, a row to a lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) pa_prefill_quant_join_kernel(const __grid_constant__ PqParams p) {
+  grid_dependency_wait();
+  const int c0 = blockIdx.x, c1 = __ldcg(&p.cuts[c0].last);
+  if (c1 < 0) return;
+  const int active = __ldcg(&p.cuts[c0].active);
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), quarter = threadIdx.x >> 5;
+  if (row >= active) return;
+  auto slot_of = [&](int c) { return (size_t)(c == c0 ? 2 * c0 + 1 : 2 * c) * 256; };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) + row).x);
+  const float nb = M == -INFINITY ? 0.f : M;
+  float o[D / 4], total = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) o[i] = 0.f;
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const float2 ml = __ldcg(p.part_ml + slot_of(c) + row);
+    const float4* src = p.part_o + slot_of(c) * (D / 4) + (size_t)quarter * (D / 16) * 256 + row;
+    float4 a[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) a[i] = __ldcg(src + (size_t)i * 256);
+    if (ml.y == 0.f) continue;  // nothing of the part is visible to the row
+    const float f = exp2f(ml.x - nb);
+    total += ml.y * f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      o[4 * i] = fmaf(a[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(a[i].y, f, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(a[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(a[i].w, f, o[4 * i + 3]);
+    }
+  }
+  const float inv = p.v_scale / total;
+  const int g = __ldcg(&p.cuts[c0].row0) + row, t = p.by_group.of(g);
+  T* out = static_cast<T*>(p.out) +
+           ((size_t)(__ldcg(&p.cuts[c0].q0) + t) * p.num_heads + __ldcg(&p.cuts[c0].kvh) * p.group + (g - t * p.group)) * D +
+           quarter * (D / 4);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    reinterpret_cast<uint4*>(out)[i] =
+        make_uint4(PwPack<T>::pack(o[8 * i] * inv, o[8 * i + 1] * inv), PwPack<T>::pack(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                   PwPack<T>::pack(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                   PwPack<T>::pack(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
 }
 
 }  // namespace pkv

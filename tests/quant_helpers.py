@@ -99,7 +99,8 @@ class Batch:
         e4m3 codes exact; bfloat16 queries a power of two of the row's own, values below 2^-28 of the largest
         rounded to 2^-39 of it), a sum of D products in fp32 (2^-23 of the sum of absolute products a step,
         whatever the order), scaled and shifted (3 more). A weight: an exponential of it, off by the logit's
-        error and 2^-21, rounded to binary16 (2^-11 relative, or 2^-38 of the largest once subnormal), over
+        error and 2^-21, rounded to binary16 (2^-11 relative; once subnormal 2^-25, that is 2^-32 of the row's largest,
+        which stands for 2^7 at least), over
         a sum of L of them in fp32. An output: a sum of L products, V rounded as K is; then its own rounding."""
         L, n = self.seqs[s]
         q = self.q[self.first[s] + a:self.first[s] + b].double().transpose(0, 1)   # [H, b - a, D]
@@ -114,7 +115,7 @@ class Batch:
                                + 2.0 ** -39 * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1).amax(-1)[:, None, None])
         rel = torch.expm1(2 * E) + 2 ** -20 + L * u + 2.0 ** -11
         out, mag = p @ v, p @ v.abs()
-        far = 2.0 ** -38 * p.amax(-1, keepdim=True) * v.abs().sum(1, keepdim=True)
+        far = 2.0 ** -32 * p.amax(-1, keepdim=True) * v.abs().sum(1, keepdim=True)
         bound = (rel + in16 + L * u) * mag + tiny + far
         half = torch.finfo(self.dtype).eps / 2
         tol = bound + half * (out.abs() + bound) + torch.finfo(self.dtype).smallest_normal * 2 * half

@@ -157,12 +157,11 @@ def test_bad_lengths_and_blocks(pkv, kind):
 
 def test_one_workspace_serves_all_sizes(pkv):
     ws = pkv.new_prefill_workspace(128)
-    ws[pkv.PREFILL_COUNTER_BYTES:].fill_(0xFF)
+    ws.fill_(0xFF)
     for i, (kind, D, batch) in enumerate([("q4", 128, "far"), ("fp8", 64, "long"), ("q4", 64, "tiles"), ("fp8", 128, "far"),
                                           ("q4", 128, "one"), ("fp8", 128, "short"), ("q4", 128, "far")]):
         b = Batch(BATCHES[batch], 2, 2, D, 16, "bf16", kind, seed=i)
         b.check(b.run(pkv, ws=ws), (i, batch))
-        assert (ws[:pkv.PREFILL_COUNTER_BYTES] == 0).all()
 
 
 @pytest.mark.parametrize("kind", ["q4", "fp8"])

@@ -46,7 +46,7 @@ def test_refusals(pkv):
 
 
 def test_workspace_sizes(pkv):
-    assert pkv.prefill_workspace_bytes(128) >= pkv.prefill_workspace_bytes(64) >= pkv.PREFILL_COUNTER_BYTES
+    assert pkv.prefill_workspace_bytes(128) >= pkv.prefill_workspace_bytes(64) > 0
     for D in (0, -64, 96, 256):
         assert pkv.prefill_workspace_bytes(D) == 0
 
