@@ -75,7 +75,7 @@ cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   const int64_t rows = queries * a.group < 256 ? queries * a.group : 256;
   cfg.gridDim = dim3(ctas, (unsigned)((rows + 31) / 32));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(2 * D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

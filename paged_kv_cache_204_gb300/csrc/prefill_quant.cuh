@@ -76,7 +76,7 @@ __device__ __forceinline__ bool pq_wait(uint64_t* bar, uint32_t parity, uint64_t
 using PqCost = int;
 
 // A pair that lies in more than one CTA, as the one that it starts in tells the joining kernel.
-struct PqCut {
+struct alignas(16) PqCut {
   int last;  // CTA of its last part; below 0: no such pair
   int q0, kvh, row0, active;
   int pad[3];
@@ -241,15 +241,9 @@ struct PqWalk {
   }
 };
 
-// Where a CTA's stretch begins, worked out once by the whole CTA.
-struct PqBegin {
-  PqShare share;
-  PqCost at, lo, hi;
-  int s, kvh, pair;
-};
-
+// Sum over a warp's lanes of those up to this one.
 template <typename I>
-__device__ __forceinline__ I pq_warp_scan(I v) {  // inclusive
+__device__ __forceinline__ I pq_warp_scan(I v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -258,17 +252,76 @@ __device__ __forceinline__ I pq_warp_scan(I v) {  // inclusive
   }
   return v;
 }
-// Sum over the CTA of every warp's `own` (that of its last lane): the sum, and of the warps before this one.
-template <typename I>
-__device__ __forceinline__ I pq_block_sum(I own, I* sums, I& before) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();  // (the last use of sums is over)
-  if (lane == 31) sums[warp] = own;
-  __syncthreads();
-  const I upto = pq_warp_scan(lane < kPqThreads / 32 ? sums[lane] : (I)0);
-  before = __shfl_sync(kFullMask, upto, max(warp - 1, 0));
-  if (warp == 0) before = 0;
-  return __shfl_sync(kFullMask, upto, 31);
+
+// The walk at the beginning of the CTA's stretch; false where it has none. By one warp (a lane to a
+// sequence): the others have their barriers and tensor memory to see to.
+__device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
+  const int lane = threadIdx.x & 31, G = p.group;
+  long long tokens = 0;
+  PqSeq first;  // of sequence `lane`
+  first.live = false;
+#pragma unroll 1
+  for (int s = lane; s < p.num_seqs; s += 32) {
+    PqSeq q;
+    q.load(p, s);
+    if (q.live) tokens += q.tokens(q.pairs(G), G) * p.num_kv_heads;
+    if (!q.valid && blockIdx.x == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
+    if (s == lane) first = q;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(kFullMask, tokens, o);
+  PqShare& share = walk.share;
+  share.ctas = min(max((int)fminf((float)tokens / (float)(G * kPqMinTokens), 1e6f), 1), (int)gridDim.x);
+  if (tokens == 0 || (int)blockIdx.x >= share.ctas) return false;
+  share.shift = max(34 - __clzll(tokens), 0);  // tokens >> shift < 2^30
+  auto cost_of = [&](int s, PqSeq& q) {
+    if (s < 32)
+      q = first;
+    else if (s < p.num_seqs)
+      q.load(p, s);
+    return s < p.num_seqs && q.live ? q.before(q.pairs(G), G, share.shift) * p.num_kv_heads : 0;
+  };
+  share.whole = 0;
+#pragma unroll 1
+  for (int s = lane; s < p.num_seqs; s += 32) {
+    PqSeq q;
+    share.whole += cost_of(s, q);
+  }
+  share.whole = __reduce_add_sync(kFullMask, share.whole);
+  const PqCost lo = share.begin(blockIdx.x);
+  PqCost base = 0;
+#pragma unroll 1
+  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+    PqSeq q;
+    const PqCost own = cost_of(s0 + lane, q), upto = base + pq_warp_scan(own);
+    const uint32_t here = __ballot_sync(kFullMask, lo < upto);
+    if (here != 0u) {
+      const int src = __ffs(here) - 1;
+      walk.s = s0 + src;
+      const PqCost at = __shfl_sync(kFullMask, upto - own, src);
+      q.load(p, walk.s);
+      walk.seq = q;
+      walk.np = q.pairs(G);
+      const PqCost head = q.before(walk.np, G, share.shift);
+      walk.kvh = (lo - at) / head;
+      const PqCost y = (lo - at) - walk.kvh * head;
+      int a = 0, b = walk.np;  // the pair that holds y: before(a) <= y < before(b)
+      while (b - a > 1) {
+        const int mid = (a + b) / 2;
+        if (q.before(mid, G, share.shift) <= y)
+          a = mid;
+        else
+          b = mid;
+      }
+      walk.pair = a;
+      walk.at = lo - y + q.before(a, G, share.shift);
+      walk.lo = lo;
+      walk.hi = share.begin(blockIdx.x + 1);
+      return true;
+    }
+    base = __shfl_sync(kFullMask, upto, 31);
+  }
+  return false;
 }
 
 // 8 bytes of codes as 16 values d (q - 8): low halves to lo, high halves to hi. A code placed
@@ -400,88 +453,16 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   unsigned char* misc = sm + S::kMiscOff;
   uint32_t* slot = reinterpret_cast<uint32_t*>(misc);             // tensor-memory address
   uint32_t* held_blocks = reinterpret_cast<uint32_t*>(misc + 16); // [NR] blocks of a raw tile that were copied
-  PqBegin* begin = reinterpret_cast<PqBegin*>(swap);              // (read before the first part is there)
-  static_assert(sizeof(PqBegin) <= 128 && 16 + 4 * NR <= 64, "room");
+  static_assert(16 + 4 * NR <= 64, "room");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group;
 
   // ---- the CTA's stretch of the whole -----------------------------------------
   grid_launch_dependents();  // (the joining kernel waits for all of this one's memory all the same)
-  if (tid == 0) p.cuts[blockIdx.x].last = -1;
-  {
-    long long* sums64 = reinterpret_cast<long long*>(sm);  // [warps], before anything else is there
-    PqCost* sums = reinterpret_cast<PqCost*>(sm + 512);
-    auto load = [&](int s, PqSeq& q) {
-      q.live = false;
-      if (s < p.num_seqs) q.load(p, s);
-      return q.live;
-    };
-    PqSeq first;
-    long long tokens = 0;
-    for (int s = tid; s < p.num_seqs; s += kPqThreads) {
-      PqSeq q;
-      if (load(s, q)) tokens += q.tokens(q.pairs(G), G) * p.num_kv_heads;
-      if (!q.valid && blockIdx.x == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
-      if (s == tid) first = q;
-    }
-    if (tid >= p.num_seqs) first.live = false;
-    long long unused;
-    tokens = pq_block_sum(pq_warp_scan(tokens), sums64, unused);
-    const float most = (float)tokens / (float)(G * kPqMinTokens);
-    PqShare share;
-    share.ctas = min(max((int)fminf(most, 1e6f), 1), (int)gridDim.x);
-    if (tokens == 0 || (int)blockIdx.x >= share.ctas) return;
-    share.shift = max(34 - __clzll(tokens), 0);  // tokens >> shift < 2^30
-    auto cost_of = [&](bool live, const PqSeq& q) {
-      return live ? q.before(q.pairs(G), G, share.shift) * p.num_kv_heads : 0;
-    };
-    PqCost mine = 0, dummy;
-    if (p.num_seqs <= kPqThreads) {
-      mine = cost_of(first.live, first);
-    } else {
-      for (int s = tid; s < p.num_seqs; s += kPqThreads) {
-        PqSeq q;
-        const bool live = load(s, q);
-        mine += cost_of(live, q);
-      }
-    }
-    share.whole = pq_block_sum(pq_warp_scan(mine), sums, dummy);
-    const PqCost lo = share.begin(blockIdx.x);
-    PqCost base = 0;
-    for (int s0 = 0; s0 < p.num_seqs && base <= lo; s0 += kPqThreads) {
-      PqSeq q = first;
-      const bool live = p.num_seqs <= kPqThreads ? first.live : load(s0 + tid, q);
-      const PqCost own = cost_of(live, q), upto = pq_warp_scan(own);
-      PqCost before;
-      const PqCost all = pq_block_sum(upto, sums, before);
-      before += base + upto - own;
-      if (own > 0 && before <= lo && lo < before + own) {
-        const int np = q.pairs(G);
-        const PqCost head = q.before(np, G, share.shift);
-        begin->s = s0 + tid;
-        begin->kvh = (lo - before) / head;
-        const PqCost y = (lo - before) % head;
-        int a = 0, b = np;  // the pair that holds y: before(a) <= y < before(b)
-        while (b - a > 1) {
-          const int mid = (a + b) / 2;
-          if (q.before(mid, G, share.shift) <= y)
-            a = mid;
-          else
-            b = mid;
-        }
-        begin->pair = a;
-        begin->at = lo - y + q.before(a, G, share.shift);
-        begin->lo = lo;
-        begin->hi = share.begin(blockIdx.x + 1);
-        begin->share = share;
-      }
-      base += all;
-    }
-  }
 
   // ---- set-up: barriers, tensor memory ----------------------------------------
-  if (tid == 0) {
+  if (tid == kPqThreads - 1) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kPqConvert);
@@ -574,17 +555,14 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     if (warp == 18) {
       // ---- the walk
       PqWalk walk;
-      walk.share = begin->share;
-      walk.s = begin->s, walk.kvh = begin->kvh, walk.pair = begin->pair;
-      walk.at = begin->at, walk.lo = begin->lo, walk.hi = begin->hi;
-      walk.seq.load(p, walk.s);
-      walk.np = walk.seq.pairs(G);
+      if (lane == 0) p.cuts[blockIdx.x].last = -1;
+      const bool any = pq_begin(p, walk);
       for (uint32_t n = 0;; ++n) {
         if (n >= kPqRing && !wait(&part_empty[n % kPqRing], (n / kPqRing + 1) & 1)) {
           bad = true;
           break;
         }
-        const bool stop = walk.done();
+        const bool stop = !any || walk.done();
         PqPart part;
         if (!stop) part = walk.part(p);
         if (lane == 0) {
@@ -1087,47 +1065,52 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   }
 }
 
-// The cut pairs' parts joined: grid = (CTA that a pair starts in, 32 rows of it), a warp to a quarter of the
-// head dims, a row to a lane.
+// The cut pairs' parts joined: grid = (CTA that a pair starts in, 32 rows of it), 16 head dims to a warp, a row to
+// a lane; the parts come four at a time, so that their loads are under way together.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) pa_prefill_quant_join_kernel(const __grid_constant__ PqParams p) {
+__global__ void __launch_bounds__(2 * D) pa_prefill_quant_join_kernel(const __grid_constant__ PqParams p) {
   grid_dependency_wait();
-  const int c0 = blockIdx.x, c1 = __ldcg(&p.cuts[c0].last);
-  if (c1 < 0) return;
+  const int c0 = blockIdx.x;
+  const int4 told = __ldcg(reinterpret_cast<const int4*>(p.cuts + c0));  // last, q0, kvh, row0
   const int active = __ldcg(&p.cuts[c0].active);
-  const int row = blockIdx.y * 32 + (threadIdx.x & 31), quarter = threadIdx.x >> 5;
+  const int c1 = told.x;
+  if (c1 < 0) return;
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), k0 = threadIdx.x >> 5;
   if (row >= active) return;
-  auto slot_of = [&](int c) { return (size_t)(c == c0 ? 2 * c0 + 1 : 2 * c) * 256; };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot_of(c) + row).x);
-  const float nb = M == -INFINITY ? 0.f : M;
-  float o[D / 4], total = 0.f;
+  float M = -INFINITY, o[16], total = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 4; ++i) o[i] = 0.f;
-#pragma unroll 2
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = __ldcg(p.part_ml + slot_of(c) + row);
-    const float4* src = p.part_o + slot_of(c) * (D / 4) + (size_t)quarter * (D / 16) * 256 + row;
-    float4 a[D / 16];
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 1
+  for (int c = c0; c <= c1; c += 4) {
+    float2 ml[4];
+    float4 a[4][4];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) a[i] = __ldcg(src + (size_t)i * 256);
-    if (ml.y == 0.f) continue;  // nothing of the part is visible to the row
-    const float f = exp2f(ml.x - nb);
-    total += ml.y * f;
+    for (int e = 0; e < 4; ++e) {
+      const size_t slot = (size_t)(c + e == c0 ? 2 * c0 + 1 : 2 * min(c + e, c1)) * 256;
+      ml[e] = __ldcg(p.part_ml + slot + row);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      o[4 * i] = fmaf(a[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(a[i].y, f, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(a[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(a[i].w, f, o[4 * i + 3]);
+      for (int i = 0; i < 4; ++i) a[e][i] = __ldcg(p.part_o + slot * (D / 4) + (size_t)(4 * k0 + i) * 256 + row);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + e > c1 || ml[e].y == 0.f) continue;  // (0: nothing of the part is visible to the row)
+      const float top = fmaxf(M, ml[e].x), nb = top == -INFINITY ? 0.f : top;
+      const float keep = exp2f(M - nb), f = exp2f(ml[e].x - nb);
+      M = top;
+      total = fmaf(total, keep, ml[e].y * f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[4 * i] = fmaf(o[4 * i], keep, a[e][i].x * f), o[4 * i + 1] = fmaf(o[4 * i + 1], keep, a[e][i].y * f);
+        o[4 * i + 2] = fmaf(o[4 * i + 2], keep, a[e][i].z * f), o[4 * i + 3] = fmaf(o[4 * i + 3], keep, a[e][i].w * f);
+      }
     }
   }
   const float inv = p.v_scale / total;
-  const int g = __ldcg(&p.cuts[c0].row0) + row, t = p.by_group.of(g);
+  const int g = told.w + row, t = p.by_group.of(g);
   T* out = static_cast<T*>(p.out) +
-           ((size_t)(__ldcg(&p.cuts[c0].q0) + t) * p.num_heads + __ldcg(&p.cuts[c0].kvh) * p.group + (g - t * p.group)) * D +
-           quarter * (D / 4);
+           ((size_t)(told.y + t) * p.num_heads + told.z * p.group + (g - t * p.group)) * D + 16 * k0;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
+  for (int i = 0; i < 2; ++i)
     reinterpret_cast<uint4*>(out)[i] =
         make_uint4(PwPack<T>::pack(o[8 * i] * inv, o[8 * i + 1] * inv), PwPack<T>::pack(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                    PwPack<T>::pack(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
