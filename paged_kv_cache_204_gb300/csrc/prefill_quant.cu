@@ -60,6 +60,7 @@ cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
   const int64_t queries = a.max_query_len < longest ? a.max_query_len : longest;
   if (queries * a.group > 0x7fffffffLL - 256) return cudaErrorNotSupported;
   p.max_query_len = a.max_query_len;
+  p.start = pq_start(D);
   p.by_group.set((uint32_t)a.group);
   char* ws = static_cast<char*>(a.workspace);
   p.cuts = reinterpret_cast<PqCut*>(ws);

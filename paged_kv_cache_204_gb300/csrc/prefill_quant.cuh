@@ -36,8 +36,13 @@ constexpr int kPqMaxCtas = 152;
 // Registers of a thread after the split, which the launch's 96 add up to: softmax, MMA and copy, conversion.
 constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 96, kPqIssueRegs = 48, kPqConvertRegs = 48;
 static_assert(4 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs <= kPqThreads / 128 * kPqLaunchRegs, "no more than the launch has");
-constexpr int kPqStart = 256;     // a pair's start and end, as tokens of its walk
-constexpr int kPqMinTokens = 512; // a CTA's stretch is no shorter
+// A pair's start and end, as tokens of its walk. Head_dim 128: 522 us with 256, 466 with 512, 484 with 1024 (8192
+// queries over q4_0, 32 query and 8 kv heads); head_dim 64, where a tile takes less: 109 with 256, 108 with 384, 116 with
+// 512 (8 prompts of up to 1500 tokens, 40 heads).
+constexpr int pq_start(int head_dim) { return head_dim == 64 ? 384 : 512; }
+// A CTA's stretch is no shorter: one chunk of 100 queries behind 2677 tokens takes 31 us (35 with 1024, 50 with 2048; 128
+// to 384 give the same).
+constexpr int kPqMinTokens = 512;
 constexpr int kPqRing = 4;        // parts that the walking warp may be ahead
 
 // pw_wait for a kernel of many warps that wait much of their time: sixty-four attempts between two looks at the
@@ -94,6 +99,7 @@ struct PqParams {
   uint32_t flip;     // sign bits of a pair of query elements for a negative scale, else 0
   int zero_scale;    // scale 0: rows have equal weights, their exponents left alone
   int num_seqs, num_heads, num_kv_heads, group, block_size, block_bits, max_blocks_per_seq, num_blocks, max_query_len;
+  int start;         // pq_start()
   PwDivisor by_group;
   PqCut* cuts;       // [kPqMaxCtas]
   float2* part_ml;   // [2 kPqMaxCtas][256]
@@ -140,13 +146,13 @@ struct PqSeq {
   }
   __device__ __forceinline__ int pairs(int group) const { return (int)(((int64_t)n * group + 255) / 256); }
   // tokens x group of the first k of its pairs (per kv head) ...
-  __device__ __forceinline__ long long tokens(int k, int group) const {
-    const long long each = (long long)group * (kPqStart + L - n), rows = (long long)n * group;
+  __device__ __forceinline__ long long tokens(int k, int group, int start) const {
+    const long long each = (long long)group * (start + L - n), rows = (long long)n * group;
     return k * each + (256LL * k < rows ? 128LL * k * (k + 1) : 128LL * k * (k - 1) + rows);
   }
   // ... and their cost: no pair without any
-  __device__ __forceinline__ PqCost before(int k, int group, int shift) const {
-    return (PqCost)(tokens(k, group) >> shift) + k;
+  __device__ __forceinline__ PqCost before(int k, int group, int start, int shift) const {
+    return (PqCost)(tokens(k, group, start) >> shift) + k;
   }
 };
 
@@ -166,18 +172,19 @@ struct PqShare {
 struct alignas(16) PqPart {
   int s, kvh, q0, base;      // sequence; kv head; its first query; tokens before it
   int row0, active;          // first row; rows of the pair
-  int end_a, end_b;          // tokens that the last queries of A and B see
+  int end_a, end_b;          // tokens that the last queries of A and B see (0: B has none)
   int j0, j1;                // K/V tiles of this part
-  int c0, c1;                // CTAs that the pair's parts lie in
   int kind;                  // bits below
-  int pad[3];
+  int last;                  // CTA of the pair's last part
+  int pad[4];
   static constexpr int kStop = 1;   // no part: the walk is over
   static constexpr int kDual = 2;   // one tile of rows: A and B take K/V tiles in turn
   static constexpr int kHead = 4;   // the pair starts here
+  static constexpr int kWhole = 8;  // and ends here
   __device__ __forceinline__ bool stop() const { return kind & kStop; }
   __device__ __forceinline__ bool dual() const { return kind & kDual; }
-  __device__ __forceinline__ bool whole() const { return c0 == c1; }
-  __device__ __forceinline__ int end() const { return dual() ? end_a : end_b; }
+  __device__ __forceinline__ bool whole() const { return kind & kWhole; }
+  __device__ __forceinline__ int end() const { return max(end_a, end_b); }
   __device__ __forceinline__ int active_of(int x) const { return dual() ? active : max(min(active - 128 * x, 128), 0); }
   // Queries of tile x (A: 0, B: 1) take part in K/V tile j.
   __device__ __forceinline__ bool sees(int x, int j) const {
@@ -194,25 +201,32 @@ struct PqWalk {
   PqCost at, cost, lo, hi;  // the pair's place and length; the CTA's stretch
 
   __device__ __forceinline__ bool done() const { return at >= hi; }
-  __device__ __forceinline__ PqPart part(const PqParams& p) {
-    PqPart t;
-    cost = seq.before(pair + 1, p.group, share.shift) - seq.before(pair, p.group, share.shift);
+  // The pair at hand, or what of it lies here; false where that is nothing.
+  __device__ __forceinline__ bool part(const PqParams& p, PqPart& t) {
+    cost = seq.before(pair + 1, p.group, p.start, share.shift) - seq.before(pair, p.group, p.start, share.shift);
     t.s = s, t.kvh = kvh, t.q0 = seq.q0, t.base = seq.L - seq.n;
     t.row0 = pair * 256;
     t.active = min(seq.n * p.group - t.row0, 256);
-    const bool dual = t.active <= 128, head = lo <= at;
+    const bool one = t.active <= 128;
     t.end_a = t.base + 1 + p.by_group.of(t.row0 + min(t.active, 128) - 1);
-    t.end_b = dual ? 0 : t.base + 1 + p.by_group.of(t.row0 + t.active - 1);
-    t.kind = (dual ? PqPart::kDual : 0) | (head ? PqPart::kHead : 0);
+    t.end_b = one ? 0 : t.base + 1 + p.by_group.of(t.row0 + t.active - 1);
     const int tiles = (t.end() + 127) / 128;
     // (the same place gives the same tile to the CTA before it and to the one behind)
     const float scale = (float)tiles / (float)cost;
     auto tile_at = [&](PqCost y) { return y <= 0 ? 0 : (y >= cost ? tiles : min((int)((float)y * scale), tiles)); };
     t.j0 = tile_at(lo - at);
     t.j1 = tile_at(hi - at);
-    t.c0 = head ? (int)blockIdx.x : share.of(at);
-    t.c1 = at + cost <= hi ? (int)blockIdx.x : share.of(at + cost - 1);
-    return t;
+    t.kind = (lo <= at ? PqPart::kHead : 0) | (t.j0 == 0 && t.j1 == tiles ? PqPart::kWhole : 0);
+    t.last = blockIdx.x;
+    if (!t.whole()) {
+      // one CTA may have every tile, although borders lie in the pair: the others have nothing to do then
+      int c = lo <= at ? (int)blockIdx.x : share.of(at);
+      while (tile_at(share.begin(c + 1) - at) == 0) ++c;
+      if (tile_at(share.begin(c + 1) - at) == tiles) return false;
+      t.last = share.of(at + cost - 1);
+    }
+    if (one && t.j1 - t.j0 > 1) t.kind |= PqPart::kDual;
+    return true;
   }
   __device__ __forceinline__ void next(const PqParams& p) {
     at += cost;
@@ -264,7 +278,7 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
   for (int s = lane; s < p.num_seqs; s += 32) {
     PqSeq q;
     q.load(p, s);
-    if (q.live) tokens += q.tokens(q.pairs(G), G) * p.num_kv_heads;
+    if (q.live) tokens += q.tokens(q.pairs(G), G, p.start) * p.num_kv_heads;
     if (!q.valid && blockIdx.x == 0) set_err(p.dev_err, PKV_DEV_ERR_CONTEXT_LEN);
     if (s == lane) first = q;
   }
@@ -279,7 +293,7 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
       q = first;
     else if (s < p.num_seqs)
       q.load(p, s);
-    return s < p.num_seqs && q.live ? q.before(q.pairs(G), G, share.shift) * p.num_kv_heads : 0;
+    return s < p.num_seqs && q.live ? q.before(q.pairs(G), G, p.start, share.shift) * p.num_kv_heads : 0;
   };
   share.whole = 0;
 #pragma unroll 1
@@ -302,19 +316,19 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
       q.load(p, walk.s);
       walk.seq = q;
       walk.np = q.pairs(G);
-      const PqCost head = q.before(walk.np, G, share.shift);
+      const PqCost head = q.before(walk.np, G, p.start, share.shift);
       walk.kvh = (lo - at) / head;
       const PqCost y = (lo - at) - walk.kvh * head;
       int a = 0, b = walk.np;  // the pair that holds y: before(a) <= y < before(b)
       while (b - a > 1) {
         const int mid = (a + b) / 2;
-        if (q.before(mid, G, share.shift) <= y)
+        if (q.before(mid, G, p.start, share.shift) <= y)
           a = mid;
         else
           b = mid;
       }
       walk.pair = a;
-      walk.at = lo - y + q.before(a, G, share.shift);
+      walk.at = lo - y + q.before(a, G, p.start, share.shift);
       walk.lo = lo;
       walk.hi = share.begin(blockIdx.x + 1);
       return true;
@@ -562,13 +576,13 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           bad = true;
           break;
         }
-        const bool stop = !any || walk.done();
         PqPart part;
-        if (!stop) part = walk.part(p);
+        while (any && !walk.done() && !walk.part(p, part)) walk.next(p);
+        const bool stop = !any || walk.done();
         if (lane == 0) {
           if (!stop && (part.kind & PqPart::kHead) && !part.whole()) {
             PqCut& told = p.cuts[blockIdx.x];
-            told.last = part.c1;
+            told.last = part.last;
             told.q0 = part.q0, told.kvh = part.kvh, told.row0 = part.row0, told.active = part.active;
           }
           if (stop)
@@ -1086,7 +1100,8 @@ __global__ void __launch_bounds__(2 * D) pa_prefill_quant_join_kernel(const __gr
     float4 a[4][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const size_t slot = (size_t)(c + e == c0 ? 2 * c0 + 1 : 2 * min(c + e, c1)) * 256;
+      if (c + e > c1) break;
+      const size_t slot = (size_t)(c + e == c0 ? 2 * c0 + 1 : 2 * (c + e)) * 256;
       ml[e] = __ldcg(p.part_ml + slot + row);
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[e][i] = __ldcg(p.part_o + slot * (D / 4) + (size_t)(4 * k0 + i) * 256 + row);
