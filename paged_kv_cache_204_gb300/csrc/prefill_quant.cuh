@@ -34,7 +34,7 @@ constexpr int kPqSoft = 16;       // softmax warps: A's first and second halves 
 constexpr int kPqConvert = 4;     // converting warps
 constexpr int kPqMaxCtas = 152;
 // Registers of a thread after the split, which the launch's 96 add up to: softmax, MMA and copy, conversion.
-constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 96, kPqIssueRegs = 48, kPqConvertRegs = 48;
+constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 88, kPqIssueRegs = 56, kPqConvertRegs = 72;
 static_assert(4 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs <= kPqThreads / 128 * kPqLaunchRegs, "no more than the launch has");
 // A pair's start and end, as tokens of its walk. Head_dim 128: 522 us with 256, 466 with 512, 484 with 1024 (8192
 // queries over q4_0, 32 query and 8 kv heads); head_dim 64, where a tile takes less: 109 with 256, 108 with 384, 116 with
@@ -364,60 +364,57 @@ __device__ __forceinline__ uint32_t pq_from_e4m3x2(uint32_t two) {
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 
-// One half (h) of row r of a tile: its bytes at `row` become the operand's values (zeros where
-// !held) in the swizzled tile at `tile`.
+// Row r of a tile: its bytes at `row` become the operand's values (zeros where !held) in the swizzled tile
+// at `tile`.
 template <PqFormat F, int D>
-__device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, int h, bool held) {
+__device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, bool held) {
   unsigned char* at = tile + r * 128;
   const uint32_t swz = (r & 7) << 4;
   // values 8 c .. 8 c + 7 of the row
   auto put = [&](int c, uint4 v) {
     *reinterpret_cast<uint4*>(at + (c >> 3) * (128 * 128) + ((((uint32_t)c & 7) << 4) ^ swz)) = v;
   };
-  const int c0 = h * (D / 16);
   if (!held) {
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) put(c0 + c, make_uint4(0u, 0u, 0u, 0u));
+    for (int c = 0; c < D / 8; ++c) put(c, make_uint4(0u, 0u, 0u, 0u));
     return;
   }
   // all is read before anything is written, so that the reads need not wait for one another
   if constexpr (F == PqFormat::kQ4) {
-    constexpr int kBlocks = D / 64;  // of this half
-    uint32_t w[4 * kBlocks], scales;
-    const unsigned char* codes = row + D / 16 + 16 * kBlocks * h;
+    constexpr int kWords = D / 64 * 9;
+    uint32_t w[kWords];
     if constexpr (D == 128) {  // (rows start on 8 bytes at head_dim 128, on 4 at 64)
-      scales = reinterpret_cast<const uint32_t*>(row)[h];
 #pragma unroll
-      for (int i = 0; i < 2 * kBlocks; ++i) {
-        const uint2 x = reinterpret_cast<const uint2*>(codes)[i];
+      for (int i = 0; i < kWords / 2; ++i) {
+        const uint2 x = reinterpret_cast<const uint2*>(row)[i];
         w[2 * i] = x.x, w[2 * i + 1] = x.y;
       }
     } else {
-      scales = reinterpret_cast<const unsigned short*>(row)[h];
 #pragma unroll
-      for (int i = 0; i < 4 * kBlocks; ++i) w[i] = reinterpret_cast<const uint32_t*>(codes)[i];
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[i];
     }
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const __half2 d = __half2half2(__ushort_as_half((unsigned short)(scales >> (16 * b))));
+    for (int b = 0; b < D / 32; ++b) {
+      const __half2 d = __half2half2(__ushort_as_half((unsigned short)(w[b / 2] >> (16 * (b & 1)))));
+      const uint32_t* codes = w + D / 64 + 4 * b;
       uint4 lo, hi;
-      pq_from_q4(w[4 * b], w[4 * b + 1], d, lo, hi);
-      put(c0 + 4 * b, lo);
-      put(c0 + 4 * b + 2, hi);
-      pq_from_q4(w[4 * b + 2], w[4 * b + 3], d, lo, hi);
-      put(c0 + 4 * b + 1, lo);
-      put(c0 + 4 * b + 3, hi);
+      pq_from_q4(codes[0], codes[1], d, lo, hi);
+      put(4 * b, lo);
+      put(4 * b + 2, hi);
+      pq_from_q4(codes[2], codes[3], d, lo, hi);
+      put(4 * b + 1, lo);
+      put(4 * b + 3, hi);
     }
   } else {
     // lanes take a row's 16-byte chunks in orders of their own, so that eight lanes' chunks fall
     // into different banks
     const int turn = D == 128 ? r & 7 : (r >> 1) & 3;
-    uint4 x[D / 32];
+    uint4 x[D / 16];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = *reinterpret_cast<const uint4*>(row + 16 * ((h * (D / 32) + i) ^ turn));
+    for (int i = 0; i < D / 16; ++i) x[i] = *reinterpret_cast<const uint4*>(row + 16 * (i ^ turn));
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int c = (h * (D / 32) + i) ^ turn;
+    for (int i = 0; i < D / 16; ++i) {
+      const int c = i ^ turn;
       put(2 * c, make_uint4(pq_from_e4m3x2(x[i].x & 0xffffu), pq_from_e4m3x2(x[i].x >> 16),
                             pq_from_e4m3x2(x[i].y & 0xffffu), pq_from_e4m3x2(x[i].y >> 16)));
       put(2 * c + 1, make_uint4(pq_from_e4m3x2(x[i].z & 0xffffu), pq_from_e4m3x2(x[i].z >> 16),
@@ -549,10 +546,8 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           break;
         }
         const bool held = j * 128 + r < end && ((held_blocks[stage] >> block) & 1u);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pq_convert<F, D>(sm + S::kRawOff + stage * S::kRaw + r * S::kRow,
-                           sm + S::kStageOff + (2 * c + is_v) * S::kTile, r, h, held);
+        pq_convert<F, D>(sm + S::kRawOff + stage * S::kRaw + r * S::kRow,
+                         sm + S::kStageOff + (2 * c + is_v) * S::kTile, r, held);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
