@@ -689,7 +689,7 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
 /* pkv_paged_attention_prefill over fp8 caches: K is k_scale * code, V v_scale *
  * code, q and out of `dtype` (PKV_F16 or PKV_BF16). Arguments and errors as in
  * pkv_paged_attention_prefill, and
- *   k_scale, v_scale  finite and > 0 (with scale * k_scale finite)
+ *   k_scale, v_scale  finite and > 0 (with scale * k_scale * log2(e) finite in binary32)
  *   max_query_len     a sequence with more new tokens sets
  *                     PKV_DEV_ERR_CONTEXT_LEN and is skipped
  *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whatever
@@ -702,7 +702,10 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
  * less than 2^-28 of the row's largest). V rows that some query of the call sees
  * must be finite (a NaN there may also reach queries that do not see the token);
  * rows that no query sees may hold anything. A row whose largest logit is 2^27 or
- * more in magnitude may come out as NaN. */
+ * more in magnitude may come out as NaN. How a call's queries share the GPU follows
+ * from its lengths: equal arguments give equal bits, and a sequence's rows may
+ * differ in their last bits in another batch. With R = min(max_query_len, tokens of
+ * a table) * num_heads / num_kv_heads: PKV_ERR_UNSUPPORTED for R above 2^31 - 256. */
 pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
                                            const int32_t* block_tables, const int32_t* context_lens,
                                            const int32_t* query_start, float scale, float k_scale, float v_scale,

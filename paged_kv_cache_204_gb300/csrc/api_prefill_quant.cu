@@ -18,7 +18,7 @@ pkv_status prefill(void* out, const void* q, const void* k_cache, const void* v_
                    size_t workspace_bytes, int32_t* dev_err, pkv_stream_t stream) {
   if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
       max_blocks_per_seq <= 0 || num_blocks <= 0 || max_query_len < 0 || !std::isfinite(scale) ||
-      !valid_scale(k_scale) || !valid_scale(v_scale) || !std::isfinite(scale * k_scale))
+      !valid_scale(k_scale) || !valid_scale(v_scale) || !std::isfinite(scale * k_scale * 1.4426950408889634f))
     return PKV_ERR_INVALID_ARG;
   if (num_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
   if ((dtype != PKV_F16 && dtype != PKV_BF16) || (block_size != 8 && block_size != 16 && block_size != 32))

@@ -4,21 +4,33 @@
 // Work: the queries of a sequence against one kv head are n x group rows, row m = i * group + j
 // for new token i and the kv head's j-th query head, taken in pairs of tiles (A, B) of 128 rows.
 // A pair walks the K/V tiles of 128 tokens up to its last query's. On the fifth-generation tensor
-// cores S = Q K^T and O += P V accumulate in fp32 in tensor memory; a softmax warpgroup of its own
-// serves each of A and B, a row to a thread. The operands are binary16 whatever the queries' type
+// cores S = Q K^T and O += P V accumulate in fp32 in tensor memory; two softmax warpgroups serve
+// each of A and B, half a row to a thread. The operands are binary16 whatever the queries' type
 // (11 significant bits for 8, and bfloat16 queries are exact in it once a power of two of their
 // row's own is taken out): a copying warp brings a tile's bytes into shared memory, block by block,
 // and four warps turn them, a row to a thread, into the operand's values: e4m3 codes exactly (the
-// pool's scale multiplies 32-bit sums), q4_0 values d (q - 8) with one rounding. A tile's V and
-// the next one's K, which the MMAs of one step need together, are a link of a chain of two buffers.
-//
+// pool's scale multiplies 32-bit sums), q4_0 values d (q - 8) with one rounding. Doing it once for
+// 256 rows costs a sixth of a tile's instructions; the scales of q4_0 differ by token and by 32 dims,
+// so that they cannot be left to the sums of one MMA.
 // Where a pair has one tile only, B takes every other K/V tile of A's rows, so that one tile's
 // softmax runs under the other's MMAs there too, and A's warps join the two.
 //
 // Split: the pairs of all sequences and kv heads are laid end to end, each as long as its walk and
 // a start, and every CTA takes an equal stretch (the grid has one to an SM, fewer where the whole
 // is short). A pair that a border cuts leaves partial results in the workspace, which a second kernel
-// joins (log-sum-exp), 32 rows to a CTA.
+// joins (log-sum-exp), 32 rows to a CTA. (The last CTA of a pair as the joiner took 13 us of 51 for the
+// chunk below: one SM read 1.3 MB.)
+//
+// Bound by the way from S over the softmax back to the MMAs: a K/V tile takes A and B about 4300 cycles,
+// of which the MMAs are 2048; A's S, softmax (about 1900) and O follow one another, and B's only half hide
+// them, tensor memory having no room for a second S of either. 8192 queries over q4_0 (32 query, 8 kv heads, head_dim
+// 128, bfloat16): about 470 us, 1170 TFLOP/s over the visible tokens, where the same heads over 16-bit pools take the
+// window prefill 513 us; 1024 queries of 4 sequences of up to 6001 tokens over e4m3 (64 query heads): 300 us; 8 prompts
+// of up to 1500 tokens over q4_0 (40 heads of 64): 107 us; one chunk of 100 queries behind 2677 tokens: 31 us; 5 drafted
+// tokens for 16 sequences of up to 32768 (q4_0): 173 us, 2.0 TB/s, there bound by the copying and the converting
+// warps (about 1100 cycles each for a tile's K or V). Tried and slower there and elsewhere: copies by the converting
+// warps (bulk: 586 us for the 8192 queries; 16 bytes a lane: 513), three times the converting warps where few have
+// rows (200 us for the drafted tokens), S in halves of 64 tokens, two of each A and B under way (560 us).
 #pragma once
 
 #include <type_traits>
@@ -28,12 +40,13 @@
 
 namespace pkv {
 
-// 4 softmax warpgroups; MMA warps of A and B, copying warp, walking warp; a converting warpgroup
+// 4 softmax warpgroups; MMA warps of A and B, copying warp, walking warp; a converting warpgroup. (With one softmax
+// warpgroup to A and B: 522 us instead of 516 for the 8192 queries, 154 instead of 113 for the 8 prompts.)
 constexpr int kPqThreads = 768;
 constexpr int kPqSoft = 16;       // softmax warps: A's first and second halves of the columns, B's
 constexpr int kPqConvert = 4;     // converting warps
 constexpr int kPqMaxCtas = 152;
-// Registers of a thread after the split, which the launch's 96 add up to: softmax, MMA and copy, conversion.
+// Registers of a thread after the split, which the launch's 80 add up to: softmax, MMA and copy, conversion.
 constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 88, kPqIssueRegs = 56, kPqConvertRegs = 72;
 static_assert(4 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs <= kPqThreads / 128 * kPqLaunchRegs, "no more than the launch has");
 // A pair's start and end, as tokens of its walk. Head_dim 128: 522 us with 256, 466 with 512, 484 with 1024 (8192
@@ -428,6 +441,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   using S = PqShape<F, D>;
   using Out = PwPack<T>;
   using P16 = PwPack<__half>;
+  // The base of a row's running maximum moves only when that grows by more than kRescaleLog2, and it lies kTopLog2 -
+  // kRescaleLog2 below the maximum that it was taken from: every weight stays below 2^kTopLog2, binary16's range, and
+  // the largest at or above 2^7, so that a weight keeps its bits down to 2^-21 of it and has an error of 2^-32 of it
+  // below that (131072 tokens that far below one other lose 2^-15 of the output). Moved by 2, some row of a
+  // warp's 32 moves it in every third tile: 560 us instead of 516 for the 8192 queries.
   constexpr float kTopLog2 = 15.f, kRescaleLog2 = 8.f;
   constexpr int CB = S::kCB, NR = S::kRawStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -469,7 +487,6 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group;
 
-  // ---- the CTA's stretch of the whole -----------------------------------------
   grid_launch_dependents();  // (the joining kernel waits for all of this one's memory all the same)
 
   // ---- set-up: barriers, tensor memory ----------------------------------------
@@ -522,8 +539,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
 
   // (the registers of a warpgroup change hands for all its warps at once)
   if (warp >= 20) {
-    // ---- conversion: K of one tile, V of the one before, into the operands' buffers; a thread to
-    // half a row
+    // ---- conversion: K of one tile, V of the one before, into the operands' buffers; a thread to a row
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqConvertRegs));
     const int r = tid & 127, block = r >> p.block_bits;
     uint32_t tiles = 0;  // of earlier parts

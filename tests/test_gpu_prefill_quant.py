@@ -259,3 +259,74 @@ def test_session(pkv, kind, dtype, D, bs):
             want = torch.empty_like(out)
             decode(want, q, k, v, tables, context, scale, *more, 320, pkv.new_workspace(3, H, D, 320))
             assert (out.double() - want.double()).abs().max() <= tol
+
+
+@pytest.mark.parametrize("kind,batch", [("q4", "long"), ("fp8", "far"), ("q4", "short")])
+def test_gives_up_on_a_wait(pkv, kind, batch):
+    """With a limit of 0 any wait not over at its first test gives up: the call reports it and the next one works."""
+    b = Batch(BATCHES[batch], 2, 4, 128, 16, "bf16", kind)
+    ws = pkv.new_prefill_workspace(128)
+    good = b.run(pkv, ws=ws)
+    old, err = pkv.get_wait_timeout_ns(), new_err()
+    try:
+        pkv.set_wait_timeout_ns(0)
+        b.run(pkv, ws=ws, err=err)
+        torch.cuda.synchronize()
+    finally:
+        pkv.set_wait_timeout_ns(old)
+    assert int(err.item()) == pkv.DEV_ERR_TIMEOUT
+    err.zero_()
+    got = b.run(pkv, ws=ws, err=err)
+    assert int(err.item()) == 0
+    live = torch.isfinite(good.float())
+    assert torch.equal(got[live], good[live])
+
+
+@pytest.mark.parametrize("kind", ["q4", "fp8"])
+def test_blocks_past_four_gigabytes(pkv, kind):
+    """Blocks at the far end of pools of more than 2^32 bytes."""
+    b = Batch([(300, 40), (77, 1)], 8, 2, 128, 16, "bf16", kind, seed=9)
+    row = 128 if kind == "fp8" else 72
+    nb = (1 << 32) // (8 * 16 * row) + 1000
+    far = nb - b.nb
+    for name in ("k", "v"):
+        pool = torch.empty(nb, 8, 16, row, dtype=torch.uint8, device=DEV)
+        pool[far:] = getattr(b, name)
+        setattr(b, name, pool)
+    b.tables = torch.where(b.tables >= 0, b.tables + far, b.tables)
+    b.nb = nb
+    err = new_err()
+    b.check(b.run(pkv, err=err))
+    assert err.item() == 0
+
+
+def test_extra_rows_of_queries_and_wide_tables(pkv):
+    """Output rows behind the last sequence and table entries behind a sequence's blocks are left alone."""
+    b = Batch([(500, 60), (40, 3)], 2, 2, 64, 8, "f16", "q4", seed=11)
+    q = torch.cat([b.q, torch.full((9, b.H, 64), float("nan"), device=DEV, dtype=b.dtype)])
+    out = torch.full_like(q, 3.0)
+    b.q = q
+    b.bt[0, 500 // 8 + 1:] = 1 << 30
+    b.tables = torch.from_numpy(b.bt).to(DEV)
+    err = new_err()
+    b.run(pkv, err=err, out=out)
+    b.check(out)
+    assert err.item() == 0 and (out[63:] == 3).all()
+
+
+def test_binding_refusals(pkv):
+    b = Batch([(100, 10)], 2, 2, 64, 16, "bf16", "q4")
+    ws, out = pkv.new_prefill_workspace(64), torch.empty_like(b.q)
+    good = dict(out=out, q=b.q, k_cache=b.k, v_cache=b.v, block_tables=b.tables, context_lens=b.context, query_start=b.starts,
+                scale=b.scale, max_query_len=10, workspace=ws)
+    for name, bad in (("q", b.q.transpose(0, 1)), ("q", b.q.cpu()), ("q", b.q[0]), ("out", out.half()), ("out", out[:5]),
+                      ("k_cache", b.k.bfloat16()), ("v_cache", b.v[:1]), ("k_cache", b.k.cpu()), ("block_tables", b.tables.long()),
+                      ("block_tables", b.tables[0]), ("context_lens", b.context.long()), ("context_lens", b.starts),
+                      ("query_start", b.context), ("workspace", ws.cpu()), ("workspace", None), ("max_query_len", 1 << 40)):
+        with pytest.raises((ValueError, TypeError)):
+            pkv.paged_attention_prefill_q4_0(**{**good, name: bad})
+    with pytest.raises(ValueError):  # e4m3 rows are head_dim bytes
+        pkv.paged_attention_prefill_fp8(**{k: v for k, v in good.items()}, k_scale=1.0, v_scale=1.0)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.paged_attention_prefill_q4_0(**{**good, "workspace": ws[:100]})
+    assert e.value.status == pkv.PKV_ERR_WORKSPACE

@@ -275,3 +275,48 @@ def test_positions_of_zero_store_what_reshape_and_cache_stores(pkv):
             got, want = got.view(torch.uint8), want.view(torch.uint8)
         assert torch.equal(got, want) and torch.equal(s.v_bytes, v.view(torch.uint8))
         assert torch.equal(s.q_out, s.q)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("f16", "q4"), ("bf16", "fp8")])
+def test_slots_past_four_gigabytes(pkv, dtype, cache):
+    """Slots at the far end of pools of more than 2^32 bytes: the same bytes as at the near end."""
+    s = Step(pkv, 50, 8, 4, 128, 16, dtype, cache)
+    want = s.expected()
+    width = s.k_cache.shape[3] * s.k_cache.element_size()
+    nb = (1 << 32) // (4 * 16 * width) + 500
+    pools = [torch.empty(nb, 4, 16, s.k_cache.shape[3], dtype=s.k_cache.dtype, device=DEV) for _ in range(2)]
+    far = nb - s.nb
+    for pool, near in zip(pools, (s.k_cache, s.v_cache)):
+        pool[far:] = near
+    s.k_cache, s.v_cache = pools
+    s.slots = s.slots + far * 16
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    s.run(err=err)
+    assert err.item() == 0
+    for pool, bytes_ in zip(pools, want[1:]):
+        assert np.array_equal(pool[far:].contiguous().view(torch.uint8).cpu().numpy().reshape(bytes_.shape), bytes_)
+    assert torch.equal(s.q_out.cpu().view(torch.uint8), want[0].view(torch.uint8))
+
+
+def test_binding_refusals(pkv):
+    s = Step(pkv, 10, 8, 2, 128, 16, "bf16", axes=2)
+    pos, slots = torch.from_numpy(s.positions).to(DEV), torch.from_numpy(s.slots).to(DEV)
+    axis = bytes(s.axis.tolist())
+    good = dict(q_out=s.q_out, q=s.q, k=s.k, v=s.v, k_cache=s.k_cache, v_cache=s.v_cache, slot_mapping=slots, positions=pos,
+                cos_sin=s.table, pair_axis=axis)
+    for name, bad in (("q", s.q.float()), ("q", s.q[:, :, ::2]), ("q", s.q.transpose(0, 1)), ("q", s.q.cpu()), ("k", s.k[:5]),
+                      ("k", s.k[:, :1]), ("v", s.v.half()), ("q_out", s.q_out[:, :4]), ("k_cache", s.k_cache.float()),
+                      ("v_cache", s.v_cache[:2]), ("slot_mapping", slots.int()), ("slot_mapping", slots[:3]),
+                      ("positions", pos.long()), ("positions", pos[:, :4]), ("positions", pos[None]), ("cos_sin", s.table.double()),
+                      ("cos_sin", s.table[0]), ("cos_sin", s.table.t()), ("pair_axis", axis[:-1]), ("pair_axis", list(axis)),
+                      ("dev_err", slots)):
+        with pytest.raises((ValueError, TypeError)):
+            pkv.rope_and_cache(**{**good, name: bad})
+    for bad in (dict(pair_axis=None), dict(pair_axis=bytes([2] * 64)), dict(q_out=s.q[1:], q=s.q[:-1], k=s.k[1:], v=s.v[1:],
+                                                                           slot_mapping=slots[1:], positions=pos[:, 1:].contiguous())):
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.rope_and_cache(**{**good, **bad})
+        assert e.value.status == pkv.PKV_ERR_INVALID_ARG
+    for cache in (pkv.rope_and_cache_q4_0, lambda **a: pkv.rope_and_cache_fp8(**a, k_scale=1.0, v_scale=1.0)):
+        with pytest.raises(ValueError):
+            cache(**good)
