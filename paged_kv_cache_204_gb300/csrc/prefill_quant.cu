@@ -12,7 +12,7 @@ size_t ml_bytes() { return sizeof(float2) * 2 * kPqMaxCtas * 256; }
 
 template <typename T, PqFormat F, int D>
 cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
-  using S = PqShape<F, D>;
+  using S = PqShape<T, F, D>;
   auto kernel = pa_prefill_quant_kernel<T, F, D>;
   static int sms_of_device[64] = {0};  // SMs per device ordinal (0 = not yet known)
   int dev = 0;

@@ -9,7 +9,8 @@
 // (11 significant bits for 8, and bfloat16 queries are exact in it once a power of two of their
 // row's own is taken out): a copying warp brings a tile's bytes into shared memory, block by block,
 // and four warps turn them, a row to a thread, into the operand's values: e4m3 codes exactly (the
-// pool's scale multiplies 32-bit sums), q4_0 values d (q - 8) with one rounding. Doing it once for
+// pool's scale multiplies 32-bit sums), q4_0 values d (q - 8) with one rounding, or, K beside binary16 queries, in two
+// parts. Doing it once for
 // 256 rows costs a sixth of a tile's instructions; the scales of q4_0 differ by token and by 32 dims,
 // so that they cannot be left to the sums of one MMA.
 // Where a pair has one tile only, B takes every other K/V tile of A's rows, so that one tile's
@@ -26,7 +27,7 @@
 // them, tensor memory having no room for a second S of either. 8192 queries over q4_0 (32 query, 8 kv heads, head_dim
 // 128, bfloat16): about 470 us, 1170 TFLOP/s over the visible tokens, where the same heads over 16-bit pools take the
 // window prefill 513 us; 1024 queries of 4 sequences of up to 6001 tokens over e4m3 (64 query heads): 300 us; 8 prompts
-// of up to 1500 tokens over q4_0 (40 heads of 64): 107 us; one chunk of 100 queries behind 2677 tokens: 31 us; 5 drafted
+// of up to 1500 tokens over q4_0 (40 heads of 64, binary16): 123 us; one chunk of 100 queries behind 2677 tokens: 31 us; 5 drafted
 // tokens for 16 sequences of up to 32768 (q4_0): 173 us, 2.0 TB/s, there bound by the copying and the converting
 // warps (about 1100 cycles each for a tile's K or V). Tried and slower there and elsewhere: copies by the converting
 // warps (bulk: 586 us for the 8192 queries; 16 bytes a lane: 513), three times the converting warps where few have
@@ -123,7 +124,17 @@ struct PqParams {
 
 enum class PqFormat { kQ4, kFp8 };
 
-template <PqFormat F, int D>
+// Binary16 queries over q4_0: P and K enter in two 16-bit parts, a value rounded and what that leaves, since one
+// rounding of either is as much as an output's own. It costs 3 to 17 % at head_dim 64 (the 8 prompts: 123 us instead of
+// 106) and, with room for one tile of K only, up to 40 % at 128 (16 sequences of 40 queries behind up to 2600 tokens, 64
+// heads: 124 us instead of 89). Error against 64 bits over that of the output's rounding alone,
+// standard normal rows: 1.6 to 1.9 with one part of both, 1.5 to 1.6 with one of K (2.0 with logits of twice the
+// spread, since K's roundings grow with them), 1.3 with two of both. e4m3 values are exact (1.4 with one part of P), and a
+// bfloat16 output's rounding is 8 times as large.
+template <typename T, PqFormat F>
+constexpr bool kPqTwoParts = std::is_same<T, __half>::value && F == PqFormat::kQ4;
+
+template <typename T, PqFormat F, int D>
 struct PqShape {
   static constexpr int kCB = D / 64;
   static constexpr int kColBlock = 128 * 128;
@@ -131,8 +142,11 @@ struct PqShape {
   static constexpr int kRow = F == PqFormat::kQ4 ? D / 16 * 9 : D;   // bytes of a cache row
   static constexpr int kRaw = 128 * kRow;
   static constexpr int kRawStages = D == 64 ? 6 : (F == PqFormat::kQ4 ? 3 : 2);
-  static constexpr int kStageOff = 2 * kTile;                        // K, V, K, V
-  static constexpr int kRawOff = kStageOff + 4 * kTile;
+  static constexpr int kParts = kPqTwoParts<T, F> ? 2 : 1;           // of K and P
+  static constexpr int kKStages = kParts == 2 && D == 128 ? 1 : 2;   // (there is no room for two tiles of two parts)
+  static constexpr int kKOff = 2 * kTile;
+  static constexpr int kVOff = kKOff + kKStages * kParts * kTile;    // two V tiles
+  static constexpr int kRawOff = kVOff + 2 * kTile;
   static constexpr int kBarOff = kRawOff + kRawStages * kRaw;
   static constexpr int kBars = 2 * kRawStages + 18 + 2 * kPqRing + 16 + 2;
   static constexpr int kRingOff = (kBarOff + 8 * kBars + 15) / 16 * 16;
@@ -353,14 +367,23 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
 
 // 8 bytes of codes as 16 values d (q - 8): low halves to lo, high halves to hi. A code placed
 // under the exponent of 1024 (low halves, last place 1) or of 64 (high halves, last place 1/16)
-// is a binary16 number that exceeds it by that constant.
+// is a binary16 number that exceeds it by that constant. kRest: not the values, but what their rounding
+// leaves, which is exact: a multiple of 2^-24, as d is, of at most 11 bits (at most 16, and no matter what beside an
+// infinite value).
+template <bool kRest>
 __device__ __forceinline__ void pq_from_q4(uint32_t w0, uint32_t w1, __half2 d, uint4& lo, uint4& hi) {
   const __half2 k1032 = __half2half2(__ushort_as_half(0x6408)), k72 = __half2half2(__ushort_as_half(0x5480));
   auto part = [&](uint32_t w, uint32_t exponent, uint32_t sel, __half2 minus) {
     const uint32_t u = __byte_perm(w, exponent, sel);
     __half2 h;
     memcpy(&h, &u, 4);
-    h = __hmul2(__hsub2(h, minus), d);
+    h = __hsub2(h, minus);
+    if constexpr (kRest) {
+      const __half2 most = __half2half2(__ushort_as_half(0x4c00));
+      h = __hmax2(__hmin2(__hfma2(h, d, __hneg2(__hmul2(h, d))), most), __hneg2(most));
+    } else {
+      h = __hmul2(h, d);
+    }
     uint32_t r;
     memcpy(&r, &h, 4);
     return r;
@@ -378,8 +401,8 @@ __device__ __forceinline__ uint32_t pq_from_e4m3x2(uint32_t two) {
 }
 
 // Row r of a tile: its bytes at `row` become the operand's values (zeros where !held) in the swizzled tile
-// at `tile`.
-template <PqFormat F, int D>
+// at `tile`. kRest: what the values' rounding leaves as well, in the tile behind it.
+template <PqFormat F, int D, bool kRest>
 __device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, bool held) {
   unsigned char* at = tile + r * 128;
   const uint32_t swz = (r & 7) << 4;
@@ -389,7 +412,7 @@ __device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned ch
   };
   if (!held) {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) put(c, make_uint4(0u, 0u, 0u, 0u));
+    for (int c = 0; c < (kRest ? 2 : 1) * D / 8; ++c) put(c, make_uint4(0u, 0u, 0u, 0u));
     return;
   }
   // all is read before anything is written, so that the reads need not wait for one another
@@ -411,12 +434,17 @@ __device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned ch
       const __half2 d = __half2half2(__ushort_as_half((unsigned short)(w[b / 2] >> (16 * (b & 1)))));
       const uint32_t* codes = w + D / 64 + 4 * b;
       uint4 lo, hi;
-      pq_from_q4(codes[0], codes[1], d, lo, hi);
-      put(4 * b, lo);
-      put(4 * b + 2, hi);
-      pq_from_q4(codes[2], codes[3], d, lo, hi);
-      put(4 * b + 1, lo);
-      put(4 * b + 3, hi);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pq_from_q4<false>(codes[2 * i], codes[2 * i + 1], d, lo, hi);
+        put(4 * b + i, lo);
+        put(4 * b + 2 + i, hi);
+        if constexpr (kRest) {
+          pq_from_q4<true>(codes[2 * i], codes[2 * i + 1], d, lo, hi);
+          put(D / 8 + 4 * b + i, lo);
+          put(D / 8 + 4 * b + 2 + i, hi);
+        }
+      }
     }
   } else {
     // lanes take a row's 16-byte chunks in orders of their own, so that eight lanes' chunks fall
@@ -438,7 +466,7 @@ __device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned ch
 
 template <typename T, PqFormat F, int D>
 __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const __grid_constant__ PqParams p) {
-  using S = PqShape<F, D>;
+  using S = PqShape<T, F, D>;
   using Out = PwPack<T>;
   using P16 = PwPack<__half>;
   // The base of a row's running maximum moves only when that grows by more than kRescaleLog2, and it lies kTopLog2 -
@@ -449,21 +477,17 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   constexpr float kTopLog2 = 15.f, kRescaleLog2 = 8.f;
   constexpr int CB = S::kCB, NR = S::kRawStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  // 16-bit parts of P. One part, 2^-12 of a weight and rms half of that, is far below a bfloat16
-  // output's rounding. Beside a binary16 output's it is as much again, and so are together the roundings of
-  // q4_0's K and V: there P has a high part and a remainder (error against 64 bits 1.65 times the
-  // rounding's alone with one part, 1.3 with two; 1.4 over e4m3 pools, whose values are exact).
-  constexpr int kParts = !kBf16 && F == PqFormat::kQ4 ? 2 : 1;
+  constexpr int kParts = S::kParts, KS = S::kKStages;
   extern __shared__ __align__(1024) unsigned char sm[];
   // Every barrier's phases follow one another in the order of the work, and nobody who waits for
   // a phase can fall two behind. K and V tiles are counted through all parts of the CTA: tile m is in
-  // buffers m % 2.
+  // buffers m % KS and m % 2.
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
   uint64_t* raw_full = bars;             // [NR] a tile's bytes landed
   uint64_t* raw_empty = raw_full + NR;   // [NR] and were converted (an arrival per converting warp)
-  uint64_t* k_ready = raw_empty + NR;    // [2] a K tile is in place (likewise)
+  uint64_t* k_ready = raw_empty + NR;    // [KS] a K tile is in place (likewise)
   uint64_t* v_ready = k_ready + 2;       // [2] a V tile is
-  uint64_t* k_empty = k_ready + 4;       // [2] the MMAs are done with it (A's and B's: two arrivals)
+  uint64_t* k_empty = k_ready + 4;       // [KS] the MMAs are done with it (A's and B's: two arrivals)
   uint64_t* v_empty = k_ready + 6;       // [2] likewise
   uint64_t* s_full = k_ready + 8;        // [A, B] S computed
   uint64_t* p_full = k_ready + 10;       // [A, B] P written (one arrival per softmax warp)
@@ -549,11 +573,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     for (uint32_t n = 0; take(n, part); ++n) {
       const int end = part.end(), j0 = part.j0, j1 = part.j1;
       for (int i = 0; i < 2 * (j1 - j0) && !bad; ++i) {
-        // K0, K1, V0, K2, V1, ...
-        const bool is_v = i == 2 * (j1 - j0) - 1 || (i > 0 && (i & 1) == 0);
-        const int j = j0 + (is_v ? (i - 1) / 2 : (i + 1) / 2);
-        const uint32_t m = tiles + (j - j0), c = m & 1;
-        if (m >= 2 && !wait((is_v ? v_empty : k_empty) + c, ((m >> 1) + 1) & 1)) {
+        // K0, K1, V0, K2, V1, ...; with one buffer for K, where K1 must wait for S of K0, K0, V0, K1, V1, ...
+        const bool is_v = KS == 1 ? i & 1 : i == 2 * (j1 - j0) - 1 || (i > 0 && (i & 1) == 0);
+        const int j = j0 + (KS == 1 ? i / 2 : is_v ? (i - 1) / 2 : (i + 1) / 2);
+        const uint32_t m = tiles + (j - j0), ks = is_v ? 2 : KS, c = m % ks;
+        if (m >= ks && !wait((is_v ? v_empty : k_empty) + c, (m / ks + 1) & 1)) {
           bad = true;
           break;
         }
@@ -562,8 +586,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           break;
         }
         const bool held = j * 128 + r < end && ((held_blocks[stage] >> block) & 1u);
-        pq_convert<F, D>(sm + S::kRawOff + stage * S::kRaw + r * S::kRow,
-                         sm + S::kStageOff + (2 * c + is_v) * S::kTile, r, held);
+        const unsigned char* row = sm + S::kRawOff + stage * S::kRaw + r * S::kRow;
+        if (kParts == 2 && !is_v)
+          pq_convert<F, D, kParts == 2>(row, sm + S::kKOff + c * (kParts * S::kTile), r, held);
+        else
+          pq_convert<F, D, false>(row, sm + (is_v ? S::kVOff : S::kKOff) + c * S::kTile, r, held);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -639,14 +666,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           if (++stage == NR) stage = 0, phase ^= 1;
         };
         int id = fetch(j0), id_v = -2;
-        for (int j = j0; j <= j1 && j0 < j1 && !bad; ++j) {  // K of tile j, V of the one before
+        for (int j = j0; j <= j1 && j0 < j1 && !bad; ++j) {  // K of tile j, V of the one before (KS == 1: V too)
           if (id != -2 && (id < 0 || id >= p.num_blocks)) {
             set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
             id = -2;
           }
           const int id_next = fetch(j + 1);
           if (j < j1) copy(id, p.k_cache);
-          if (j > j0 && !bad) copy(id_v, p.v_cache);
+          if (KS == 1) id_v = id;
+          if ((KS == 1 ? j < j1 : j > j0) && !bad) copy(id_v, p.v_cache);
           id_v = id;
           id = id_next;
         }
@@ -670,8 +698,8 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       const uint32_t tb = __shfl_sync(kFullMask, tbase, 0);
       const uint32_t sb = __shfl_sync(kFullMask, smem_u32(sm), 0);
       // of a descriptor only the start address in its low word moves
-      const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kStageOff, 16, 1024);
-      const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kStageOff + S::kTile, S::kColBlock, 1024);
+      const uint32_t kd = (uint32_t)smem_desc_sw128(sb + S::kKOff, 16, 1024);
+      const uint32_t vd = (uint32_t)smem_desc_sw128(sb + S::kVOff, S::kColBlock, 1024);
       const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);  // K-major and MN-major alike
       uint32_t tiles = 0, done = 0, turns = 0;  // tiles of earlier parts; P's and steps in turn so far
       PqPart part;
@@ -685,10 +713,10 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
         for (int i = 0; i <= count && count > 0 && !bad; ++i) {  // O of tile i - 1, S of tile i
           const uint32_t mk = tiles + i, mv = mk - 1;
           const bool next = i < count && part.sees(x, part.j0 + i);
-          const uint32_t kb = __shfl_sync(kFullMask, kd + ((mk & 1) * (2 * S::kTile) >> 4), 0);
-          const uint32_t vb = __shfl_sync(kFullMask, vd + ((mv & 1) * (2 * S::kTile) >> 4), 0);
+          const uint32_t kb = __shfl_sync(kFullMask, kd + (mk % KS * (kParts * S::kTile) >> 4), 0);
+          const uint32_t vb = __shfl_sync(kFullMask, vd + ((mv & 1) * S::kTile >> 4), 0);
           // (the turn comes last, so that nothing but the issue lies between it and the other's)
-          if (i < count) bad = !wait(&k_ready[mk & 1], (mk >> 1) & 1);
+          if (i < count) bad = !wait(&k_ready[mk % KS], (mk / KS) & 1);
           // (a part's first P comes from warps that have read the O of the part before)
           if (!bad && seen) bad = !wait(&v_ready[mv & 1], (mv >> 1) & 1) || !wait(&p_full[x], done++ & 1);
           if (!bad && in_turn && (x == 1 || turns > 0)) bad = !wait(&turn[x], (turns + (x ^ 1)) & 1);
@@ -705,13 +733,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
             }
             if (next) {
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
-                pw_mma_ss(tb + 128 * x, qd + off, kb + off, hi, id_s, ks > 0);
-              }
+              for (int part16 = 0; part16 < kParts; ++part16)
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = ((ks >> 2) * S::kColBlock + (ks & 3) * 32) >> 4;
+                  pw_mma_ss(tb + 128 * x, qd + off, kb + (part16 * S::kTile >> 4) + off, hi, id_s, part16 > 0 || ks > 0);
+                }
               mma_commit(&s_full[x]);  // (the softmax gives K back)
             } else if (i < count) {
-              mbar_arrive(&k_empty[mk & 1]);
+              mbar_arrive(&k_empty[mk % KS]);
             }
             if (in_turn) mbar_arrive(&turn[x ^ 1]);
           }
@@ -855,7 +885,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
         for (int j = j0 + (dual ? x : 0); j < j1; j += step) {
           if (!bad && !wait(&s_full[x], done & 1)) bad = true;
           tc_fence_after();
-          if ((warp & 7) == 0 && lane == 0) mbar_arrive(&k_empty[(tiles + (j - j0)) & 1]);
+          if ((warp & 7) == 0 && lane == 0) mbar_arrive(&k_empty[(tiles + (j - j0)) % KS]);
           ++done;
           if (idle) {  // (its rows of P, and so of O, may hold anything)
             if (bad) break;
