@@ -690,6 +690,7 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
  * code, q and out of `dtype` (PKV_F16 or PKV_BF16). Arguments and errors as in
  * pkv_paged_attention_prefill, and
  *   k_scale, v_scale  finite and > 0 (with scale * k_scale * log2(e) finite in binary32)
+ *   out               must not overlap q (INVALID_ARG for the same address)
  *   max_query_len     a sequence with more new tokens sets
  *                     PKV_DEV_ERR_CONTEXT_LEN and is skipped
  *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whatever

@@ -53,7 +53,8 @@ _binding_module = None
 
 def _binding():
     """The Python extension of the later operators (bounded caches, rotating cache writes, prefill over
-    quantised caches), loaded when one of them is first called: nothing else needs it, and it is bound to the PyTorch that it was compiled against."""
+    quantised caches), loaded when one of them is first called: nothing else needs it, and it is bound to the
+    PyTorch that it was compiled against."""
     global _binding_module
     if _binding_module is None:
         made_for = _build.binding_for()

@@ -35,6 +35,7 @@ pkv_status prefill(void* out, const void* q, const void* k_cache, const void* v_
     return PKV_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < pkv::prefill_quant_workspace_bytes(head_dim)) return PKV_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return PKV_ERR_INVALID_ARG;
+  if (out == q) return PKV_ERR_INVALID_ARG;  // parts of a pair read its queries when others may have written outputs
   pkv::PrefillQuantParams p{};
   p.out = out;
   p.q = q;

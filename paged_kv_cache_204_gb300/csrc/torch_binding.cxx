@@ -1,7 +1,8 @@
 // Python extension: the bounded-cache entry points of pkv.h, the rotating cache
-// writes and prefill over quantised caches, called with torch tensors. Argument checks and marshalling only. A call from Python spends about
-// as long on reading ten tensors' attributes, one by one, as the smallest of these
-// operators on the GPU (15 us against 7); here that is about 1 us.
+// writes and prefill over quantised caches, called with torch tensors. Argument
+// checks and marshalling only. A call from Python spends about as long on reading
+// ten tensors' attributes, one by one, as the smallest of these operators on the
+// GPU (15 us against 7); here that is about 1 us.
 //
 // Every function takes its arguments by position, raises ValueError for a tensor
 // of the wrong type, shape, layout or device, and returns the pkv_status.
@@ -343,6 +344,8 @@ PyObject* prefill_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* need = "a contiguous [rows, num_heads, head_dim] tensor on the pools' device, out of q's type";
     const void* q = want(qt, "q", qt.scalar_type(), qt.sizes(), c.dev, need);
     void* out = want(ot, "out", qt.scalar_type(), qt.sizes(), c.dev, need);
+    const char *q0 = static_cast<const char*>(q), *o0 = static_cast<const char*>(out);
+    if (qt.nbytes() > 0 && q0 < o0 + ot.nbytes() && o0 < q0 + qt.nbytes()) refuse("out: must not overlap q");
     const int H = Pools::size(qt, 1), D = Pools::size(qt, 2);
     if (c.D != (q4 ? D / 16 * 9 : D))
       refuse_tensor(c.k, "k_cache", q4 ? "q4_0 rows of 9 head_dim / 16 bytes" : "e4m3 rows of head_dim bytes");

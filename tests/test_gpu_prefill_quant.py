@@ -345,6 +345,10 @@ def test_binding_refusals(pkv):
             pkv.paged_attention_prefill_q4_0(**{**good, name: bad})
     with pytest.raises(ValueError):  # e4m3 rows are head_dim bytes
         pkv.paged_attention_prefill_fp8(**{k: v for k, v in good.items()}, k_scale=1.0, v_scale=1.0)
+    both = torch.empty(15, b.H, 64, device=DEV, dtype=b.dtype)
+    for q, o in ((b.q, b.q), (both[:10], both[5:])):
+        with pytest.raises(ValueError, match="overlap"):
+            pkv.paged_attention_prefill_q4_0(**{**good, "q": q, "out": o})
     with pytest.raises(pkv.PkvError) as e:
         pkv.paged_attention_prefill_q4_0(**{**good, "workspace": ws[:100]})
     assert e.value.status == pkv.PKV_ERR_WORKSPACE

@@ -41,6 +41,8 @@ def test_refusals(pkv):
             assert rc(**bad) == UNS, bad
         need = pkv.prefill_workspace_bytes(128)
         assert rc() == WS and rc(ws=FAKE, ws_bytes=need - 1) == WS and rc(ws=FAKE + 8, ws_bytes=need) == INV
+        # queries are read by CTAs that come after others' outputs: no run in place
+        assert rc(ws=FAKE, ws_bytes=need, out=FAKE) == INV
     for bad in (dict(ks=0.0), dict(ks=-1.0), dict(vs=float("nan")), dict(vs=float("inf")), dict(scale=1e30, ks=1e30)):
         assert fp8(**bad) == INV, bad
 
