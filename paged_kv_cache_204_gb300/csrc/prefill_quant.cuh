@@ -31,7 +31,8 @@
 // tokens for 16 sequences of up to 32768 (q4_0): 173 us, 2.0 TB/s, there bound by the copying and the converting
 // warps (about 1100 cycles each for a tile's K or V). Tried and slower there and elsewhere: copies by the converting
 // warps (bulk: 586 us for the 8192 queries; 16 bytes a lane: 513), three times the converting warps where few have
-// rows (200 us for the drafted tokens), S in halves of 64 tokens, two of each A and B under way (560 us).
+// rows (200 us for the drafted tokens), twice as many with half a row to a thread (180, and 186 with a copying warp each for K
+// and V), S in halves of 64 tokens, two of each A and B under way (560 us).
 #pragma once
 
 #include <type_traits>
