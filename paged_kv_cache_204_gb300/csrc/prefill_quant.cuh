@@ -645,32 +645,31 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       for (uint32_t n = 0; take(n, part); ++n) {
         const int32_t* bt = p.block_tables + (size_t)part.s * p.max_blocks_per_seq;
         const int blocks = (part.end() + p.block_size - 1) >> p.block_bits, j0 = part.j0, j1 = part.j1;
-        auto fetch = [&](int j) {
-          const int b = j * per_tile + lane;
-          return j < j1 && lane < per_tile && b < blocks ? __ldg(bt + b) : -2;  // -2: none there
-        };
-        auto copy = [&](int b, const unsigned char* pool) {
+        // whether this lane has a block of tile j; what the table says there is checked when it has come
+        auto has = [&](int j) { return j < j1 && lane < per_tile && j * per_tile + lane < blocks; };
+        auto fetch = [&](int j) { return has(j) ? __ldg(bt + j * per_tile + lane) : -1; };
+        auto copy = [&](int b, const unsigned char* pool) {  // b: a block of the pool, below 0: none
           if (raw >= NR && !wait(&raw_empty[stage], phase)) {
             bad = true;
             return;
           }
-          const uint32_t some = __ballot_sync(kFullMask, b != -2);
+          const uint32_t some = __ballot_sync(kFullMask, b >= 0);
           if (lane == 0) {
             held_blocks[stage] = some;
             mbar_arrive_expect_tx(&raw_full[stage], __popc(some) * bytes);
           }
           __syncwarp();
-          if (b != -2)
+          if (b >= 0)
             bulk_copy_g2s(sm + S::kRawOff + stage * S::kRaw + lane * bytes,
                           pool + ((size_t)b * p.num_kv_heads + part.kvh) * bytes, bytes, &raw_full[stage]);
           ++raw;
           if (++stage == NR) stage = 0, phase ^= 1;
         };
-        int id = fetch(j0), id_v = -2;
+        int id = fetch(j0), id_v = -1;
         for (int j = j0; j <= j1 && j0 < j1 && !bad; ++j) {  // K of tile j, V of the one before (KS == 1: V too)
-          if (id != -2 && (id < 0 || id >= p.num_blocks)) {
-            set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
-            id = -2;
+          if (id < 0 || id >= p.num_blocks) {
+            if (has(j)) set_err(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+            id = -1;
           }
           const int id_next = fetch(j + 1);
           if (j < j1) copy(id, p.k_cache);

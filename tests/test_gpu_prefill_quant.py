@@ -353,3 +353,31 @@ def test_binding_refusals(pkv):
     with pytest.raises(pkv.PkvError) as e:
         pkv.paged_attention_prefill_q4_0(**{**good, "workspace": ws[:100]})
     assert e.value.status == pkv.PKV_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kind", ["q4", "fp8"])
+def test_every_negative_block_id_is_reported(pkv, kind):
+    """A visible entry of any negative value, in a sequence's first, middle and last tile and in a last block of one
+    token; entries that no query of the call sees may have any value."""
+    for dtype, D in (("bf16", 128), ("f16", 128), ("f16", 64)):
+        b = Batch([(400, 10), (50, 5), (257, 3)], 2, 2, D, 16, dtype, kind, seed=13)
+        for bad in (-2, -1, -3, -17, -(1 << 31), b.nb):
+            for s, at in ((0, 0), (0, 11), (0, 24), (1, 3), (2, 16)):
+                b.tables = torch.from_numpy(b.bt).to(DEV)
+                b.tables[s, at] = bad
+                b.tables[s, -(-b.lens[s] // 16):] = bad
+                err = new_err()
+                out = b.run(pkv, err=err)
+                assert err.item() == pkv.DEV_ERR_BLOCK_ID, (bad, s, at)
+                keep = b.k_rows[s], b.v_rows[s]
+                b.k_rows[s], b.v_rows[s] = keep[0].clone(), keep[1].clone()
+                b.k_rows[s][:, 16 * at:16 * at + 16] = 0  # its rows count as zeros
+                b.v_rows[s][:, 16 * at:16 * at + 16] = 0
+                b.check(out, (bad, s, at))
+                b.k_rows[s], b.v_rows[s] = keep
+        b.tables = torch.from_numpy(b.bt).to(DEV)
+        for s, L in enumerate(b.lens):
+            b.tables[s, -(-L // 16):] = -2
+        err = new_err()
+        b.check(b.run(pkv, err=err))
+        assert err.item() == 0
