@@ -715,10 +715,12 @@ pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void*
                                            pkv_dtype dtype, void* workspace, size_t workspace_bytes,
                                            int32_t* dev_err, pkv_stream_t stream);
 
-/* The same over q4_0 caches. K and V values d * (q - 8) are rounded to binary16
- * on the way (relative 2^-11, below 2^-14 absolute 2^-25; values beyond 65504,
- * which only rows of bfloat16 give, become infinite and count as such), but
- * with binary16 queries K enters exactly and probabilities to 2^-22. */
+/* The same over q4_0 caches. K and V values d * (q - 8) are rounded to 11
+ * significant bits on the way (relative 2^-11, below 2^-14 absolute 2^-25), but
+ * with binary16 queries K enters exactly and probabilities to 2^-22. Any finite d
+ * serves: values beyond 65504 (up to 8 * 65504: bfloat16 rows have them, and
+ * binary16 keys that were turned) are taken in binary32, with the queries that see
+ * them and others whose work lies beside theirs, a hundred times slower and more. */
 pkv_status pkv_paged_attention_prefill_q4_0(void* out, const void* q, const void* k_cache, const void* v_cache,
                                             const int32_t* block_tables, const int32_t* context_lens,
                                             const int32_t* query_start, float scale, int num_heads, int num_kv_heads,

@@ -83,7 +83,7 @@ cudaError_t launch(const PrefillQuantParams& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pa_prefill_quant_join_kernel<T, D>, p);
+  return cudaLaunchKernelEx(&cfg, pa_prefill_quant_join_kernel<T, F, D>, p);
 }
 
 template <PqFormat F>

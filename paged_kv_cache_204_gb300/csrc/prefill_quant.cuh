@@ -95,11 +95,13 @@ __device__ __forceinline__ bool pq_wait(uint64_t* bar, uint32_t parity, uint64_t
 // What a stretch is measured in: tokens x group, halved until the whole fits in 30 bits.
 using PqCost = int;
 
-// A pair that lies in more than one CTA, as the one that it starts in tells the joining kernel.
+// What a CTA tells the joining kernel: the pair that starts in it and goes on in others, and whether it has met rows
+// that it cannot do.
 struct alignas(16) PqCut {
   int last;  // CTA of its last part; below 0: no such pair
   int q0, kvh, row0, active;
-  int pad[3];
+  int wide;  // of the CTA: it has met a scale whose values exceed binary16's range
+  int pad[2];
 };
 
 struct PqParams {
@@ -366,6 +368,13 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
   return false;
 }
 
+// q4_0 values d (q - 8) go up to 8 * 65504, eight times what binary16 holds: bfloat16 rows have them, and keys of
+// binary16 once they were turned. The kernel goes on as if there were none; the converting warps note a scale of 8192 or
+// more in magnitude, and the joining kernel does these pairs again in 32 bits. (That note and the joining kernel's look at
+// it take 2 of the drafted tokens' 175 us. With a vote and a flag for each 32 rows, and MMAs that run eight times over
+// eighths of the values, it was 184; with such parts walked a second time in here, the 8 prompts took 131 to 142 us instead
+// of 124: longer code in all the roles.)
+
 // 8 bytes of codes as 16 values d (q - 8): low halves to lo, high halves to hi. A code placed
 // under the exponent of 1024 (low halves, last place 1) or of 64 (high halves, last place 1/16)
 // is a binary16 number that exceeds it by that constant. kRest: not the values, but what their rounding
@@ -402,9 +411,10 @@ __device__ __forceinline__ uint32_t pq_from_e4m3x2(uint32_t two) {
 }
 
 // Row r of a tile: its bytes at `row` become the operand's values (zeros where !held) in the swizzled tile
-// at `tile`. kRest: what the values' rounding leaves as well, in the tile behind it.
+// at `tile`. kRest: what the values' rounding leaves as well, in the tile behind it. large: the
+// largest magnitudes of the scales so far.
 template <PqFormat F, int D, bool kRest>
-__device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, bool held) {
+__device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned char* tile, int r, bool held, __half2& large) {
   unsigned char* at = tile + r * 128;
   const uint32_t swz = (r & 7) << 4;
   // values 8 c .. 8 c + 7 of the row
@@ -429,6 +439,12 @@ __device__ __forceinline__ void pq_convert(const unsigned char* row, unsigned ch
     } else {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[i];
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      __half2 d;
+      memcpy(&d, &w[i], 4);
+      large = __hmax2(large, __habs2(d));
     }
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) {
@@ -570,6 +586,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
     uint32_t tiles = 0;  // of earlier parts
     int stage = 0;
     uint32_t phase = 0;
+    __half2 large = __half2half2(__ushort_as_half(0));
     PqPart part;
     for (uint32_t n = 0; take(n, part); ++n) {
       const int end = part.end(), j0 = part.j0, j1 = part.j1;
@@ -589,9 +606,9 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
         const bool held = j * 128 + r < end && ((held_blocks[stage] >> block) & 1u);
         const unsigned char* row = sm + S::kRawOff + stage * S::kRaw + r * S::kRow;
         if (kParts == 2 && !is_v)
-          pq_convert<F, D, kParts == 2>(row, sm + S::kKOff + c * (kParts * S::kTile), r, held);
+          pq_convert<F, D, kParts == 2>(row, sm + S::kKOff + c * (kParts * S::kTile), r, held, large);
         else
-          pq_convert<F, D, false>(row, sm + (is_v ? S::kVOff : S::kKOff) + c * S::kTile, r, held);
+          pq_convert<F, D, false>(row, sm + (is_v ? S::kVOff : S::kKOff) + c * S::kTile, r, held, large);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -602,13 +619,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
       }
       tiles += j1 - j0;
     }
+    if (F == PqFormat::kQ4 && __any_sync(kFullMask, fmaxf(__low2float(large), __high2float(large)) >= 8192.f) && lane == 0)
+      p.cuts[blockIdx.x].wide = 1;
     if (bad && lane == 0) set_err(p.dev_err, PKV_DEV_ERR_TIMEOUT);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqIssueRegs));
     if (warp == 18) {
       // ---- the walk
       PqWalk walk;
-      if (lane == 0) p.cuts[blockIdx.x].last = -1;
+      if (lane == 0) p.cuts[blockIdx.x].last = -1, p.cuts[blockIdx.x].wide = 0;  // (before any part is told)
       const bool any = pq_begin(p, walk);
       for (uint32_t n = 0;; ++n) {
         if (n >= kPqRing && !wait(&part_empty[n % kPqRing], (n / kPqRing + 1) & 1)) {
@@ -1120,15 +1139,116 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
   }
 }
 
+// Row `row` of a pair over q4_0 in 32 bits, by a warp: a token to a lane for the scores, D / 32 dims to a lane for
+// the output. qs: room for the query row.
+template <typename T, int D>
+__device__ __forceinline__ void pq_wide_row(const PqParams& p, const PqPart& part, int row, float* qs) {
+  constexpr int E = D / 32, kHalf = 16 / E, kRow = D / 16 * 9;  // values to a lane, lanes to a block's halves
+  const int lane = threadIdx.x & 31, G = p.group;
+  const int g = part.row0 + row, t = p.by_group.of(g), pos = part.base + t;
+  const size_t at = ((size_t)(part.q0 + t) * p.num_heads + part.kvh * G + (g - t * G)) * D;
+  const float factor = p.zero_scale ? 0.f : (p.flip != 0u ? -p.scale_log2 : p.scale_log2);
+  for (int i = lane; i < D; i += 32) qs[i] = factor * static_cast<float>(static_cast<const T*>(p.q)[at + i]);
+  __syncwarp();
+  const int32_t* bt = p.block_tables + (size_t)part.s * p.max_blocks_per_seq;
+  const int block = lane / (2 * kHalf), upper = lane / kHalf & 1;  // this lane's dims: E of half a block
+  const int byte0 = D / 16 + 16 * block + E * (lane % kHalf);
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int t0 = 0; t0 <= pos; t0 += 32) {
+    const int tok = t0 + lane;
+    long long from = -1;  // this lane's row; a bad block's rows are zeros
+    if (tok <= pos) {
+      const int b = __ldg(bt + (tok >> p.block_bits));
+      if (b >= 0 && b < p.num_blocks)
+        from = (((long long)b * p.num_kv_heads + part.kvh) * p.block_size + (tok & (p.block_size - 1))) * kRow;
+    }
+    float x = tok <= pos ? 0.f : -INFINITY;
+    if (from >= 0) {
+      const unsigned char* k = p.k_cache + from;
+#pragma unroll 1
+      for (int b = 0; b < D / 32; ++b) {
+        float sum = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int code = k[D / 16 + 16 * b + i];
+          sum = fmaf(qs[32 * b + i], (float)((code & 15) - 8), sum);
+          sum = fmaf(qs[32 * b + 16 + i], (float)((code >> 4) - 8), sum);
+        }
+        x = fmaf(sum, __half2float(reinterpret_cast<const __half*>(k)[b]), x);
+      }
+    }
+    float top = x;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, i));
+    top = fmaxf(top, m);
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m - base), w = exp2f(x - base);
+    m = top;
+    float total = w;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(kFullMask, total, i);
+    l = fmaf(l, keep, total);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+    const int count = min(32, pos - t0 + 1);
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const long long row_at = __shfl_sync(kFullMask, from, i);
+      const float wi = __shfl_sync(kFullMask, w, i);
+      if (row_at < 0) continue;
+      const unsigned char* v = p.v_cache + row_at;
+      const float wd = wi * __half2float(reinterpret_cast<const __half*>(v)[block]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(wd, (float)((v[byte0 + e] >> (4 * upper) & 15) - 8), o[e]);
+    }
+  }
+  const float inv = p.v_scale / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at + 32 * block + 16 * upper + E * (lane % kHalf));
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = PwPack<T>::pack(o[e] * inv, o[e + 1] * inv);
+  __syncwarp();
+}
+
+// The pairs that start in this CTA's stretch and meet rows with values beyond binary16, whole or cut: all of their
+// rows again, 32 to a CTA of the join. (8192 queries of 32 heads with such keys throughout: 184 ms instead of 0.48; a
+// prompt of 1500 tokens, 10 heads of 64: 3.2 ms instead of 0.03.)
+template <typename T, int D>
+__device__ __noinline__ void pq_wide(const PqParams& p, float* qs) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PqWalk walk;
+  if (!pq_begin(p, walk)) return;
+  for (; !walk.done(); walk.next(p)) {
+    PqPart part;
+    if (!walk.part(p, part) || !(part.whole() || (part.kind & PqPart::kHead))) continue;
+    bool wide = false;
+    for (int c = blockIdx.x + lane; c <= part.last; c += 32) wide |= __ldcg(&p.cuts[c].wide) != 0;
+    if (!__any_sync(kFullMask, wide)) continue;
+#pragma unroll 1
+    for (int row = blockIdx.y * 32 + warp; row < min(blockIdx.y * 32 + 32, part.active); row += 2 * D / 32)
+      pq_wide_row<T, D>(p, part, row, qs + warp * D);
+  }
+}
+
 // The cut pairs' parts joined: grid = (CTA that a pair starts in, 32 rows of it), 16 head dims to a warp, a row to
 // a lane; the parts come four at a time, so that their loads are under way together.
-template <typename T, int D>
+template <typename T, PqFormat F, int D>
 __global__ void __launch_bounds__(2 * D) pa_prefill_quant_join_kernel(const __grid_constant__ PqParams p) {
   grid_dependency_wait();
   const int c0 = blockIdx.x;
   const int4 told = __ldcg(reinterpret_cast<const int4*>(p.cuts + c0));  // last, q0, kvh, row0
   const int active = __ldcg(&p.cuts[c0].active);
   const int c1 = told.x;
+  if constexpr (F == PqFormat::kQ4) {
+    __shared__ float qs[2 * D / 32 * D];
+    bool wide = false;
+    for (int c = c0 + (threadIdx.x & 31); c <= max(c0, c1); c += 32) wide |= __ldcg(&p.cuts[c].wide) != 0;
+    if (__any_sync(kFullMask, wide)) {
+      pq_wide<T, D>(p, qs);
+      return;
+    }
+  }
   if (c1 < 0) return;
   const int row = blockIdx.y * 32 + (threadIdx.x & 31), k0 = threadIdx.x >> 5;
   if (row >= active) return;
