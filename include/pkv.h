@@ -634,8 +634,9 @@ pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, const float* scores, i
  *                 least a token's rows) leads from token to token, so that parts
  *                 of one projection's output serve as they are. q_out is q (same
  *                 address and stride), or a range (first to last row) that has
- *                 no byte in common with it; q_out must not meet k and v, nor
- *                 the caches anything.
+ *                 no byte in common with it; q_out's rows must have no byte in common
+ *                 with k's and v's, nor its range with the caches' (all this
+ *                 is checked), nor the caches with anything else.
  *   positions     int32 [num_axes][num_tokens]
  *   cos_sin       float [max_position][rotary_dim]: R / 2 cosines, then R / 2
  *                 sines of each position, 16-byte aligned

@@ -12,12 +12,36 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool valid_scale(float s) { return std::isfinite(s) && s > 0.f; }
 
-// First to last byte of a step's rows.
-struct Range {
+// A step's rows in bytes, one to a token, no two of which overlap; begin, end: the first byte and behind the last.
+struct Rows {
   uintptr_t begin, end;
-  Range(const void* p, int64_t stride, int64_t row, int tokens)
-      : begin(reinterpret_cast<uintptr_t>(p)), end(begin + (uintptr_t)((tokens - 1) * stride + row)) {}
-  bool meets(const Range& o) const { return begin < o.end && o.begin < end; }
+  int64_t stride, row;
+  int tokens;
+  Rows(const void* p, int64_t stride_, int64_t row_, int tokens_)
+      : begin(reinterpret_cast<uintptr_t>(p)), end(begin + (uintptr_t)((tokens_ - 1) * stride_ + row_)), stride(stride_),
+        row(row_), tokens(tokens_) {}
+  bool range_meets(const Rows& o) const { return begin < o.end && o.begin < end; }
+  // A row here has a byte in common with one of o's: parts of one projection lie between one another without that.
+  bool meets(const Rows& o) const {
+    if (!range_meets(o)) return false;
+    if (stride == o.stride) {  // o's row i + d begins d strides behind its row i: some d with -o.row < x < row, x = o - this
+      const int64_t x = (int64_t)(o.begin - begin);
+      const int64_t low = -o.row - x;  // d * stride has to lie above, and below row - x
+      int64_t d = low >= 0 ? low / stride + 1 : -(-low / stride) + (-low % stride == 0 ? 1 : 0);
+      if (d < 1 - tokens) d = 1 - tokens;
+      return d < tokens && d * stride < row - x;
+    }
+    for (int i = 0, j = 0; i < tokens && j < o.tokens;) {
+      const uintptr_t a = begin + (uintptr_t)(i * stride), b = o.begin + (uintptr_t)(j * o.stride);
+      if (a + (uintptr_t)row <= b)
+        ++i;
+      else if (b + (uintptr_t)o.row <= a)
+        ++j;
+      else
+        return true;
+    }
+    return false;
+  }
 };
 
 pkv_status rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -61,9 +85,17 @@ pkv_status rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stri
   }
   // in place (the very rows), or no byte in common
   const bool in_place = q_out == q && q_out_stride == q_stride;
-  if (!in_place && Range(q_out, q_out_stride * es, q_row * es, num_tokens)
-                       .meets(Range(q, q_stride * es, q_row * es, num_tokens)))
+  const Rows out(q_out, q_out_stride * es, q_row * es, num_tokens);
+  if (!in_place && out.range_meets(Rows(q, q_stride * es, q_row * es, num_tokens))) return PKV_ERR_INVALID_ARG;
+  if (out.meets(Rows(k, k_stride * es, kv_row * es, num_tokens)) ||
+      out.meets(Rows(v, v_stride * es, kv_row * es, num_tokens)))
     return PKV_ERR_INVALID_ARG;
+  const int64_t cache_row = cache == pkv::RopeCache::kSame ? head_dim * es
+                                                           : (cache == pkv::RopeCache::kFp8 ? head_dim : head_dim / 16 * 9);
+  for (const void* pool : {k_cache, v_cache}) {
+    const Rows whole(pool, 0, (int64_t)num_blocks * num_kv_heads * block_size * cache_row, 1);
+    if (out.range_meets(whole)) return PKV_ERR_INVALID_ARG;
+  }
   p.q_out = q_out;
   p.q = q;
   p.k = k;

@@ -320,3 +320,44 @@ def test_binding_refusals(pkv):
     for cache in (pkv.rope_and_cache_q4_0, lambda **a: pkv.rope_and_cache_fp8(**a, k_scale=1.0, v_scale=1.0)):
         with pytest.raises(ValueError):
             cache(**good)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("f16", "fp8"), ("bf16", "q4"), ("f32", "same")])
+def test_rows_of_one_buffer(pkv, dtype, cache):
+    """Outputs, keys and values anywhere in one buffer, with strides of their own: refused where a byte of an output
+    would lie on a key's or a value's, and else as from tensors of their own."""
+    T, H, G, D = 7, 3, 1, 64
+    rng = np.random.default_rng(8)
+    done = {True: 0, False: 0}
+    chunk = 16 // TD[dtype].itemsize
+    for i in range(100):
+        s = Step(pkv, T, H, G, D, 8, dtype, cache, packed=False, seed=i)
+        want = s.expected()
+        k, v = s.k.clone(), s.v.clone()
+        buf = torch.zeros(40 * T * D, device=DEV, dtype=s.dtype)
+        used, views = [], []
+        same = int(rng.integers(H + 2 * G, H + 2 * G + 4)) * D
+        for heads in (H, G, G):  # one stride for all, whole heads apart or any chunks, or strides of their own
+            stride = same if i % 2 else heads * D + int(rng.integers(0, 20)) * chunk
+            if i % 4 == 1:
+                at = int(rng.integers(0, 2 * same // D)) * D
+            else:
+                at = int(rng.integers(0, (2 * same if i % 4 == 3 else 30 * T * D) // chunk)) * chunk
+            views.append(buf.as_strided((T, heads, D), (stride, D, 1), at))
+            used.append({at + t * stride + e for t in range(T) for e in range(heads * D)})
+        views[1].copy_(k)
+        views[2].copy_(v)
+        if used[1] & used[2] and not (used[0] & (used[1] | used[2])):
+            continue  # (keys and values may share memory, but these have not both their values then)
+        s.k, s.v = views[1], views[2]
+        meet = bool(used[0] & (used[1] | used[2]))
+        done[meet] += 1
+        if meet:
+            with pytest.raises(pkv.PkvError) as e:
+                s.run(q_out=views[0])
+            assert e.value.status == pkv.PKV_ERR_INVALID_ARG
+        else:
+            views[0].fill_(float("nan"))
+            s.run(q_out=views[0])
+            s.check(want, views[0])
+    assert min(done.values()) >= 10, done
