@@ -7,7 +7,7 @@ namespace pkv {
 
 namespace {
 
-size_t cut_bytes() { return sizeof(PqCut) * 2 * kPqMaxCtas; }
+size_t cut_bytes() { return sizeof(PqCut) * kPqMaxCtas; }
 size_t ml_bytes() { return sizeof(float2) * 2 * kPqMaxCtas * 256; }
 
 template <typename T, PqFormat F, int D>

@@ -930,8 +930,8 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
               m4[i / 2 & 3] = pw_max3(m4[i / 2 & 3], __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
           }
           float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          // the base moves only when the maximum grows by more than kTopLog2: every P stays below 2^kTopLog2,
-          // and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
+          // the base moves only when the maximum exceeds it by more than kTopLog2, that is, has grown by more than
+          // kRescaleLog2 since: every P stays below 2^kTopLog2, and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
           // a base may be off by half their distance: there it is the maximum and moves whenever that does.)
           const float most = fabsf(m_use) < kPwFar ? kTopLog2 : 0.f;
           // (the difference is not a number, and no growth, for -inf - -inf)

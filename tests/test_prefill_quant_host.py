@@ -60,3 +60,10 @@ def test_binding_wants_cuda_tensors(pkv):
         pkv.paged_attention_prefill_fp8(q, q, pool, pool, t, n, t, 1.0, 1.0, 1.0, 1, pool)
     with pytest.raises(ValueError, match="CUDA"):
         pkv.paged_attention_prefill_q4_0(q, q, pool, pool, t, n, t, 1.0, 1, pool)
+
+
+def test_workspace_holds_what_is_used(pkv):
+    """Of 152 CTAs: what each tells the join (32 bytes), and two places for 256 rows' maxima, sums and outputs in 32
+    bits. Nothing beside that."""
+    for D in (64, 128):
+        assert pkv.prefill_workspace_bytes(D) == 152 * (32 + 2 * 256 * (8 + 4 * D))
