@@ -381,3 +381,26 @@ def test_every_negative_block_id_is_reported(pkv, kind):
         err = new_err()
         b.check(b.run(pkv, err=err))
         assert err.item() == 0
+
+
+@pytest.mark.parametrize("kind,dtype", [("q4", "f16"), ("fp8", "bf16")])
+@pytest.mark.parametrize("seqs", [[(16384, 16384)], [(16384, 16000), (1, 1), (16000, 3), (9000, 9000)]], ids=["one", "four"])
+def test_costs_beyond_30_bits(pkv, kind, dtype, seqs):
+    """Batches of more than 2^30 in tokens of walks x query heads of a kv head, whose stretches are measured in coarser steps:
+    every row is written, and rows at borders of pairs and all over the walk hold what they should."""
+    b = Batch(seqs, 1, 64, 64, 16, dtype, kind, seed=15)
+    err = new_err()
+    out = b.run(pkv, err=err)
+    assert err.item() == 0
+    rng = np.random.default_rng(16)
+    for s, (L, n) in enumerate(b.seqs):
+        for a in range(b.first[s], b.first[s + 1], 1024):
+            assert torch.isfinite(out[a:min(a + 1024, b.first[s + 1])]).all()
+        # a pair is 4 queries
+        at = {0, n - 1} | {int(i) // 4 * 4 + d for i in rng.integers(4, max(n - 4, 5), 40) for d in (-1, 0)}
+        # where the 152 stretches of one long prompt end, each of the same area
+        at |= {int(n * (c / 152) ** 0.5) for c in range(0, 153, 8)}
+        for i in sorted(i for i in at if 0 <= i < n):
+            want, tol = b.exact(s, i, i + 1)
+            got = out[b.first[s] + i:b.first[s] + i + 1].double()
+            assert ((got - want).abs() <= tol).all(), (s, i)
