@@ -694,6 +694,8 @@ pkv_status pkv_rope_and_cache_q4_0(void* q_out, int64_t q_out_stride, const void
  *   out               must not overlap q (INVALID_ARG for the same address)
  *   max_query_len     a sequence with more new tokens sets
  *                     PKV_DEV_ERR_CONTEXT_LEN and is skipped
+ *   query_start       a sequence with queries outside [0, query_start[num_seqs])
+ *                     sets PKV_DEV_ERR_CONTEXT_LEN and is skipped
  *   workspace         at least pkv_prefill_workspace_bytes(head_dim) bytes, whatever
  *                     they hold. One workspace serves calls of any sizes, of both
  *                     operators. Two calls that share a workspace must not

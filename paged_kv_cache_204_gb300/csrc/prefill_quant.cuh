@@ -170,8 +170,10 @@ struct PqSeq {
   __device__ __forceinline__ void load(const PqParams& p, int s) {
     L = __ldg(p.context_lens + s);
     q0 = __ldg(p.query_start + s);
-    n = __ldg(p.query_start + s + 1) - q0;
-    valid = L >= 0 && L <= p.max_blocks_per_seq * p.block_size && n >= 0 && n <= L && n <= p.max_query_len;
+    n = (int)((uint32_t)__ldg(p.query_start + s + 1) - (uint32_t)q0);
+    // (rows outside q and out, which have query_start[num_seqs] of them, are never touched)
+    const bool inside = q0 >= 0 && (uint32_t)q0 + (uint32_t)n <= (uint32_t)max(__ldg(p.query_start + p.num_seqs), 0);
+    valid = L >= 0 && L <= p.max_blocks_per_seq * p.block_size && n >= 0 && n <= L && n <= p.max_query_len && inside;
     live = valid && n > 0;
   }
   __device__ __forceinline__ int pairs(int group) const { return (int)(((int64_t)n * group + 255) / 256); }

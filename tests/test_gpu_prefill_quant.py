@@ -404,3 +404,29 @@ def test_costs_beyond_30_bits(pkv, kind, dtype, seqs):
             want, tol = b.exact(s, i, i + 1)
             got = out[b.first[s] + i:b.first[s] + i + 1].double()
             assert ((got - want).abs() <= tol).all(), (s, i)
+
+
+@pytest.mark.parametrize("kind", ["q4", "fp8"])
+def test_queries_outside_the_batch(pkv, kind):
+    """query_start that begins below 0, or goes beyond its last entry: the sequences whose rows would lie outside are
+    left out and reported, the others are done."""
+    b = Batch([(100, 10), (50, 5), (200, 20), (60, 6)], 2, 2, 128, 16, "bf16", kind, seed=14)
+    good, err, starts = b.run(pkv), new_err(), b.starts.clone()
+    room = torch.full((b.q.shape[0] + 64, b.H, b.D), 7.0, device=DEV, dtype=b.dtype)
+    out = room[32:-32]
+    for bad, done in (([-3, 10, 15, 35, 41], [1, 2, 3]), ([0, 10, 15, 35, 30], [0, 1]), ([0, 10, 15, 35, 14], [0]),
+                      ([-(1 << 31), 10, 15, 35, 41], [1, 2, 3]), ([0, 10, 15, 35, -1], []), ([0, 10, 15, 35, -(1 << 31)], [])):
+        b.starts = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        room.fill_(7.0)
+        err.zero_()
+        b.run(pkv, err=err, out=out, max_new=40)
+        assert err.item() == pkv.DEV_ERR_CONTEXT_LEN
+        for s in range(4):
+            rows = slice(int(starts[s]), int(starts[s + 1]))
+            if s in done:
+                b.check(out, bad, [s])
+            else:
+                assert (out[rows] == 7).all(), (bad, s)
+        assert (room[:32] == 7).all() and (room[-32:] == 7).all()
+    b.starts = starts
+    assert torch.equal(b.run(pkv), good)
