@@ -146,3 +146,45 @@ def test_infinite_scales(pkv):
             want, tol = b.exact(0, 0, 50)  # positions 100 .. 149
             assert torch.isfinite(out[:50]).all() and ((out[:50].double() - want).abs() <= tol).all()
             assert not torch.isfinite(out[50:]).all(-1).any()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 2.0 ** -103])
+def test_wide_rows_with_other_scales_and_bad_blocks(pkv, scale):
+    """Negative scales, equal weights, bfloat16 queries beyond binary16; a bad block among the wide ones, whose rows
+    count as zeros."""
+    for dtype, D in (("bf16", 128), ("bf16", 64), ("f16", 128)):
+        if dtype == "f16" and scale == 2.0 ** -103:
+            continue
+        b = Wide([(300, 70), (900, 5), (1, 1)], 2, 3, D, 16, dtype, seed=5, v_tokens=None if dtype == "bf16" else (),
+                 q_sigma=2.0 ** (84 if scale == 2.0 ** -103 else -17), scale=scale)
+        assert torch.isfinite(b.q).all()
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        b.check(b.run(pkv, err=err), (dtype, D))
+        assert err.item() == 0
+        b.tables[0, 5] = -2
+        b.tables[1, 40] = b.nb
+        for s, at in ((0, 5), (1, 40)):
+            for rows in (b.k_rows, b.v_rows):
+                rows[s] = rows[s].clone()
+                rows[s][:, 16 * at:16 * at + 16] = 0
+        b.check(b.run(pkv, err=err), (dtype, D, "bad"))
+        assert err.item() == pkv.DEV_ERR_BLOCK_ID
+
+
+def test_wide_rows_in_a_replayed_graph(pkv):
+    """A graph whose pool gets wide rows, and loses them, between replays."""
+    b = Wide([(700, 300), (3000, 9)], 2, 4, 128, 16, "bf16", seed=6, k_tokens=(), v_tokens=(), q_sigma=2.0 ** -17)
+    wide = Wide(b.seqs, 2, 4, 128, 16, "bf16", seed=6, v_tokens=(), q_sigma=2.0 ** -17)
+    ws, out, plain = pkv.new_prefill_workspace(128), torch.empty_like(b.q), b.k.clone()
+    b.run(pkv, ws=ws, out=out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.run(pkv, ws=ws, out=out)
+    small = b.k_rows
+    for pool, rows in ((plain, small), (wide.k, wide.k_rows), (plain, small), (wide.k, wide.k_rows)):
+        b.k.copy_(pool)
+        b.k_rows = rows
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        b.check(out)
