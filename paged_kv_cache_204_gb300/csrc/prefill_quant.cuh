@@ -22,17 +22,18 @@
 // joins (log-sum-exp), 32 rows to a CTA. (The last CTA of a pair as the joiner took 13 us of 51 for the
 // chunk below: one SM read 1.3 MB.)
 //
-// Bound by the way from S over the softmax back to the MMAs: a K/V tile takes A and B about 4300 cycles,
+// Bound by the way from S over the softmax back to the MMAs: at head_dim 128 a K/V tile takes A and B about 4300 cycles,
 // of which the MMAs are 2048; A's S, softmax (about 1900) and O follow one another, and B's only half hide
-// them, tensor memory having no room for a second S of either. 8192 queries over q4_0 (32 query, 8 kv heads, head_dim
-// 128, bfloat16): about 470 us, 1170 TFLOP/s over the visible tokens, where the same heads over 16-bit pools take the
-// window prefill 513 us; 1024 queries of 4 sequences of up to 6001 tokens over e4m3 (64 query heads): 300 us; 8 prompts
-// of up to 1500 tokens over q4_0 (40 heads of 64, binary16): 123 us; one chunk of 100 queries behind 2677 tokens: 31 us; 5 drafted
-// tokens for 16 sequences of up to 32768 (q4_0): 173 us, 2.0 TB/s, there bound by the copying and the converting
-// warps (about 1100 cycles each for a tile's K or V). Tried and slower there and elsewhere: copies by the converting
-// warps (bulk: 586 us for the 8192 queries; 16 bytes a lane: 513), three times the converting warps where few have
-// rows (200 us for the drafted tokens), twice as many with half a row to a thread (180, and 186 with a copying warp each for K
-// and V), S in halves of 64 tokens, two of each A and B under way (560 us).
+// them, tensor memory having no room for a second S of either (at 64 it has 128 columns that are not used). 8192 queries
+// over q4_0 (32 query, 8 kv heads, head_dim 128, bfloat16): 482 us, 1140 TFLOP/s over the visible tokens, where the same
+// heads over 16-bit pools take the window prefill 513 us; 1024 queries of 4 sequences of up to 6001 tokens over e4m3 (64
+// query heads): 298 us; 8 prompts of up to 1500 tokens over q4_0 (40 heads of 64, binary16): 121 us; one chunk of 100
+// queries behind 2677 tokens: 31 us; 5 drafted tokens for 16 sequences of up to 32768: 176 us over q4_0, 2.0 TB/s, 221
+// over e4m3, there bound by the copying and the converting warps (about 1100 and 1500 cycles each for a tile's K or V).
+// Tried and slower there and elsewhere, when the 8192 queries took 516 us and the drafted tokens 173 to 186: copies by the
+// converting warps (bulk: 586 us for the 8192 queries; 16 bytes a lane: 513), three times the converting warps where few
+// have rows (200 us for the drafted tokens), twice as many with half a row to a thread (180, and 186 with a copying warp
+// each for K and V), S in halves of 64 tokens, two of each A and B under way (560 us).
 #pragma once
 
 #include <type_traits>
@@ -52,8 +53,9 @@ constexpr int kPqMaxCtas = 152;
 constexpr int kPqLaunchRegs = 80, kPqSoftRegs = 88, kPqIssueRegs = 56, kPqConvertRegs = 72;
 static_assert(4 * kPqSoftRegs + kPqIssueRegs + kPqConvertRegs <= kPqThreads / 128 * kPqLaunchRegs, "no more than the launch has");
 // A pair's start and end, as tokens of its walk. Head_dim 128: 522 us with 256, 466 with 512, 484 with 1024 (8192
-// queries over q4_0, 32 query and 8 kv heads); head_dim 64, where a tile takes less: 109 with 256, 108 with 384, 116 with
-// 512 (8 prompts of up to 1500 tokens, 40 heads).
+// queries over q4_0, 32 query and 8 kv heads, which took 16 us less before rows were read whole); head_dim 64, where a tile
+// takes less: 109 with 256, 108 with 384, 116 with 512 (8 prompts of up to 1500 tokens, 40 heads, K in one part). Not
+// swept over e4m3.
 constexpr int pq_start(int head_dim) { return head_dim == 64 ? 384 : 512; }
 // A CTA's stretch is no shorter: one chunk of 100 queries behind 2677 tokens takes 31 us (35 with 1024, 50 with 2048; 128
 // to 384 give the same).
@@ -128,9 +130,10 @@ struct PqParams {
 enum class PqFormat { kQ4, kFp8 };
 
 // Binary16 queries over q4_0: P and K enter in two 16-bit parts, a value rounded and what that leaves, since one
-// rounding of either is as much as an output's own. It costs 3 to 17 % at head_dim 64 (the 8 prompts: 123 us instead of
-// 106) and, with room for one tile of K only, up to 40 % at 128 (16 sequences of 40 queries behind up to 2600 tokens, 64
-// heads: 124 us instead of 89). Error against 64 bits over that of the output's rounding alone,
+// rounding of either is as much as an output's own. K's second part costs 3 to 17 % at head_dim 64 (the 8 prompts: 123 us
+// instead of 106). At 128 there is room for one tile of K only, and both second parts together cost 63 to 103 % (16
+// sequences of 40 queries behind 300 to 2600 tokens, 64 heads: 111 us instead of 68; the 8192 queries: 915 instead of 470;
+// the drafted tokens: 350 instead of 173). Error against 64 bits over that of the output's rounding alone,
 // standard normal rows: 1.6 to 1.9 with one part of both, 1.5 to 1.6 with one of K (2.0 with logits of twice the
 // spread, since K's roundings grow with them), 1.3 with two of both. e4m3 values are exact (1.4 with one part of P), and a
 // bfloat16 output's rounding is 8 times as large.

@@ -12,9 +12,10 @@
 // thread and the run's cosines and sines stay in registers for every row that the thread takes.
 //
 // Bound by HBM: every row is read once and written once. 8192 tokens of 32 heads (8 kv, head_dim 128, bfloat16)
-// take 32.8 us, 6.27 TB/s; into e4m3 36.1 us (the divisions), into q4_0 37.9 us (the blocks' maxima and codes);
-// 4099 tokens of 40 heads of 64 with three axes 25.1 us, 5.06 TB/s; 128 tokens of 40 heads 2.7 us, one token
-// 1.8 us: a launch.
+// take 32.6 us, 6.30 TB/s; into e4m3 35.7 us (the divisions: 1.3 times the instructions), into q4_0 37.2 us (the blocks'
+// maxima and codes: 1.5 times, issue slots 62 % busy); 4099 tokens of 40 heads of 64 21.5 us, 5.92 TB/s, and 24.7 us with
+// three axes (a CTA waits for a position, then for its table row, and has one short token to do it for); 128 tokens of 40
+// heads 2.7 us, one token 1.8 us: a launch.
 #include "common.cuh"
 #include "rope_cache.h"
 

@@ -46,3 +46,19 @@ def test_output_on_caches(pkv):
             size = 10 * 2 * 16 * row
             for at in (1 * MB, 1 * MB + 4 * 2048 - 16, 1 * MB - size + 16):
                 assert call(**apart(**{name: at})) == pkv.PKV_ERR_INVALID_ARG, (name, at)
+
+
+def test_refusals_with_everything_apart(pkv):
+    """The refusals of single arguments, from a call in which nothing else stands against it."""
+    INV, UNS = pkv.PKV_ERR_INVALID_ARG, pkv.PKV_ERR_UNSUPPORTED
+    for call in calls(pkv):
+        for bad in (dict(T=-1), dict(H=0), dict(G=0), dict(H=9), dict(bs=0), dict(nb=0), dict(most=0), dict(R=0), dict(axes=2),
+                    dict(out=1 * MB + 8), dict(q=2 * MB + 2), dict(k=3 * MB + 8), dict(v=4 * MB + 4), dict(kc=5 * MB + 8),
+                    dict(vc=6 * MB + 8), dict(slots=7 * MB + 4), dict(pos=8 * MB + 2), dict(table=9 * MB + 4), dict(err=MB + 1),
+                    dict(so=8 * 128 - 8), dict(sq=8 * 128 + 4), dict(sk=2 * 128 - 8), dict(sv=2 * 128 + 1), dict(sq=1 << 62),
+                    dict(axis=bytes([0] * 63 + [1])), dict(axes=3, axis=bytes([3] + [0] * 63)), dict(q=1 * MB, sq=8 * 128 + 8),
+                    dict(q=1 * MB + 2048), dict(q=1 * MB - 4 * 2048 + 16),
+                    *({name: None} for name in ("out", "q", "k", "v", "kc", "vc", "slots", "pos", "table"))):
+            assert call(**apart(**bad)) == INV, bad
+        for bad in (dict(D=96, R=96), dict(bs=64), dict(dtype=3), dict(R=72), dict(R=144), dict(axes=5, axis=bytes(64))):
+            assert call(**apart(**bad)) == UNS, bad
