@@ -24,10 +24,9 @@ struct Rows {
   // A row here has a byte in common with one of o's: parts of one projection lie between one another without that.
   bool meets(const Rows& o) const {
     if (!range_meets(o)) return false;
-    if (stride == o.stride) {  // o's row i + d begins d strides behind its row i: some d with -o.row < x < row, x = o - this
-      const int64_t x = (int64_t)(o.begin - begin);
-      const int64_t low = -o.row - x;  // d * stride has to lie above, and below row - x
-      int64_t d = low >= 0 ? low / stride + 1 : -(-low / stride) + (-low % stride == 0 ? 1 : 0);
+    if (stride == o.stride) {  // o's row i + d begins x + d * stride behind row i here: is that above -o.row and below row?
+      const int64_t x = (int64_t)(o.begin - begin), low = -o.row - x;
+      int64_t d = low >= 0 ? low / stride + 1 : -(-low / stride) + (-low % stride == 0 ? 1 : 0);  // the first above
       if (d < 1 - tokens) d = 1 - tokens;
       return d < tokens && d * stride < row - x;
     }

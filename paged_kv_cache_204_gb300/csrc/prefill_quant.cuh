@@ -376,7 +376,7 @@ __device__ __forceinline__ bool pq_begin(const PqParams& p, PqWalk& walk) {
 // q4_0 values d (q - 8) go up to 8 * 65504, eight times what binary16 holds: bfloat16 rows have them, and keys of
 // binary16 once they were turned. The kernel goes on as if there were none; the converting warps note a scale of 8192 or
 // more in magnitude, and the joining kernel does these pairs again in 32 bits. (That note and the joining kernel's look at
-// it take 2 of the drafted tokens' 175 us. With a vote and a flag for each 32 rows, and MMAs that run eight times over
+// it take 3 of the drafted tokens' 176 us. With a vote and a flag for each 32 rows, and MMAs that run eight times over
 // eighths of the values, it was 184; with such parts walked a second time in here, the 8 prompts took 131 to 142 us instead
 // of 124: longer code in all the roles.)
 
@@ -936,8 +936,9 @@ __global__ void __launch_bounds__(kPqThreads, 1) pa_prefill_quant_kernel(const _
           }
           float mt = sc * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           // the base moves only when the maximum exceeds it by more than kTopLog2, that is, has grown by more than
-          // kRescaleLog2 since: every P stays below 2^kTopLog2, and O and the row sum have the same base. (Logits from kPwFar on are whole numbers, and
-          // a base may be off by half their distance: there it is the maximum and moves whenever that does.)
+          // kRescaleLog2 since: every P stays below 2^kTopLog2, and O and the row sum have the same base. (Logits
+          // from kPwFar on are whole numbers, and a base may be off by half their distance: there it is the
+          // maximum and moves whenever that does.)
           const float most = fabsf(m_use) < kPwFar ? kTopLog2 : 0.f;
           // (the difference is not a number, and no growth, for -inf - -inf)
           float alpha = 1.f;
